@@ -1,4 +1,4 @@
-"""Python binding of libmuon_mi355x.so (the MI355X Muon / Dimuon step).
+"""Python binding of libmuon_mi355x.so (the MI355X Muon / Dimuon step, AdamW and the gradient norm).
 
 Argument marshalling only: tensors are turned into device pointers and
 shapes, and every step of the method runs in the library's HIP kernels.  The
@@ -7,7 +7,10 @@ is no fallback.
 
 Entry points mirror the C ABI in ``include/muon_mi355x.h``:
 ``muon_step``, ``dimuon_step``, ``muon_workspace_bytes``,
-``muon_status_string``.
+``muon_status_string``; ``adamw_step``, ``AdamWPlan`` (AdamW for the
+parameters Muon does not take, moments in 32 or 8 bits); ``grad_norm``,
+``GradNormPlan`` (global gradient norm and clip coefficient, which the steps
+take as ``grad_scale``).
 """
 
 from __future__ import annotations
@@ -27,15 +30,21 @@ _DT_NAME = {"f32": MUON_F32, "bf16": MUON_BF16}
 
 STATUS_NAMES = {0: "MUON_OK", 1: "MUON_ERR_INVALID_ARG", 2: "MUON_ERR_DTYPE",
                 3: "MUON_ERR_WORKSPACE", 4: "MUON_ERR_ALIAS", 5: "MUON_ERR_HIP",
-                6: "MUON_ERR_UNSUPPORTED"}
+                6: "MUON_ERR_UNSUPPORTED", 7: "MUON_ERR_MEMORY"}
 
 EXPORTED_SYMBOLS = ("muon_config_default", "muon_workspace_bytes", "muon_step", "dimuon_step", "muon_step_noalloc",
                     "muon_set_launch_events", "muon_plan_create", "muon_plan_step", "muon_plan_set_lr",
-                    "muon_plan_reset", "muon_plan_set_graph", "muon_plan_destroy", "muon_status_string", "muon_last_error", "muon_abi_version")
+                    "muon_plan_reset", "muon_plan_set_graph", "muon_plan_destroy", "muon_status_string", "muon_last_error", "muon_abi_version",
+                    "adamw_config_default", "adamw_workspace_bytes", "adamw_state_elems", "adamw_step",
+                    "adamw_plan_create", "adamw_plan_step", "adamw_plan_set_lr", "adamw_plan_set_step",
+                    "adamw_plan_get_state", "adamw_plan_set_state", "adamw_plan_destroy",
+                    "muon_grad_norm_workspace_bytes", "muon_grad_norm", "muon_grad_norm_plan_create",
+                    "muon_grad_norm_plan_run", "muon_grad_norm_plan_destroy")
 
 LAUNCH_KINDS = {-1: "start", 0: "thin_b", 1: "momentum", 2: "condition", 3: "prescale", 4: "norm",
                 5: "gram", 6: "poly", 7: "combine", 8: "postnorm", 9: "update", 10: "thin_energy",
-                11: "thin_a", 12: "momentum_prescale", 13: "energy"}
+                11: "thin_a", 12: "momentum_prescale", 13: "energy", 14: "adamw", 15: "state_get", 16: "state_set",
+                17: "grad_norm"}
 
 
 class MuonMatrix(ctypes.Structure):
@@ -52,7 +61,26 @@ class MuonConfig(ctypes.Structure):
                 ("w_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32),
                 ("mom_dtype", ctypes.c_int32), ("ns_dtype", ctypes.c_int32),
                 ("dimuon_eps", ctypes.c_float), ("nesterov", ctypes.c_int32),
-                ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32 * 4)]
+                ("weight_decay", ctypes.c_float), ("reserved0", ctypes.c_int32),
+                ("grad_scale", ctypes.c_void_p), ("reserved", ctypes.c_int32 * 1)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class AdamWCConfig(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("lr", ctypes.c_float),
+                ("eps", ctypes.c_float), ("seed", ctypes.c_uint64), ("grad_scale", ctypes.c_void_p),
+                ("w_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
+                ("rounding", ctypes.c_int32), ("reserved", ctypes.c_int32 * 4)]
+
+
+class MuonGrad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved0", ctypes.c_int32)]
 
 
 class MuonError(RuntimeError):
@@ -102,6 +130,29 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_plan_set_graph.restype = ctypes.c_int
     lib.muon_plan_destroy.argtypes = [ctypes.c_void_p]
     lib.muon_plan_destroy.restype = None
+    lib.adamw_config_default.argtypes = [ctypes.POINTER(AdamWCConfig)]
+    lib.adamw_config_default.restype = None
+    batch = [ctypes.POINTER(AdamWTensor), ctypes.c_int64]
+    cfg_p, ws, vp = ctypes.POINTER(AdamWCConfig), [ctypes.c_void_p, ctypes.c_size_t], ctypes.c_void_p
+    grads = [ctypes.POINTER(MuonGrad), ctypes.c_int64]
+    norm = [*grads, ctypes.c_float, vp, vp, *ws, vp]
+    for name, args in (("adamw_workspace_bytes", [*batch, cfg_p, ctypes.POINTER(ctypes.c_size_t)]),
+                       ("adamw_state_elems", [*batch, ctypes.POINTER(ctypes.c_int64)]),
+                       ("adamw_step", [*batch, cfg_p, ctypes.c_int64, *ws, vp]),
+                       ("adamw_plan_create", [*batch, cfg_p, ctypes.c_int64, *ws, vp, ctypes.POINTER(vp)]),
+                       ("adamw_plan_step", [vp, vp]),
+                       ("adamw_plan_set_lr", [vp, ctypes.c_float, vp]),
+                       ("adamw_plan_set_step", [vp, ctypes.c_int64, vp]),
+                       ("adamw_plan_get_state", [vp, vp, vp, ctypes.c_int32, vp]),
+                       ("adamw_plan_set_state", [vp, vp, vp, ctypes.c_int32, vp]),
+                       ("muon_grad_norm_workspace_bytes", [*grads, ctypes.POINTER(ctypes.c_size_t)]),
+                       ("muon_grad_norm", norm),
+                       ("muon_grad_norm_plan_create", [*norm, ctypes.POINTER(vp)]),
+                       ("muon_grad_norm_plan_run", [vp, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
+    for name in ("adamw_plan_destroy", "muon_grad_norm_plan_destroy"):
+        getattr(lib, name).argtypes, getattr(lib, name).restype = [vp], None
     lib.muon_status_string.argtypes = [ctypes.c_int]
     lib.muon_status_string.restype = ctypes.c_char_p
     lib.muon_last_error.argtypes = []
@@ -122,6 +173,15 @@ def _check(status: int):
         raise MuonError(status, lib.muon_last_error().decode() or lib.muon_status_string(status).decode())
 
 
+def _scalar_ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    """Pointer of a grad_scale: one float32 on the device (None: no scale)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1 or not t.is_cuda:
+        raise ValueError(f"grad_scale must be one float32 on the GPU, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
 @dataclass
 class StepConfig:
     """Mirror of muon_config_t with the library's defaults."""
@@ -139,6 +199,7 @@ class StepConfig:
     dimuon_eps: float = 1e-4
     nesterov: bool = False
     weight_decay: float = 0.0
+    grad_scale: Optional[torch.Tensor] = None   # one float32 on the device, e.g. grad_norm(...)[1:]
 
     def to_c(self):
         cfg = MuonConfig()
@@ -156,6 +217,7 @@ class StepConfig:
         cfg.dimuon_eps = self.dimuon_eps
         cfg.nesterov = 1 if self.nesterov else 0
         cfg.weight_decay = self.weight_decay
+        cfg.grad_scale = _scalar_ptr(self.grad_scale)
         return cfg, keep
 
 
@@ -381,7 +443,306 @@ class Plan:
             pass
 
 
+ADAMW_BLOCK = 256   # elements that share a scale of the 8-bit moments
+_STATE_CODE = {"f32": 0, "block8": 1}
+_ROUNDING_CODE = {"nearest": 0, "stochastic": 1}
+
+
+@dataclass
+class AdamWConfig:
+    """Mirror of adamw_config_t with the library's defaults."""
+    lr: float = 1e-3
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    w_dtype: str = "bf16"
+    g_dtype: str = "bf16"
+    state: str = "f32"                          # "f32" or "block8"
+    rounding: str = "stochastic"                # of 8-bit codes: "nearest" or "stochastic"
+    seed: int = 0
+    grad_scale: Optional[torch.Tensor] = None   # one float32 on the device, e.g. grad_norm(...)[1:]
+
+    def to_c(self) -> AdamWCConfig:
+        c = AdamWCConfig()
+        c.beta1, c.beta2, c.lr, c.eps = self.beta1, self.beta2, self.lr, self.eps
+        c.seed = self.seed & 0xFFFFFFFFFFFFFFFF
+        c.grad_scale = _scalar_ptr(self.grad_scale)
+        c.w_dtype, c.g_dtype = _DT_NAME[self.w_dtype], _DT_NAME[self.g_dtype]
+        c.state, c.rounding = _STATE_CODE[self.state], _ROUNDING_CODE[self.rounding]
+        return c
+
+
+@dataclass
+class AdamWParam:
+    """One tensor of an AdamW batch, of any shape: weight, gradient and
+    moments.  32-bit moments: float32 m and v of w's size.  8-bit moments: m
+    float8_e4m3fn and v uint8 of w's size, m_scale and v_scale one float32 per
+    ADAMW_BLOCK elements."""
+    w: torch.Tensor
+    g: torch.Tensor
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+    master: Optional[torch.Tensor] = None   # float32 master weights (bf16 w)
+    lr_scale: float = 1.0
+    weight_decay: float = 0.0
+
+
+def adamw_param(w: torch.Tensor, g: torch.Tensor, state: str = "f32", master: bool = False,
+                lr_scale: float = 1.0, weight_decay: float = 0.0) -> AdamWParam:
+    """AdamWParam with new (zero) moments and, with `master`, a float32 copy of w."""
+    kw = {"lr_scale": lr_scale, "weight_decay": weight_decay,
+          "master": w.detach().float() if master else None}
+    if state == "f32":
+        return AdamWParam(w, g, torch.zeros_like(w, dtype=torch.float32),
+                          torch.zeros_like(w, dtype=torch.float32), **kw)
+    if state != "block8":
+        raise ValueError(f"state must be one of {sorted(_STATE_CODE)}, got {state!r}")
+    codes = [torch.zeros(w.shape, dtype=torch.uint8, device=w.device) for _ in range(2)]
+    scales = [torch.zeros(-(-w.numel() // ADAMW_BLOCK), device=w.device) for _ in range(2)]
+    return AdamWParam(w, g, codes[0].view(torch.float8_e4m3fn), codes[1], *scales, **kw)
+
+
+def adamw_config_for(params: Sequence[AdamWParam], **kw) -> AdamWConfig:
+    """AdamWConfig whose dtypes and moment format are those of the first tensor."""
+    p = params[0]
+    name = {torch.float32: "f32", torch.bfloat16: "bf16"}
+    return AdamWConfig(w_dtype=name[p.w.dtype], g_dtype=name[p.g.dtype],
+                       state="f32" if p.m.dtype == torch.float32 else "block8", **kw)
+
+
+def _marshal_adamw(params: Sequence[AdamWParam], cfg: AdamWConfig):
+    block8 = cfg.state == "block8"
+    want = {"w": _DT_NAME[cfg.w_dtype], "g": _DT_NAME[cfg.g_dtype]}
+    state_dt = {"m": torch.float8_e4m3fn if block8 else torch.float32, "v": torch.uint8 if block8 else torch.float32}
+    arr = (AdamWTensor * len(params))()
+    for i, p in enumerate(params):
+        n = p.w.numel()
+        for name in ("w", "g", "m", "v", "m_scale", "v_scale", "master"):
+            t = getattr(p, name)
+            scale = name.endswith("_scale")
+            if t is None:
+                if name == "master" or (scale and not block8):
+                    continue
+                raise ValueError(f"tensor {i}: {name} is missing")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {i}: {name} must be contiguous")
+            if t.device != params[0].w.device:
+                raise ValueError(f"tensor {i}: {name} is on {t.device}, the batch on {params[0].w.device}")
+            if t.numel() != (-(-n // ADAMW_BLOCK) if scale else n):
+                raise ValueError(f"tensor {i}: {name} has {t.numel()} elements for {n} weights")
+            if name in want:
+                if _DT_CODE.get(t.dtype) != want[name]:
+                    raise ValueError(f"tensor {i}: {name} is {t.dtype}, config says {getattr(cfg, name + '_dtype')}")
+            elif t.dtype != state_dt.get(name, torch.float32):
+                raise ValueError(f"tensor {i}: {name} is {t.dtype}, expected {state_dt.get(name, torch.float32)}")
+            setattr(arr[i], name, t.data_ptr())
+        arr[i].n, arr[i].lr_scale, arr[i].weight_decay = n, float(p.lr_scale), float(p.weight_decay)
+    if cfg.grad_scale is not None and params and cfg.grad_scale.device != params[0].w.device:
+        raise ValueError(f"grad_scale is on {cfg.grad_scale.device}, the batch on {params[0].w.device}")
+    return arr
+
+
+def _workspace_tensor(nbytes: int, device) -> torch.Tensor:
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _stateless_workspace(workspace, nbytes, device, ts):
+    """The caller's workspace, or a new one that the allocator keeps until `ts` is done with it."""
+    if workspace is None:
+        workspace = _workspace_tensor(nbytes, device)
+        if ts != torch.cuda.current_stream(device):
+            # The block may have been freed on the current stream a moment ago.
+            ts.wait_stream(torch.cuda.current_stream(device))
+            workspace.record_stream(ts)
+    return workspace
+
+
+def adamw_workspace_bytes(params: Sequence[AdamWParam], cfg: AdamWConfig) -> int:
+    lib = load_library()
+    arr, out = _marshal_adamw(params, cfg), ctypes.c_size_t(0)
+    _check(lib.adamw_workspace_bytes(arr, len(params), ctypes.byref(cfg.to_c()), ctypes.byref(out)))
+    return int(out.value)
+
+
+def adamw_step(params: Sequence[AdamWParam], cfg: AdamWConfig, step: int,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """AdamW step number `step` (from 1 on) over the batch, asynchronous on
+    ``stream``.  Returns the workspace.  Refused under stream capture."""
+    lib = load_library()
+    arr, c = _marshal_adamw(params, cfg), cfg.to_c()
+    device = params[0].w.device if params else None
+    nbytes = ctypes.c_size_t(0)
+    _check(lib.adamw_workspace_bytes(arr, len(params), ctypes.byref(c), ctypes.byref(nbytes)))
+    ts = _torch_stream(stream, device)
+    workspace = _stateless_workspace(workspace, nbytes.value, device, ts)
+    with torch.cuda.device(device):
+        _check(lib.adamw_step(arr, len(params), ctypes.byref(c), step, workspace.data_ptr(), workspace.numel(),
+                              ts.cuda_stream))
+    return workspace
+
+
+class AdamWPlan:
+    """A prepared AdamW batch (adamw_plan_t): validated and uploaded once,
+    then stepped repeatedly.  Keeps the tensors and the workspace alive.
+    ``step()`` can be captured into a graph: every replay is the next step."""
+
+    def __init__(self, params: Sequence[AdamWParam], cfg: AdamWConfig, step: int = 0,
+                 workspace: Optional[torch.Tensor] = None, stream=None):
+        """`step`: the number of steps the moments have taken (0 for new ones)."""
+        self._handle = ctypes.c_void_p(0)
+        self._lib = lib = load_library()
+        arr, c = _marshal_adamw(params, cfg), cfg.to_c()
+        nbytes, elems = ctypes.c_size_t(0), ctypes.c_int64(0)
+        _check(lib.adamw_workspace_bytes(arr, len(params), ctypes.byref(c), ctypes.byref(nbytes)))
+        _check(lib.adamw_state_elems(arr, len(params), ctypes.byref(elems)))
+        self.params, self.cfg = list(params), cfg
+        self.device = params[0].w.device
+        self.state_elems = elems.value
+        ts = _torch_stream(stream, self.device)
+        self.workspace = _stateless_workspace(workspace, nbytes.value, self.device, ts)
+        with torch.cuda.device(self.device):
+            _check(lib.adamw_plan_create(arr, len(params), ctypes.byref(c), step, self.workspace.data_ptr(),
+                                         self.workspace.numel(), ts.cuda_stream, ctypes.byref(self._handle)))
+
+    def step(self, stream=None):
+        _check(self._lib.adamw_plan_step(self._handle, _stream_handle(stream, self.device)))
+
+    def set_lr(self, lr: float, stream=None):
+        _check(self._lib.adamw_plan_set_lr(self._handle, lr, _stream_handle(stream, self.device)))
+
+    def set_step(self, step: int, stream=None):
+        """Number of steps done, for resuming."""
+        _check(self._lib.adamw_plan_set_step(self._handle, step, _stream_handle(stream, self.device)))
+
+    def state_offsets(self) -> List[int]:
+        """Where every tensor's values start in the buffers of get_state and set_state."""
+        out, at = [], 0
+        for p in self.params:
+            out.append(at)
+            at += -(-p.w.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
+        return out
+
+    def _values(self, m, v):
+        for name, t in (("m", m), ("v", v)):
+            if t.dtype not in _DT_CODE or t.dtype != m.dtype:
+                raise ValueError(f"{name} must be float32 or bfloat16, both of one dtype, got {t.dtype}")
+            if t.numel() != self.state_elems or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{name} must be {self.state_elems} contiguous elements on {self.device}")
+        return m.data_ptr(), v.data_ptr(), _DT_CODE[m.dtype]
+
+    def get_state(self, m: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                  dtype: torch.dtype = torch.float32, stream=None):
+        """The moments as values, (m, v): flat buffers of state_elems elements
+        (new ones of `dtype`, zero in the gaps, if none are given)."""
+        if m is None and v is None:
+            with torch.cuda.stream(_torch_stream(stream, self.device)):
+                m, v = (torch.zeros(self.state_elems, dtype=dtype, device=self.device) for _ in range(2))
+        _check(self._lib.adamw_plan_get_state(self._handle, *self._values(m, v),
+                                              _stream_handle(stream, self.device)))
+        return m, v
+
+    def set_state(self, m: torch.Tensor, v: torch.Tensor, stream=None):
+        """Loads the moments from values laid out as get_state's."""
+        _check(self._lib.adamw_plan_set_state(self._handle, *self._values(m, v),
+                                              _stream_handle(stream, self.device)))
+
+    def close(self):
+        if self._handle:
+            self._lib.adamw_plan_destroy(self._handle)
+            self._handle = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _marshal_grads(grads: Sequence[torch.Tensor], out, tensor_norms):
+    arr = (MuonGrad * len(grads))()
+    for i, g in enumerate(grads):
+        if g.dtype not in _DT_CODE:
+            raise ValueError(f"tensor {i}: gradients are float32 or bfloat16, got {g.dtype}")
+        if not g.is_contiguous():
+            raise ValueError(f"tensor {i}: the gradient must be contiguous")
+        if g.device != grads[0].device:
+            raise ValueError(f"tensor {i} is on {g.device}, the batch on {grads[0].device}")
+        arr[i].g, arr[i].n, arr[i].dtype = g.data_ptr(), g.numel(), _DT_CODE[g.dtype]
+    for name, t, n in (("out", out, 2), ("tensor_norms", tensor_norms, len(grads))):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()
+                              or t.device != grads[0].device):
+            raise ValueError(f"{name} must be {n} contiguous float32 on {grads[0].device}")
+    return arr
+
+
+def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = float("inf"), out: Optional[torch.Tensor] = None,
+              tensor_norms: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """Global gradient norm and clip coefficient: two float32 on the device,
+    (N, 1 if N <= max_norm else max_norm / N).  Pass ``[1:]`` of it as
+    grad_scale to the steps.  Refused under stream capture."""
+    if not grads:
+        raise ValueError("no gradients")
+    device = grads[0].device
+    ts = _torch_stream(stream, device)
+    if out is None:
+        with torch.cuda.stream(ts):
+            out = torch.empty(2, device=device)
+    lib = load_library()
+    arr, nbytes = _marshal_grads(grads, out, tensor_norms), ctypes.c_size_t(0)
+    _check(lib.muon_grad_norm_workspace_bytes(arr, len(grads), ctypes.byref(nbytes)))
+    workspace = _stateless_workspace(workspace, nbytes.value, device, ts)
+    with torch.cuda.device(device):
+        _check(lib.muon_grad_norm(arr, len(grads), max_norm, out.data_ptr(), _ptr(tensor_norms),
+                                  workspace.data_ptr(), workspace.numel(), ts.cuda_stream))
+    return out
+
+
+class GradNormPlan:
+    """A prepared global gradient norm (muon_grad_norm_plan_t): ``run()``
+    launches one kernel and returns ``out``.  Keeps the tensors alive; can be
+    captured into a graph."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], max_norm: float = float("inf"),
+                 out: Optional[torch.Tensor] = None, tensor_norms: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None):
+        if not grads:
+            raise ValueError("no gradients")
+        self._handle = ctypes.c_void_p(0)
+        self._lib = lib = load_library()
+        self.device = grads[0].device
+        self.grads, self.tensor_norms = list(grads), tensor_norms
+        self.out = out if out is not None else torch.zeros(2, device=self.device)
+        arr, nbytes = _marshal_grads(grads, self.out, tensor_norms), ctypes.c_size_t(0)
+        _check(lib.muon_grad_norm_workspace_bytes(arr, len(grads), ctypes.byref(nbytes)))
+        ts = _torch_stream(stream, self.device)
+        self.workspace = _stateless_workspace(workspace, nbytes.value, self.device, ts)
+        with torch.cuda.device(self.device):
+            _check(lib.muon_grad_norm_plan_create(arr, len(grads), max_norm, self.out.data_ptr(),
+                                                  _ptr(tensor_norms), self.workspace.data_ptr(),
+                                                  self.workspace.numel(), ts.cuda_stream,
+                                                  ctypes.byref(self._handle)))
+
+    def run(self, stream=None) -> torch.Tensor:
+        _check(self._lib.muon_grad_norm_plan_run(self._handle, _stream_handle(stream, self.device)))
+        return self.out
+
+    def close(self):
+        if self._handle:
+            self._lib.muon_grad_norm_plan_destroy(self._handle)
+            self._handle = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
 __all__ = ["MuonMatrix", "MuonConfig", "MuonError", "StepConfig", "Param", "load_library",
            "muon_step", "dimuon_step", "muon_step_noalloc", "muon_workspace_bytes", "muon_status_string",
            "Plan", "workspace_for", "config_for", "EXPORTED_SYMBOLS", "LaunchTimer",
-           "LAUNCH_KINDS"]
+           "LAUNCH_KINDS", "AdamWConfig", "AdamWParam", "AdamWPlan", "adamw_param", "adamw_config_for",
+           "adamw_step", "adamw_workspace_bytes", "ADAMW_BLOCK", "grad_norm", "GradNormPlan"]

@@ -13,7 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon_mi355x.so")
-SOURCES = ["api.hip", "stream_kernels.hip", "gemm_kernels.hip", "thin_kernel.hip"]
+SOURCES = ["api.hip", "stream_kernels.hip", "gemm_kernels.hip", "thin_kernel.hip",
+           "adamw_api.hip", "adamw_kernels.hip", "norm_kernel.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,135 @@
+// AdamW and the global gradient norm: structures shared by the host planner
+// and the kernels, and the launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+#include "muon_mi355x.h"
+
+namespace muon {
+
+// A tensor is worked on in pieces of kAdamPiece elements (a multiple of
+// ADAMW_BLOCK, so that a block of the 8-bit moments never spans two pieces).
+constexpr int kAdamThreads = 256;
+constexpr int kAdamPiece = 4096;
+
+// Per-tensor descriptor (uploaded once per batch into the workspace).
+struct alignas(16) AdamDesc {
+  void* w;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float* master;
+  int64_t n;
+  int64_t first;          // index of the tensor's first element in the batch (a multiple of ADAMW_BLOCK)
+  float lr_scale;
+  float weight_decay;
+};
+
+// One piece of a tensor.
+struct alignas(8) AdamPiece {
+  uint32_t tensor, piece;
+};
+
+// State of a plan's step sequence, in the workspace.  b1t, b2t and the values
+// derived from them are those of the step to come; the last workgroup of a
+// step advances them, so a captured step replays as the next one.
+struct alignas(16) AdamCtl {
+  double b1t, b2t;        // beta1^t, beta2^t
+  int64_t t;              // number of the step to come, from 1 on
+  float lr;
+  float rb1;              // 1 / (1 - beta1^t)
+  float rb2;              // 1 / sqrt(1 - beta2^t)
+  uint32_t key;           // key of the rounding hash for step t
+  uint32_t ticket;        // workgroups of the running step that have read the values above
+};
+
+struct AdamArgs {
+  const AdamDesc* desc;
+  const AdamPiece* pieces;
+  int64_t npieces;
+  AdamCtl* ctl;
+  const float* grad_scale;  // or NULL
+  double beta1, beta2;
+  uint64_t seed;
+  float eps;
+  int32_t w_dt, g_dt;
+  int32_t block8;         // 8-bit moments
+  int32_t stochastic;
+  int32_t has_master;
+};
+
+// The counter hash of the stochastic rounding: two rounds of xor-shift and
+// multiply by odd constants (the fraction bits of sqrt 2 and sqrt 3), after
+// which every output bit flips with probability 1/2 +- 0.004 for any flipped
+// input bit.
+__host__ __device__ inline uint32_t adam_mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+__host__ __device__ inline uint32_t adam_key(uint64_t seed, int64_t t) {
+  const uint64_t u = static_cast<uint64_t>(t);
+  uint32_t k = adam_mix(static_cast<uint32_t>(u >> 32) ^ 0x3C6EF372u);
+  k = adam_mix(static_cast<uint32_t>(u) ^ k);
+  k = adam_mix(static_cast<uint32_t>(seed >> 32) ^ k);
+  return adam_mix(static_cast<uint32_t>(seed) ^ k);
+}
+
+// Values of the step t = ctl.t, from b1t and b2t.
+__host__ __device__ inline void adam_derive(AdamCtl& c, uint64_t seed) {
+  c.rb1 = static_cast<float>(1.0 / (1.0 - c.b1t));
+  c.rb2 = static_cast<float>(1.0 / sqrt(1.0 - c.b2t));
+  c.key = adam_key(seed, c.t);
+}
+
+hipError_t launch_adamw(const AdamArgs& a, bool advance, hipStream_t s);
+// Writes the step values (`set_step`) or only the learning rate.
+hipError_t launch_adamw_ctl(AdamCtl* ctl, const AdamCtl& value, bool set_step, hipStream_t s);
+hipError_t launch_adamw_get(const AdamArgs& a, void* m, void* v, int32_t dt, hipStream_t s);
+hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int32_t dt, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Global gradient norm
+// ---------------------------------------------------------------------------
+constexpr int kNormThreads = 256;
+constexpr int kNormGrid = 2048;        // most workgroups of one launch
+constexpr int kNormUnitBytes = 8192;   // smallest share of work
+
+struct alignas(16) NormTensor {
+  const void* g;
+  int64_t n;
+  int32_t dt;
+  uint32_t run0;          // this tensor's runs are run0 .. (next tensor's run0) - 1
+};
+
+// A stretch of one tensor that one workgroup sums; its sum goes to
+// partial[index of the run].
+struct alignas(16) NormRun {
+  int64_t begin, count;   // elements
+  uint32_t tensor;
+  uint32_t pad[3];
+};
+
+struct NormArgs {
+  const NormTensor* tensors;   // ntensors + 1 entries (the last closes run0)
+  const NormRun* runs;
+  const uint32_t* first_run;   // per workgroup, nwg + 1 entries
+  double* partial;             // one per run
+  uint32_t* ticket;
+  float* out;
+  float* tensor_norms;         // or NULL
+  float max_norm;
+  uint32_t ntensors, nruns, nwg;
+};
+
+hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s);
+
+}  // namespace muon

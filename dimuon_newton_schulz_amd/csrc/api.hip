@@ -3,65 +3,25 @@
 // sequence of one Muon / Dimuon step.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <map>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "common.h"
+#include "host.h"
 #include "muon_mi355x.h"
 
 namespace muon {
 namespace {
 
-thread_local std::string g_last_error;
-
-// Launch-event hook (timing only).
-struct EventHook {
-  void* const* events = nullptr;
-  int32_t* kinds = nullptr;
-  int32_t n = 0;
-  int32_t next = 0;
-  int32_t last_count = 0;
-};
-thread_local EventHook g_hook;
-
-hipError_t hook_record(int32_t kind, hipStream_t s) {
-  if (!g_hook.events || g_hook.next >= g_hook.n) return hipSuccess;
-  hipError_t e = hipEventRecord(static_cast<hipEvent_t>(g_hook.events[g_hook.next]), s);
-  if (g_hook.kinds) g_hook.kinds[g_hook.next] = kind;
-  ++g_hook.next;
-  return e;
-}
-
-muon_status_t fail(muon_status_t st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return st;
-}
-
 constexpr int64_t kMaxDim = 65536;
 constexpr int kThinMaxK = 32;
-constexpr size_t kAlign = 256;
-
-inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-inline int64_t ceil_div(int64_t x, int64_t a) { return (x + a - 1) / a; }
 inline int next_pow2(int64_t x) {
   int p = 1;
   while (p < x) p <<= 1;
   return p;
 }
-inline size_t dtype_size(int32_t dt) { return dt == DT_F32 ? 4 : 2; }
-
-bool finite(float x) { return std::isfinite(x); }
-
 // ---------------------------------------------------------------------------
 // Plan
 // ---------------------------------------------------------------------------
@@ -108,6 +68,8 @@ muon_status_t validate_config(const muon_config_t* cfg) {
     return fail(MUON_ERR_INVALID_ARG, "lr, momentum and weight_decay must be finite");
   if (!finite(cfg->dimuon_eps) || cfg->dimuon_eps < 0.0f)
     return fail(MUON_ERR_INVALID_ARG, "dimuon_eps must be finite and >= 0");
+  if (reinterpret_cast<uintptr_t>(cfg->grad_scale) % 4 != 0)
+    return fail(MUON_ERR_INVALID_ARG, "grad_scale is not 4-byte aligned");
   if (cfg->coeff_schedule) {
     for (int i = 0; i < 3 * cfg->ns_steps; ++i)
       if (!finite(cfg->coeff_schedule[i])) return fail(MUON_ERR_INVALID_ARG, "coeff_schedule[%d] is not finite", i);
@@ -133,11 +95,9 @@ muon_status_t validate_shapes(const muon_matrix_t* mats, int64_t count) {
   return MUON_OK;
 }
 
-struct Range { uintptr_t lo, hi; int64_t mat; const char* what; bool writable; };
-
 muon_status_t validate_buffers(const muon_matrix_t* mats, int64_t count, const muon_config_t* cfg) {
   std::vector<Range> rs;
-  rs.reserve(count * 5);
+  rs.reserve(count * 5 + 1);
   for (int64_t i = 0; i < count; ++i) {
     const muon_matrix_t& x = mats[i];
     const size_t elems = static_cast<size_t>(x.m) * static_cast<size_t>(x.n);
@@ -158,23 +118,11 @@ muon_status_t validate_buffers(const muon_matrix_t* mats, int64_t count, const m
       rs.push_back({lo, lo + b.bytes, i, b.what, b.wr});
     }
   }
-  std::sort(rs.begin(), rs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  // Any overlap that involves a written buffer is an error.  Scanning in
-  // address order, keep the written range reaching furthest and the range
-  // (of any kind) reaching furthest.
-  const Range* far_any = nullptr;
-  const Range* far_wr = nullptr;
-  for (const Range& r : rs) {
-    const Range* hit = nullptr;
-    if (r.writable && far_any && far_any->hi > r.lo) hit = far_any;
-    else if (far_wr && far_wr->hi > r.lo) hit = far_wr;
-    if (hit)
-      return fail(MUON_ERR_ALIAS, "matrix %lld %s overlaps matrix %lld %s", (long long)r.mat, r.what,
-                  (long long)hit->mat, hit->what);
-    if (!far_any || r.hi > far_any->hi) far_any = &r;
-    if (r.writable && (!far_wr || r.hi > far_wr->hi)) far_wr = &r;
+  if (cfg->grad_scale) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(cfg->grad_scale);
+    rs.push_back({lo, lo + 4, 0, "grad_scale", false});
   }
-  return MUON_OK;
+  return check_overlaps(rs, "matrix");
 }
 
 template <typename T>
@@ -511,95 +459,6 @@ muon_status_t build_plan(const muon_matrix_t* mats, int64_t count, const muon_co
 }
 
 // ---------------------------------------------------------------------------
-// Descriptor upload: the table is copied from a pinned host buffer into the
-// workspace prefix on the step's stream.  An event records when the copy has
-// consumed the host buffer, so the buffer is never overwritten early.
-// ---------------------------------------------------------------------------
-struct Staging {
-  void* host = nullptr;
-  size_t cap = 0;
-  hipEvent_t ev = nullptr;
-  bool pending = false;
-
-  // True when the buffer may be written: no copy from it is in flight.
-  bool idle() {
-    if (!pending) return true;
-    if (hipEventQuery(ev) == hipSuccess) pending = false;
-    return !pending;
-  }
-
-  muon_status_t upload(const std::vector<unsigned char>& table, void* dst, hipStream_t s) {
-    hipError_t err;
-    if (pending) {
-      if ((err = hipEventSynchronize(ev)) != hipSuccess)
-        return fail(MUON_ERR_HIP, "hipEventSynchronize: %s", hipGetErrorString(err));
-      pending = false;
-    }
-    if (cap < table.size()) {
-      if (host) (void)hipHostFree(host);
-      host = nullptr;
-      cap = 0;
-      if ((err = hipHostMalloc(&host, table.size(), hipHostMallocDefault)) != hipSuccess) {
-        host = nullptr;
-        return fail(MUON_ERR_HIP, "hipHostMalloc(%zu): %s", table.size(), hipGetErrorString(err));
-      }
-      cap = table.size();
-    }
-    if (!ev && (err = hipEventCreateWithFlags(&ev, hipEventDisableTiming)) != hipSuccess) {
-      ev = nullptr;
-      return fail(MUON_ERR_HIP, "hipEventCreate: %s", hipGetErrorString(err));
-    }
-    std::memcpy(host, table.data(), table.size());
-    if ((err = hipMemcpyAsync(dst, host, table.size(), hipMemcpyHostToDevice, s)) != hipSuccess)
-      return fail(MUON_ERR_HIP, "hipMemcpyAsync: %s", hipGetErrorString(err));
-    if ((err = hipEventRecord(ev, s)) != hipSuccess)
-      return fail(MUON_ERR_HIP, "hipEventRecord: %s", hipGetErrorString(err));
-    pending = true;
-    return MUON_OK;
-  }
-
-  void release() {
-    if (pending && ev) (void)hipEventSynchronize(ev);
-    if (ev) (void)hipEventDestroy(ev);
-    if (host) (void)hipHostFree(host);
-    host = nullptr;
-    ev = nullptr;
-    cap = 0;
-    pending = false;
-  }
-};
-
-// Staging buffers of the stateless calls, per host thread.  A call takes an
-// idle buffer (its previous copy has completed), or a new one while the
-// thread holds fewer than kPoolMax; only a thread with kPoolMax copies in
-// flight waits, for its oldest.  The buffers are freed when the thread exits.
-constexpr size_t kPoolMax = 64;
-struct StagingPool {
-  std::vector<Staging*> slots;
-  size_t oldest = 0;   // slot waited on when every slot is busy
-
-  Staging* take() {
-    for (Staging* st : slots)
-      if (st->idle()) return st;
-    if (slots.size() < kPoolMax) {
-      slots.push_back(new Staging());
-      return slots.back();
-    }
-    Staging* st = slots[oldest];
-    oldest = (oldest + 1) % slots.size();
-    return st;   // upload() waits for its copy
-  }
-
-  ~StagingPool() {
-    for (Staging* st : slots) {
-      st->release();
-      delete st;
-    }
-  }
-};
-thread_local StagingPool g_pool;
-
-// ---------------------------------------------------------------------------
 // Shared pieces of a step
 // ---------------------------------------------------------------------------
 muon_status_t prepare(const muon_matrix_t* mats, int64_t count, const muon_config_t* cfg, void* ws,
@@ -615,6 +474,8 @@ muon_status_t prepare(const muon_matrix_t* mats, int64_t count, const muon_confi
     return fail(MUON_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, p.total_bytes);
   // The workspace must not overlap any caller buffer.
   const uintptr_t lo = reinterpret_cast<uintptr_t>(ws), hi = lo + p.total_bytes;
+  const uintptr_t gs = reinterpret_cast<uintptr_t>(cfg->grad_scale);
+  if (gs && gs < hi && lo < gs + 4) return fail(MUON_ERR_ALIAS, "grad_scale lies in the workspace");
   for (int64_t i = 0; i < count; ++i) {
     const muon_matrix_t& x = mats[i];
     const size_t elems = static_cast<size_t>(x.m) * x.n;
@@ -646,6 +507,7 @@ StepArgs make_args(const Plan& p, const muon_config_t& cfg, void* ws, bool dimuo
   a.w_dt = cfg.w_dtype;
   a.ns_dt = cfg.ns_dtype;
   a.nesterov = cfg.nesterov ? 1 : 0;
+  a.grad_scale = cfg.grad_scale;
   a.dimuon = dimuon ? 1 : 0;
   return a;
 }
@@ -658,19 +520,6 @@ void make_coeffs(const muon_config_t& cfg, Coeffs* cf) {
       cf[t] = {cfg.a, cfg.b, cfg.c};
   }
 }
-
-#define MUON_HIP_TRY(expr)                                                                 \
-  do {                                                                                     \
-    hipError_t e_ = (expr);                                                                \
-    if (e_ != hipSuccess) return fail(MUON_ERR_HIP, "%s: %s", #expr, hipGetErrorString(e_)); \
-  } while (0)
-
-// Launch, then record the hook's event for this launch kind.
-#define MUON_LAUNCH(kind, expr)              \
-  do {                                       \
-    MUON_HIP_TRY(expr);                      \
-    MUON_HIP_TRY(hook_record((kind), s));    \
-  } while (0)
 
 // The launch sequence of one step; the descriptor table is already on the
 // device (ordered before these launches on stream s).
@@ -1038,6 +887,7 @@ const char* muon_status_string(muon_status_t status) {
     case MUON_ERR_ALIAS: return "buffers overlap";
     case MUON_ERR_HIP: return "HIP runtime error";
     case MUON_ERR_UNSUPPORTED: return "unsupported shape or count";
+    case MUON_ERR_MEMORY: return "host memory exhausted";
   }
   return "unknown status";
 }

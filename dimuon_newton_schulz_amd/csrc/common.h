@@ -92,6 +92,7 @@ struct StepArgs {
   int32_t g_dt, mom_dt, w_dt, ns_dt;
   int32_t nesterov;
   int32_t dimuon;
+  const float* grad_scale;   // caller, device: factor of the gradients, or NULL
 };
 
 // --------------------------------------------------------------------------

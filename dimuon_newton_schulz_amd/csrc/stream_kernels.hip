@@ -276,6 +276,11 @@ __global__ __launch_bounds__(256) void k_prescale(StepArgs a, const Tile* __rest
       load8(d.mom, a.mom_dt, off, sj0 + c0 + 8, n, v + 8);
       load8(d.g, a.g_dt, off, sj0 + c0, n, gv);
       load8(d.g, a.g_dt, off, sj0 + c0 + 8, n, gv + 8);
+      if (a.grad_scale) {
+        const float gs = *a.grad_scale;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) gv[e] *= gs;
+      }
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = momentum_value(a.mu, v[e], gv[e], a.mom_dt);
       store8(d.mom, a.mom_dt, off, sj0 + c0, n, v);

@@ -603,6 +603,13 @@ __device__ __forceinline__ void pass_a_core(const StepArgs& args, const MatDesc&
   }
 
   // ---- momentum ----------------------------------------------------------------
+  if (args.grad_scale) {
+    const float gs = *args.grad_scale;
+#pragma unroll
+    for (int a = 0; a < KP; ++a)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[a][e] *= gs;
+  }
 #pragma unroll
   for (int a = 0; a < KP; ++a)
 #pragma unroll
@@ -805,7 +812,7 @@ template <int KP, bool TALL>
 __device__ __forceinline__ void pass_b_tail(const StepArgs& args, const MatDesc& d, int s, int parity,
                                             ThinSmem<KP>& sm, bool full, double inv_nu, float dg,
                                             float (&y)[KP][TS<KP>::VEC], float (&w)[KP][TS<KP>::VEC],
-                                            const float (&g)[KP][TS<KP>::VEC], const float (&dloc)[TS<KP>::VEC]) {
+                                            float (&g)[KP][TS<KP>::VEC], const float (&dloc)[TS<KP>::VEC]) {
   constexpr int VEC = TS<KP>::VEC, L = TS<KP>::L;
   const int tid = threadIdx.x;
   const int k = d.k, N = d.N, n = d.n;
@@ -837,6 +844,13 @@ __device__ __forceinline__ void pass_b_tail(const StepArgs& args, const MatDesc&
 
   // ---- V, O = (post D_g Q D_g / nu) V D_l^2, update --------------------------
   if (args.nesterov) {
+    if (args.grad_scale) {
+      const float gs = *args.grad_scale;
+#pragma unroll
+      for (int a = 0; a < KP; ++a)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) g[a][e] *= gs;
+    }
 #pragma unroll
     for (int a = 0; a < KP; ++a)
 #pragma unroll

@@ -1,7 +1,9 @@
 /*
- * muon_mi355x.h: C ABI of the MI355X (gfx950) Muon / Dimuon optimizer step.
+ * muon_mi355x.h: C ABI of the MI355X (gfx950) Muon / Dimuon optimizer step,
+ * of AdamW for the parameters Muon does not take, and of the global gradient
+ * norm that clips both.
  *
- * One call updates a batch of independent 2-D weight matrices of mixed
+ * One Muon call updates a batch of independent 2-D weight matrices of mixed
  * shapes:
  *
  *   momentum      M_t = mu * M_{t-1} + G
@@ -93,7 +95,9 @@ typedef enum muon_status {
   MUON_ERR_WORKSPACE = 3,    /* workspace null, misaligned or too small */
   MUON_ERR_ALIAS = 4,        /* two buffers of the batch overlap where they must not */
   MUON_ERR_HIP = 5,          /* a HIP runtime call or kernel launch failed */
-  MUON_ERR_UNSUPPORTED = 6   /* shape outside the supported range */
+  MUON_ERR_UNSUPPORTED = 6,  /* shape outside the supported range, or a call that
+                                cannot run under stream capture */
+  MUON_ERR_MEMORY = 7        /* host memory exhausted */
 } muon_status_t;
 
 /* One matrix of the batch.  Sizes are in elements. */
@@ -125,7 +129,13 @@ typedef struct muon_config {
   float dimuon_eps;             /* floor added to the relative energy (1e-4) */
   int32_t nesterov;             /* nonzero: orthogonalise G + mu*M_t instead of M_t */
   float weight_decay;           /* W_t = W_{t-1} - lr*(scale*O_t + weight_decay*W_{t-1}) */
-  int32_t reserved[4];
+  int32_t reserved0;
+  const float* grad_scale;      /* device or NULL: one float32 s, read by the step; the step then
+                                   uses s*G (rounded to float32) wherever G stands.  The clip
+                                   coefficient of muon_grad_norm (out + 1) goes here.  Must stay
+                                   allocated while a plan uses it, and lie outside every buffer
+                                   the step writes. */
+  int32_t reserved[1];
 } muon_config_t;
 
 /* Fill `cfg` with the defaults: lr 0.02, mu 0.95, NS5 (3.4445, -4.7750,
@@ -198,7 +208,11 @@ typedef enum muon_launch_kind {
   MUON_LAUNCH_THIN_A = 11,    /* thin path pass A: momentum, Gram partials */
   MUON_LAUNCH_MOMENTUM_PRESCALE = 12, /* momentum, Dimuon energies of M_t, conditioned and
                                          normalised bf16/f32 copy (+ transpose), one pass */
-  MUON_LAUNCH_ENERGY = 13     /* energies of M_{t-1} (general path, no cached energies) */
+  MUON_LAUNCH_ENERGY = 13,    /* energies of M_{t-1} (general path, no cached energies) */
+  MUON_LAUNCH_ADAMW = 14,     /* AdamW step */
+  MUON_LAUNCH_STATE_GET = 15, /* AdamW moments to values */
+  MUON_LAUNCH_STATE_SET = 16, /* values to AdamW moments */
+  MUON_LAUNCH_GRAD_NORM = 17  /* global gradient norm */
 } muon_launch_kind_t;
 
 /* Timing hook, per host thread; not part of the method.  When `events` is
@@ -243,6 +257,190 @@ muon_status_t muon_plan_set_lr(muon_plan_t* plan, float lr);
 muon_status_t muon_plan_set_graph(muon_plan_t* plan, int32_t enable);
 /* Waits for the plan's upload to finish, then frees the plan (NULL is a no-op). */
 void muon_plan_destroy(muon_plan_t* plan);
+
+/* ------------------------------------------------------------------------
+ * AdamW, for the parameters Muon does not take (embeddings, heads, norm
+ * weights, biases): one call updates many tensors of any sizes.
+ *
+ *   y   = s * g                               (s: grad_scale, 1 if NULL)
+ *   m_t = beta1 * m_{t-1} + (1 - beta1) * y
+ *   v_t = beta2 * v_{t-1} + (1 - beta2) * y^2
+ *   w_t = w_{t-1} - lr * ( lr_scale * m^ / (sqrt(v^) + eps) + weight_decay * w_{t-1} )
+ *   with m^ = m_t / (1 - beta1^t),  v^ = v_t / (1 - beta2^t)
+ *
+ * (decoupled weight decay, as in muon_step; the sitech.ge Muon blog and "From
+ * PCG to Muon" leave the parameters that are not hidden matrices to AdamW).
+ * All arithmetic is in binary32; the weight is rounded to its dtype once, at
+ * the end, to nearest even.  With `master`, w_{t-1} is read from the float32
+ * master copy, which takes w_t unrounded, and w is only written.
+ *
+ * Moments in 32 bits (ADAMW_STATE_F32): m and v are float32, n elements each.
+ *
+ * Moments in 8 bits (ADAMW_STATE_BLOCK8): a tensor's elements are cut, in
+ * memory order, into blocks of ADAMW_BLOCK (the last one may be shorter).
+ * A block holds one float32 per moment and one byte per element and moment:
+ *   m  = e4m3(code) * m_scale     m_scale = max|m| / 256 over the block.
+ *        The code is OCP float8 e4m3 (torch.float8_e4m3fn); the block's
+ *        largest |m| has the code of 256.
+ *   v  = u(code) * v_scale        v_scale = max v over the block.
+ *        u is an unsigned float with 5 exponent and 3 mantissa bits: u(0) = 0,
+ *        u(255) = NaN, and u(c) is the binary32 with the bits
+ *        (c + 768) << 20 otherwise, so u(248) = 1.  A v above zero never takes
+ *        code 0: it is stored as at least u(1) = 1.125 * 2^-31, so that no
+ *        element's denominator falls to eps.
+ * A non-finite m or v, and a negative v, has the code of NaN, and the block's
+ * scale is that of its other elements.  m^ and v^ of a step come from the
+ * new moments before they are rounded to codes.  Rounding to a code:
+ *   ADAMW_ROUND_NEAREST     half a code step is added, then the value is cut.
+ *        Once an element's v changes by less than half a code step (1/32 to
+ *        1/16 of it) per step, its code stays where it is relative to the
+ *        block's largest v.
+ *   ADAMW_ROUND_STOCHASTIC  (r + 1/2) / 65536 of a code step is added, r in
+ *        0..65535 from a counter hash: the expected value is the unrounded
+ *        one (to 2^-17 of a code step).  r depends only on the seed, the step
+ *        number t and the element's place in the batch, so a step repeats bit
+ *        for bit.  With i the element's index in the batch (every tensor's
+ *        first element at a multiple of ADAMW_BLOCK, in the batch's order),
+ *        lo and hi meaning the lower and upper 32 bits, and all sums and
+ *        products modulo 2^32:
+ *          mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15;
+ *                  x *= 0xBB67AE85; x ^= x >> 16
+ *          key  = mix(lo(seed) ^ mix(hi(seed) ^ mix(lo(t) ^ mix(hi(t) ^ 0x3C6EF372))))
+ *          h    = mix(lo(i) + mix(key + hi(i)))
+ *        m takes the lower 16 bits of h as r, v the upper 16.
+ *
+ * Numerical edge cases are not errors: NaN and Inf propagate, and eps = 0
+ * with v = 0 divides by zero, as IEEE arithmetic does.
+ *
+ * Buffers: contiguous, 16-byte aligned (the scales 4-byte), none written by
+ * the call overlapping another (gradients may share memory).  A tensor with
+ * n = 0 is skipped and its pointers are not looked at.  Device memory,
+ * workspaces, streams and errors are as in the Muon calls; plan calls make
+ * the plan's device current while they run and restore the caller's.
+ * ------------------------------------------------------------------------ */
+#define ADAMW_BLOCK 256
+
+typedef enum adamw_state {
+  ADAMW_STATE_F32 = 0,
+  ADAMW_STATE_BLOCK8 = 1
+} adamw_state_t;
+
+typedef enum adamw_rounding {
+  ADAMW_ROUND_NEAREST = 0,
+  ADAMW_ROUND_STOCHASTIC = 1
+} adamw_rounding_t;
+
+/* One tensor of the batch.  Sizes are in elements. */
+typedef struct adamw_tensor {
+  void* w;              /* device, n of cfg.w_dtype: w_{t-1} in (without master), w_t out */
+  const void* g;        /* device, n of cfg.g_dtype: gradient, read only */
+  void* m;              /* device, n float32 or n bytes: first moment, in and out */
+  void* v;              /* device, n float32 or n bytes: second moment, in and out */
+  float* m_scale;       /* device, ceil(n / ADAMW_BLOCK) float32 (BLOCK8 only) */
+  float* v_scale;       /* device, ceil(n / ADAMW_BLOCK) float32 (BLOCK8 only) */
+  float* master;        /* device or NULL: n float32 master weights (w_dtype BF16 only;
+                           all tensors of a batch or none) */
+  int64_t n;            /* elements, 0 <= n <= 2^40 */
+  float lr_scale;       /* multiplies the Adam term of the update; 1 for plain AdamW */
+  float weight_decay;
+} adamw_tensor_t;
+
+typedef struct adamw_config {
+  double beta1, beta2;          /* in [0, 1) */
+  float lr;
+  float eps;                    /* >= 0 */
+  uint64_t seed;                /* of the stochastic rounding */
+  const float* grad_scale;      /* device or NULL: one float32 s (the clip coefficient of
+                                   muon_grad_norm, out + 1); read by the step, lies outside
+                                   every buffer the step writes */
+  muon_dtype_t w_dtype;         /* F32 or BF16 */
+  muon_dtype_t g_dtype;         /* F32 or BF16 */
+  int32_t state;                /* adamw_state_t */
+  int32_t rounding;             /* adamw_rounding_t (BLOCK8) */
+  int32_t reserved[4];
+} adamw_config_t;
+
+/* Fill `cfg` with the defaults: betas 0.9 and 0.999, lr 1e-3, eps 1e-8, bf16
+ * weights and gradients, 32-bit moments, stochastic rounding, seed 0. */
+void adamw_config_default(adamw_config_t* cfg);
+
+/* Bytes of device workspace a call or a plan over this batch needs.
+ * Errors: INVALID_ARG, DTYPE, UNSUPPORTED (n above 2^40, more than 2^20
+ * tensors, more than 2^31 - 1 pieces of 4096 elements), MEMORY. */
+muon_status_t adamw_workspace_bytes(const adamw_tensor_t* tensors, int64_t count,
+                                    const adamw_config_t* cfg, size_t* bytes);
+
+/* One AdamW step over `count` tensors (host array); `step` is t, from 1 on.
+ * Asynchronous on `stream`.  Uploads its descriptor table through a pinned
+ * staging buffer, so it is refused while `stream` is being captured: capture
+ * a plan's step instead.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, ALIAS, UNSUPPORTED, HIP, MEMORY. */
+muon_status_t adamw_step(const adamw_tensor_t* tensors, int64_t count, const adamw_config_t* cfg,
+                         int64_t step, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Prepared batch for repeated steps.  `steps_done` is the number of steps the
+ * moments have already taken (0 for new ones).  The step number and the
+ * learning rate live in the workspace and each step advances the number on
+ * the device, so a captured adamw_plan_step replays as the next step, with
+ * the rate set last.  Calls on one plan must be ordered, for example on one
+ * stream.  set_lr, set_step, get_state and set_state are asynchronous on
+ * `stream`, and can be captured too (a replay then sets the captured value).
+ * Errors of create: as adamw_step; of the others: INVALID_ARG, ALIAS, DTYPE,
+ * HIP. */
+typedef struct adamw_plan adamw_plan_t;
+muon_status_t adamw_plan_create(const adamw_tensor_t* tensors, int64_t count, const adamw_config_t* cfg,
+                                int64_t steps_done, void* workspace, size_t workspace_bytes,
+                                void* stream, adamw_plan_t** plan);
+muon_status_t adamw_plan_step(adamw_plan_t* plan, void* stream);
+/* Learning rate of later steps (finite). */
+muon_status_t adamw_plan_set_lr(adamw_plan_t* plan, float lr, void* stream);
+/* Number of steps done, for resuming (>= 0). */
+muon_status_t adamw_plan_set_step(adamw_plan_t* plan, int64_t steps_done, void* stream);
+/* The moments as values, for checkpoints and for moving between 32- and 8-bit
+ * moments.  `m` and `v` are device buffers of adamw_state_elems() elements of
+ * `dtype` (F32 or BF16), 16-byte aligned, overlapping no buffer of the plan;
+ * tensor i's n values start at the sum over j < i of n_j rounded up to
+ * ADAMW_BLOCK.  The gaps are left as they were.  set_state rounds to 8-bit
+ * codes to nearest.  The codes of a block whose scales are normal float32
+ * numbers survive get_state in F32 followed by set_state. */
+muon_status_t adamw_plan_get_state(adamw_plan_t* plan, void* m, void* v, muon_dtype_t dtype, void* stream);
+muon_status_t adamw_plan_set_state(adamw_plan_t* plan, const void* m, const void* v, muon_dtype_t dtype,
+                                   void* stream);
+muon_status_t adamw_state_elems(const adamw_tensor_t* tensors, int64_t count, int64_t* elems);
+/* Waits for the plan's upload to finish, then frees the plan (NULL is a no-op). */
+void adamw_plan_destroy(adamw_plan_t* plan);
+
+/* ------------------------------------------------------------------------
+ * Global gradient norm and clip coefficient over many tensors:
+ *   out[0] = N = sqrt(sum over all elements of g^2)
+ *   out[1] = 1 if N <= max_norm, else max_norm / N
+ * out[1] is meant for grad_scale of muon_config_t and adamw_config_t: the
+ * gradients are clipped where the steps read them, and no pass rewrites them.
+ * tensor_norms (NULL or `count` float32) receives every tensor's own norm.
+ * Squares and sums are binary64 in an order that depends only on the sizes
+ * and dtypes, so no float32 gradient overflows the sum and results repeat bit
+ * for bit.  NaN gives N = NaN and out[1] = NaN; Inf gives N = Inf and 0.
+ * A tensor with n = 0 has norm 0.  max_norm > 0; +Inf measures only.
+ * The gradients may share memory; out and tensor_norms overlap no other
+ * buffer.  Workspace, stream and capture rules are those of adamw_step and
+ * of its plan.
+ * ------------------------------------------------------------------------ */
+typedef struct muon_grad {
+  const void* g;        /* device, n of dtype, 16-byte aligned */
+  int64_t n;            /* elements, 0 <= n <= 2^40 */
+  muon_dtype_t dtype;   /* F32 or BF16; a batch may mix them */
+  int32_t reserved0;
+} muon_grad_t;
+
+muon_status_t muon_grad_norm_workspace_bytes(const muon_grad_t* grads, int64_t count, size_t* bytes);
+muon_status_t muon_grad_norm(const muon_grad_t* grads, int64_t count, float max_norm, float* out,
+                             float* tensor_norms, void* workspace, size_t workspace_bytes, void* stream);
+typedef struct muon_grad_norm_plan muon_grad_norm_plan_t;
+muon_status_t muon_grad_norm_plan_create(const muon_grad_t* grads, int64_t count, float max_norm, float* out,
+                                         float* tensor_norms, void* workspace, size_t workspace_bytes,
+                                         void* stream, muon_grad_norm_plan_t** plan);
+muon_status_t muon_grad_norm_plan_run(muon_grad_norm_plan_t* plan, void* stream);
+void muon_grad_norm_plan_destroy(muon_grad_norm_plan_t* plan);
 
 /* Static description of a status code. */
 const char* muon_status_string(muon_status_t status);
