@@ -5,49 +5,242 @@
 namespace muon {
 namespace {
 
-constexpr float kMTop = 256.0f;   // code value of a block's largest |m|
+// A workgroup walks pieces blockIdx.x, blockIdx.x + gridDim.x, ...; the
+// workgroups running at once stream through neighbouring memory.
+constexpr int kGrid32 = 2048, kGrid8 = 2048, kGridState = 2048;
 
 // ---------------------------------------------------------------------------
-// 8-bit codes.  `add` is what rounding adds to the 20 float32 mantissa bits
-// that a code drops.
+// Groups of N consecutive elements, element index a multiple of N and the
+// base 16-byte aligned; `cnt` of them exist (the others read as zero and are
+// not written).
 // ---------------------------------------------------------------------------
-constexpr uint32_t kNearestAdd = 0x80000u;
-__device__ __forceinline__ uint32_t add_of(uint32_t r16) { return r16 * 16u + 8u; }
-
-__device__ __forceinline__ bool finite_f32(float x) { return fabsf(x) < __builtin_inff(); }
-
-// e4m3 value of m at scale ms: below 2^-6 the step of e4m3 stays 2^-9, which
-// is its step in [2^-6, 2^-5), so those values are rounded after adding 2^-6.
-__device__ __forceinline__ uint8_t encode_m(float m, float ms, uint32_t add) {
-  if (!finite_f32(m)) return 0x7F;
-  const float y = ms > 0.0f ? fminf(fabsf(m) / ms, 448.0f) : 0.0f;
-  const float off = y < 0.015625f ? 0.015625f : 0.0f;
-  float q = __uint_as_float((__float_as_uint(y + off) + add) & 0xFFF00000u) - off;
-  q = copysignf(q, m);
-  return static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false) & 0xFF);   // exact
+template <bool BF16, int N>
+__device__ __forceinline__ void load_group(const void* p, int64_t i, int cnt, float (&out)[N]) {
+  if (cnt >= N) {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      float t[4];
+      if constexpr (BF16 && N == 8) {
+        if (e != 0) continue;
+        const uint4 u = *reinterpret_cast<const MUON_GLOBAL uint4*>(gmem(static_cast<const uint16_t*>(p)) + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          out[2 * k] = __uint_as_float(w[k] << 16);
+          out[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+      } else {
+        load4_aligned(p, i + e, BF16 ? DT_BF16 : DT_F32, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[e + k] = t[k];
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) out[e] = e < cnt ? load_elem(p, i + e, BF16 ? DT_BF16 : DT_F32) : 0.0f;
 }
 
-__device__ __forceinline__ float decode_m(uint8_t c, float ms) {
-  return __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(c), 0) * ms;
+template <bool BF16, int N>
+__device__ __forceinline__ void store_group(void* p, int64_t i, int cnt, const float (&v)[N]) {
+  if (cnt >= N) {
+    if constexpr (BF16 && N == 8) {
+      uint4 u;
+      u.x = pack_bf16x2(v[0], v[1]);
+      u.y = pack_bf16x2(v[2], v[3]);
+      u.z = pack_bf16x2(v[4], v[5]);
+      u.w = pack_bf16x2(v[6], v[7]);
+      *reinterpret_cast<MUON_GLOBAL uint4*>(gmem(static_cast<uint16_t*>(p)) + i) = u;
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; e += 4) {
+        const float t[4] = {v[e], v[e + 1], v[e + 2], v[e + 3]};
+        store4_aligned(p, i + e, BF16 ? DT_BF16 : DT_F32, t);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (e < cnt) store_elem(p, i + e, BF16 ? DT_BF16 : DT_F32, v[e]);
 }
 
-__device__ __forceinline__ uint8_t encode_v(float v, float vs, uint32_t add) {
-  if (!finite_f32(v) || v < 0.0f) return 255;
-  if (v == 0.0f) return 0;
-  const float y = fminf(v / vs, 1.0f);   // vs >= v > 0
-  const int c = static_cast<int>((__float_as_uint(y) + add) >> 20) - 768;
-  return static_cast<uint8_t>(c < 1 ? 1 : c);
+__device__ __forceinline__ uint2 load_codes(const void* p, int64_t i, int cnt) {
+  const MUON_GLOBAL uint8_t* q = gmem(static_cast<const uint8_t*>(p)) + i;
+  if (cnt >= 8) return *reinterpret_cast<const MUON_GLOBAL uint2*>(q);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < cnt) w[e >> 2] |= static_cast<uint32_t>(q[e]) << (8 * (e & 3));
+  return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ float decode_v(uint8_t c, float vs) {
-  if (c == 0) return 0.0f;
-  if (c == 255) return __builtin_nanf("");
-  return __uint_as_float((static_cast<uint32_t>(c) + 768u) << 20) * vs;
+__device__ __forceinline__ void store_codes(void* p, int64_t i, int cnt, uint2 c) {
+  MUON_GLOBAL uint8_t* q = gmem(static_cast<uint8_t*>(p)) + i;
+  if (cnt >= 8) {
+    *reinterpret_cast<MUON_GLOBAL uint2*>(q) = c;
+    return;
+  }
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < cnt) q[e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
 }
 
-// What an element adds to its block's maxima.
-__device__ __forceinline__ float max_m_of(float m) { return finite_f32(m) ? fabsf(m) : 0.0f; }
-__device__ __forceinline__ float max_v_of(float v) { return finite_f32(v) && v > 0.0f ? v : 0.0f; }
+// ---------------------------------------------------------------------------
+// 8-bit moments.  A block of 256 elements is half a wave's: 32 lanes of eight
+// elements (16-byte bf16 and 8-byte code accesses; a block's maximum takes
+// four DPP steps and one exchange of 16-lane rows).
+// ---------------------------------------------------------------------------
+constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr uint32_t kNearestAdd = 0x80000u;   // half of the 20 mantissa bits that a code drops
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false));
+}
+
+// Maximum over each half of the wave, in every lane of it.
+__device__ __forceinline__ uint32_t half_max(uint32_t v) {
+  v = max(v, dpp_u32<0xB1>(v));    // quad_perm [1,0,3,2]
+  v = max(v, dpp_u32<0x4E>(v));    // quad_perm [2,3,0,1]
+  v = max(v, dpp_u32<0x141>(v));   // row_half_mirror
+  v = max(v, dpp_u32<0x140>(v));   // row_mirror
+  const auto rows = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return max(static_cast<uint32_t>(rows[0]), static_cast<uint32_t>(rows[1]));
+}
+
+// Scales of a block and what its encoding needs, from the bits of the largest
+// |m| and v.  The reciprocals (1 ulp) are taken of values that keep them
+// normal numbers: v is encoded as y * 2^40 or y * 2^-24, its code's offset
+// following (y = v / vs, whose bits give the code).
+struct BlockScale {
+  float ms, vs, minv, vinv, vtop;
+  uint32_t voff;   // code offset << 20
+};
+
+__device__ __forceinline__ BlockScale block_scale(uint32_t mbits, uint32_t vbits) {
+  BlockScale b;
+  // Below 2^-118 (0x04800000) 1 / ms would overflow: such a block is zero.
+  b.ms = mbits >= 0x04800000u ? __uint_as_float(mbits) * 0x1p-8f : 0.0f;
+  b.minv = b.ms > 0.0f ? __builtin_amdgcn_rcpf(b.ms) : 0.0f;
+  b.vs = __uint_as_float(vbits);
+  const bool big = b.vs >= 1.0f;
+  b.vinv = big ? __builtin_amdgcn_rcpf(b.vs * 0x1p-40f) : __builtin_amdgcn_rcpf(b.vs * 0x1p32f) * 0x1p8f;
+  if (vbits == 0) b.vinv = 0.0f;
+  b.vtop = big ? 0x1p40f : 0x1p-24f;
+  b.voff = big ? 1088u << 20 : 576u << 20;
+  return b;
+}
+
+// e4m3 value of |m| / ms with the sign of m.  Below 2^-6 the step of e4m3
+// stays 2^-9, which is its step in [2^-6, 2^-5): those values are rounded
+// after adding 2^-6.
+__device__ __forceinline__ float round_m(float m, const BlockScale& b, uint32_t add) {
+  const float y = fminf(fabsf(m) * b.minv, 256.0f);
+  const float off = y < 0x1p-6f ? 0x1p-6f : 0.0f;
+  const float q = __uint_as_float((__float_as_uint(y + off) + add) & 0xFFF00000u) - off;
+  return copysignf(q, m);
+}
+
+// Code of v >= 0; at least 1 if v > 0.
+__device__ __forceinline__ uint32_t code_v(float v, const BlockScale& b, uint32_t add) {
+  const float y = fminf(v * b.vinv, b.vtop);
+  const int c = static_cast<int>(__float_as_uint(y) + add - b.voff) >> 20;
+  return static_cast<uint32_t>(max(c, static_cast<int>(min(__float_as_uint(v), 1u))));
+}
+
+// Rounds eight elements to codes, of which `cnt` exist (the others are zero).
+// idx is the first one's index in the batch.
+template <bool STOCHASTIC>
+__device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8], uint32_t key, int64_t idx,
+                                        uint2& mc, uint2& vc, float& ms, float& vs) {
+  uint32_t mmax = 0, vmax = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    mmax = max(mmax, __float_as_uint(m[e]) & 0x7FFFFFFFu);
+    vmax = max(vmax, __float_as_uint(v[e]));
+  }
+  mmax = half_max(mmax);
+  vmax = half_max(vmax);
+  // NaN, Inf and negative v have bits from kInfBits on: then the maxima are
+  // taken over the other elements, and those get the codes of NaN.
+  const bool odd = __any(mmax >= kInfBits || vmax >= kInfBits);
+  uint32_t mbad = 0, vbad = 0;
+  if (odd) {
+    mmax = 0;
+    vmax = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t mb = __float_as_uint(m[e]) & 0x7FFFFFFFu, vb = __float_as_uint(v[e]);
+      if (mb >= kInfBits) mbad |= 1u << e; else mmax = max(mmax, mb);
+      if (vb >= kInfBits) vbad |= 1u << e; else vmax = max(vmax, vb);
+    }
+    mmax = half_max(mmax);
+    vmax = half_max(vmax);
+  }
+  const BlockScale b = block_scale(mmax, vmax);
+  ms = b.ms;
+  vs = b.vs;
+  uint32_t hi = 0;
+  if constexpr (STOCHASTIC) hi = adam_mix(key + static_cast<uint32_t>(static_cast<uint64_t>(idx) >> 32));
+  float q[8];
+  uint32_t c[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint32_t am = kNearestAdd, av = kNearestAdd;
+    if constexpr (STOCHASTIC) {
+      const uint32_t h = adam_mix(static_cast<uint32_t>(idx) + e + hi);
+      am = (h & 0xFFFFu) << 4 | 8u;
+      av = (h >> 16) << 4 | 8u;
+    }
+    q[e] = round_m(m[e], b, am);
+    c[e] = code_v(v[e], b, av);
+  }
+  if (odd) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (mbad >> e & 1) q[e] = 0.0f;
+      if (vbad >> e & 1) c[e] = 255;
+    }
+  }
+  int lo0 = 0, lo1 = 0;
+  lo0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], lo0, false);   // exact: q is an e4m3 value
+  lo0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo0, true);
+  lo1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], lo1, false);
+  lo1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], lo1, true);
+  mc = make_uint2(static_cast<uint32_t>(lo0), static_cast<uint32_t>(lo1));
+  vc = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+  if (odd) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (mbad >> e & 1) (e < 4 ? mc.x : mc.y) |= 0x7Fu << (8 * (e & 3));   // the code was zero
+  }
+}
+
+// Unscaled values of eight codes.
+__device__ __forceinline__ void decode8(uint2 mc, uint2 vc, float (&m)[8], float (&v)[8]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(mc.x), false);
+  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(mc.x), true);
+  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(mc.y), false);
+  const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(mc.y), true);
+  m[0] = a.x; m[1] = a.y; m[2] = b.x; m[3] = b.y;
+  m[4] = c.x; m[5] = c.y; m[6] = d.x; m[7] = d.y;
+  const uint32_t w[2] = {vc.x, vc.y};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t k = w[e >> 2] >> (8 * (e & 3)) & 0xFFu;
+    v[e] = k ? __uint_as_float((k << 20) + 0x30000000u) : 0.0f;
+  }
+  // A byte 255 (NaN): a zero byte of the complement.
+  const uint32_t nan = ((~w[0] - 0x01010101u) & w[0] & 0x80808080u) | ((~w[1] - 0x01010101u) & w[1] & 0x80808080u);
+  if (__any(nan != 0)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if ((w[e >> 2] >> (8 * (e & 3)) & 0xFFu) == 255u) v[e] = __builtin_nanf("");
+  }
+}
 
 // ---------------------------------------------------------------------------
 // One step
@@ -72,13 +265,18 @@ __device__ __forceinline__ StepValues step_values(const AdamArgs& a) {
   return s;
 }
 
-__device__ __forceinline__ float moments(const StepValues& s, float g, float w, float& m, float& v, float lr_scale,
-                                         float wd) {
+// One element: m and v hold the old moments before their factors (fm, fv:
+// beta times the block's scale, or beta) and the new ones after; returns the
+// new weight.  `adam` and `decay` are lr * lr_scale / (1 - beta1^t) and
+// lr * weight_decay.  Square root and reciprocal are the 1 ulp instructions.
+__device__ __forceinline__ float update(const StepValues& s, float g, float w, float fm, float fv, float adam,
+                                        float decay, float& m, float& v) {
   const float y = g * s.gs;
-  m = s.b1 * m + s.c1 * y;
-  v = s.b2 * v + s.c2 * (y * y);
-  const float upd = (m * s.rb1) / (sqrtf(v) * s.rb2 + s.eps);
-  return w - s.lr * (lr_scale * upd + wd * w);
+  m = fm * m + s.c1 * y;
+  v = fv * v + s.c2 * (y * y);
+  const float den = __builtin_amdgcn_sqrtf(v) * s.rb2 + s.eps;
+  const float upd = (m * adam) * __builtin_amdgcn_rcpf(den);
+  return w - (upd + decay * w);
 }
 
 // The last workgroup to have read the step's values writes the next step's.
@@ -96,67 +294,109 @@ __device__ __forceinline__ void finish_step(const AdamArgs& a, bool advance) {
   *a.ctl = c;
 }
 
-__global__ __launch_bounds__(kAdamThreads) void k_adamw(AdamArgs a, bool advance) {
+// Elements of the group of N from `i` on that lie below n.
+template <bool FULL, int N>
+__device__ __forceinline__ int count_of(int64_t i, int64_t n) {
+  if constexpr (FULL) return N;
+  const int64_t k = n - i;
+  return k < 0 ? 0 : k > N ? N : static_cast<int>(k);
+}
+
+// 32-bit moments.  Four groups of four elements per thread and piece (FULL:
+// the piece is whole, and no access is guarded).
+template <bool WB, bool GB, bool MASTER, bool FULL>
+__device__ __forceinline__ void piece32(const StepValues& s, const AdamDesc& d, int64_t base) {
+  constexpr int G = kAdamPiece / (4 * kAdamThreads);
+  const float adam = s.lr * d.lr_scale * s.rb1, decay = s.lr * d.weight_decay;
+  float g[G][4], w[G][4], m[G][4], v[G][4];
+  int cnt[G];
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const int64_t i = base + j * 4 * kAdamThreads;
+    cnt[j] = count_of<FULL, 4>(i, d.n);
+    load_group<GB>(d.g, i, cnt[j], g[j]);
+    load_group<false>(d.m, i, cnt[j], m[j]);
+    load_group<false>(d.v, i, cnt[j], v[j]);
+    if constexpr (MASTER) load_group<false>(d.master, i, cnt[j], w[j]);
+    else load_group<WB>(d.w, i, cnt[j], w[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const int64_t i = base + j * 4 * kAdamThreads;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[j][e] = update(s, g[j][e], w[j][e], s.b1, s.b2, adam, decay, m[j][e], v[j][e]);
+    store_group<false>(d.m, i, cnt[j], m[j]);
+    store_group<false>(d.v, i, cnt[j], v[j]);
+    if constexpr (MASTER) store_group<false>(d.master, i, cnt[j], w[j]);
+    store_group<WB>(d.w, i, cnt[j], w[j]);
+  }
+}
+
+template <bool WB, bool GB, bool MASTER>
+__global__ __launch_bounds__(kAdamThreads) void k_adamw32(AdamArgs a, bool advance) {
   const StepValues s = step_values(a);
   for (int64_t p = blockIdx.x; p < a.npieces; p += gridDim.x) {
     const AdamPiece pc = a.pieces[p];
     const AdamDesc& d = a.desc[pc.tensor];
-    const int64_t base = static_cast<int64_t>(pc.piece) * kAdamPiece;
-    const int64_t end = base + kAdamPiece < d.n ? base + kAdamPiece : d.n;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // One wave per block of 256, four elements per lane.
-    for (int64_t b = base + wave * ADAMW_BLOCK; b < end; b += 4 * ADAMW_BLOCK) {
-      float m[4], v[4];
-      float mmax = 0.0f, vmax = 0.0f;
-      const int64_t blk = b / ADAMW_BLOCK;
-      const float ms = a.block8 ? d.m_scale[blk] : 0.0f, vs = a.block8 ? d.v_scale[blk] : 0.0f;
+    const int64_t at = static_cast<int64_t>(pc.piece) * kAdamPiece;
+    if (d.n - at >= kAdamPiece) piece32<WB, GB, MASTER, true>(s, d, at + 4 * threadIdx.x);
+    else piece32<WB, GB, MASTER, false>(s, d, at + 4 * threadIdx.x);
+  }
+  finish_step(a, advance);
+}
+
+// 8-bit moments.  Two groups of eight elements per thread and piece.
+template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, bool FULL>
+__device__ __forceinline__ void piece8(const StepValues& s, const AdamDesc& d, int64_t base) {
+  constexpr int G = kAdamPiece / (8 * kAdamThreads);
+  const float adam = s.lr * d.lr_scale * s.rb1, decay = s.lr * d.weight_decay;
+  float g[G][8], w[G][8], ms[G], vs[G];
+  uint2 mc[G], vc[G];
+  int cnt[G];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = b + 4 * lane + e;
-        m[e] = 0.0f;
-        v[e] = 0.0f;
-        if (i >= end) continue;
-        if (a.block8) {
-          m[e] = decode_m(static_cast<const uint8_t*>(d.m)[i], ms);
-          v[e] = decode_v(static_cast<const uint8_t*>(d.v)[i], vs);
-        } else {
-          m[e] = static_cast<const float*>(d.m)[i];
-          v[e] = static_cast<const float*>(d.v)[i];
-        }
-        const float g = load_elem(d.g, i, a.g_dt);
-        const float w = d.master ? d.master[i] : load_elem(d.w, i, a.w_dt);
-        const float w1 = moments(s, g, w, m[e], v[e], d.lr_scale, d.weight_decay);
-        if (d.master) d.master[i] = w1;
-        store_elem(d.w, i, a.w_dt, w1);
-        if (!a.block8) {
-          static_cast<float*>(d.m)[i] = m[e];
-          static_cast<float*>(d.v)[i] = v[e];
-        }
-        mmax = fmaxf(mmax, max_m_of(m[e]));
-        vmax = fmaxf(vmax, max_v_of(v[e]));
-      }
-      if (!a.block8) continue;
-      const float ms1 = wave_max(mmax) * (1.0f / kMTop), vs1 = wave_max(vmax);
-      if (lane == 0) {
-        d.m_scale[blk] = ms1;
-        d.v_scale[blk] = vs1;
-      }
+  for (int j = 0; j < G; ++j) {
+    const int64_t i = base + j * 8 * kAdamThreads;
+    cnt[j] = count_of<FULL, 8>(i, d.n);
+    // Lanes of a block without elements read the scale of the last block.
+    const int64_t blk = (cnt[j] > 0 ? i : d.n - 1) / ADAMW_BLOCK;
+    ms[j] = gmem(d.m_scale)[blk];
+    vs[j] = gmem(d.v_scale)[blk];
+    mc[j] = load_codes(d.m, i, cnt[j]);
+    vc[j] = load_codes(d.v, i, cnt[j]);
+    load_group<GB>(d.g, i, cnt[j], g[j]);
+    if constexpr (MASTER) load_group<false>(d.master, i, cnt[j], w[j]);
+    else load_group<WB>(d.w, i, cnt[j], w[j]);
+  }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = b + 4 * lane + e;
-        if (i >= end) continue;
-        uint32_t am = kNearestAdd, av = kNearestAdd;
-        if (a.stochastic) {
-          const uint64_t id = static_cast<uint64_t>(d.first + i);
-          const uint32_t h = adam_mix(static_cast<uint32_t>(id) +
-                                      adam_mix(s.key + static_cast<uint32_t>(id >> 32)));
-          am = add_of(h & 0xFFFFu);
-          av = add_of(h >> 16);
-        }
-        static_cast<uint8_t*>(d.m)[i] = encode_m(m[e], ms1, am);
-        static_cast<uint8_t*>(d.v)[i] = encode_v(v[e], vs1, av);
-      }
+  for (int j = 0; j < G; ++j) {
+    const int64_t i = base + j * 8 * kAdamThreads;
+    float m[8], v[8];
+    decode8(mc[j], vc[j], m, v);
+    const float fm = s.b1 * ms[j], fv = s.b2 * vs[j];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[j][e] = update(s, g[j][e], w[j][e], fm, fv, adam, decay, m[e], v[e]);
+    if constexpr (MASTER) store_group<false>(d.master, i, cnt[j], w[j]);
+    store_group<WB>(d.w, i, cnt[j], w[j]);
+    float ms1, vs1;
+    encode8<STOCHASTIC>(m, v, s.key, d.first + i, mc[j], vc[j], ms1, vs1);
+    store_codes(d.m, i, cnt[j], mc[j]);
+    store_codes(d.v, i, cnt[j], vc[j]);
+    if ((threadIdx.x & 31) == 0 && cnt[j] > 0) {
+      gmem(d.m_scale)[i / ADAMW_BLOCK] = ms1;
+      gmem(d.v_scale)[i / ADAMW_BLOCK] = vs1;
     }
+  }
+}
+
+template <bool WB, bool GB, bool MASTER, bool STOCHASTIC>
+__global__ __launch_bounds__(kAdamThreads) void k_adamw8(AdamArgs a, bool advance) {
+  const StepValues s = step_values(a);
+  for (int64_t p = blockIdx.x; p < a.npieces; p += gridDim.x) {
+    const AdamPiece pc = a.pieces[p];
+    const AdamDesc& d = a.desc[pc.tensor];
+    const int64_t at = static_cast<int64_t>(pc.piece) * kAdamPiece;
+    if (d.n - at >= kAdamPiece) piece8<WB, GB, MASTER, STOCHASTIC, true>(s, d, at + 8 * threadIdx.x);
+    else piece8<WB, GB, MASTER, STOCHASTIC, false>(s, d, at + 8 * threadIdx.x);
   }
   finish_step(a, advance);
 }
@@ -177,74 +417,112 @@ __global__ void k_ctl(AdamCtl* ctl, AdamCtl value, bool set_step) {
 // ---------------------------------------------------------------------------
 // The moments as values
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kAdamThreads) void k_get(AdamArgs a, void* m_out, void* v_out, int32_t dt) {
+template <bool BLOCK8, bool BF16, bool FULL>
+__device__ __forceinline__ void piece_get(const AdamDesc& d, int64_t base, void* m_out, void* v_out) {
+#pragma unroll
+  for (int j = 0; j < kAdamPiece / (8 * kAdamThreads); ++j) {
+    const int64_t i = base + j * 8 * kAdamThreads;
+    const int cnt = count_of<FULL, 8>(i, d.n);
+    float m[8], v[8];
+    if constexpr (BLOCK8) {
+      const int64_t blk = (cnt > 0 ? i : d.n - 1) / ADAMW_BLOCK;
+      const float ms = gmem(d.m_scale)[blk], vs = gmem(d.v_scale)[blk];
+      decode8(load_codes(d.m, i, cnt), load_codes(d.v, i, cnt), m, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        m[e] *= ms;
+        v[e] *= vs;
+      }
+    } else {
+      load_group<false>(d.m, i, cnt, m);
+      load_group<false>(d.v, i, cnt, v);
+    }
+    store_group<BF16>(m_out, d.first + i, cnt, m);
+    store_group<BF16>(v_out, d.first + i, cnt, v);
+  }
+}
+
+template <bool BLOCK8, bool BF16>
+__global__ __launch_bounds__(kAdamThreads) void k_get(AdamArgs a, void* m_out, void* v_out) {
   for (int64_t p = blockIdx.x; p < a.npieces; p += gridDim.x) {
     const AdamPiece pc = a.pieces[p];
     const AdamDesc& d = a.desc[pc.tensor];
-    const int64_t base = static_cast<int64_t>(pc.piece) * kAdamPiece;
-    const int64_t end = base + kAdamPiece < d.n ? base + kAdamPiece : d.n;
-    for (int64_t i = base + threadIdx.x; i < end; i += kAdamThreads) {
-      float m, v;
-      if (a.block8) {
-        m = decode_m(static_cast<const uint8_t*>(d.m)[i], d.m_scale[i / ADAMW_BLOCK]);
-        v = decode_v(static_cast<const uint8_t*>(d.v)[i], d.v_scale[i / ADAMW_BLOCK]);
-      } else {
-        m = static_cast<const float*>(d.m)[i];
-        v = static_cast<const float*>(d.v)[i];
+    const int64_t at = static_cast<int64_t>(pc.piece) * kAdamPiece;
+    if (d.n - at >= kAdamPiece) piece_get<BLOCK8, BF16, true>(d, at + 8 * threadIdx.x, m_out, v_out);
+    else piece_get<BLOCK8, BF16, false>(d, at + 8 * threadIdx.x, m_out, v_out);
+  }
+}
+
+template <bool BLOCK8, bool BF16, bool FULL>
+__device__ __forceinline__ void piece_set(const AdamDesc& d, int64_t base, const void* m_in, const void* v_in) {
+#pragma unroll
+  for (int j = 0; j < kAdamPiece / (8 * kAdamThreads); ++j) {
+    const int64_t i = base + j * 8 * kAdamThreads;
+    const int cnt = count_of<FULL, 8>(i, d.n);
+    float m[8], v[8];
+    load_group<BF16>(m_in, d.first + i, cnt, m);
+    load_group<BF16>(v_in, d.first + i, cnt, v);
+    if constexpr (BLOCK8) {
+      uint2 mc, vc;
+      float ms, vs;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += 0.0f;   // -0 becomes +0
+      encode8<false>(m, v, 0, 0, mc, vc, ms, vs);
+      store_codes(d.m, i, cnt, mc);
+      store_codes(d.v, i, cnt, vc);
+      if ((threadIdx.x & 31) == 0 && cnt > 0) {
+        gmem(d.m_scale)[i / ADAMW_BLOCK] = ms;
+        gmem(d.v_scale)[i / ADAMW_BLOCK] = vs;
       }
-      store_elem(m_out, d.first + i, dt, m);
-      store_elem(v_out, d.first + i, dt, v);
+    } else {
+      store_group<false>(d.m, i, cnt, m);
+      store_group<false>(d.v, i, cnt, v);
     }
   }
 }
 
-__global__ __launch_bounds__(kAdamThreads) void k_set(AdamArgs a, const void* m_in, const void* v_in, int32_t dt) {
+template <bool BLOCK8, bool BF16>
+__global__ __launch_bounds__(kAdamThreads) void k_set(AdamArgs a, const void* m_in, const void* v_in) {
   for (int64_t p = blockIdx.x; p < a.npieces; p += gridDim.x) {
     const AdamPiece pc = a.pieces[p];
     const AdamDesc& d = a.desc[pc.tensor];
-    const int64_t base = static_cast<int64_t>(pc.piece) * kAdamPiece;
-    const int64_t end = base + kAdamPiece < d.n ? base + kAdamPiece : d.n;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t b = base + wave * ADAMW_BLOCK; b < end; b += 4 * ADAMW_BLOCK) {
-      float m[4], v[4];
-      float mmax = 0.0f, vmax = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = b + 4 * lane + e;
-        m[e] = i < end ? load_elem(m_in, d.first + i, dt) : 0.0f;
-        v[e] = i < end ? load_elem(v_in, d.first + i, dt) : 0.0f;
-        mmax = fmaxf(mmax, max_m_of(m[e]));
-        vmax = fmaxf(vmax, max_v_of(v[e]));
-        if (i < end && !a.block8) {
-          static_cast<float*>(d.m)[i] = m[e];
-          static_cast<float*>(d.v)[i] = v[e];
-        }
-      }
-      if (!a.block8) continue;
-      const float ms = wave_max(mmax) * (1.0f / kMTop), vs = wave_max(vmax);
-      if (lane == 0) {
-        d.m_scale[b / ADAMW_BLOCK] = ms;
-        d.v_scale[b / ADAMW_BLOCK] = vs;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = b + 4 * lane + e;
-        if (i >= end) continue;
-        static_cast<uint8_t*>(d.m)[i] = encode_m(m[e], ms, kNearestAdd);
-        static_cast<uint8_t*>(d.v)[i] = encode_v(v[e], vs, kNearestAdd);
-      }
-    }
+    const int64_t at = static_cast<int64_t>(pc.piece) * kAdamPiece;
+    if (d.n - at >= kAdamPiece) piece_set<BLOCK8, BF16, true>(d, at + 8 * threadIdx.x, m_in, v_in);
+    else piece_set<BLOCK8, BF16, false>(d, at + 8 * threadIdx.x, m_in, v_in);
   }
 }
 
-unsigned grid_of(const AdamArgs& a) { return static_cast<unsigned>(a.npieces < 2048 ? a.npieces : 2048); }
+// At most `most` workgroups; a batch without elements still takes its step
+// (the step number advances).
+unsigned grid_of(const AdamArgs& a, int most) {
+  return static_cast<unsigned>(a.npieces < 1 ? 1 : a.npieces < most ? a.npieces : most);
+}
+
+template <bool WB, bool GB, bool MASTER>
+void launch_step(const AdamArgs& a, bool advance, hipStream_t s) {
+  const dim3 threads(kAdamThreads);
+  if (!a.block8)
+    hipLaunchKernelGGL((k_adamw32<WB, GB, MASTER>), dim3(grid_of(a, kGrid32)), threads, 0, s, a, advance);
+  else if (a.stochastic)
+    hipLaunchKernelGGL((k_adamw8<WB, GB, MASTER, true>), dim3(grid_of(a, kGrid8)), threads, 0, s, a, advance);
+  else
+    hipLaunchKernelGGL((k_adamw8<WB, GB, MASTER, false>), dim3(grid_of(a, kGrid8)), threads, 0, s, a, advance);
+}
 
 }  // namespace
 
 hipError_t launch_adamw(const AdamArgs& a, bool advance, hipStream_t s) {
-  // A batch without elements still takes its step (the step number advances).
-  const unsigned grid = a.npieces ? grid_of(a) : 1;
-  hipLaunchKernelGGL(k_adamw, dim3(grid), dim3(kAdamThreads), 0, s, a, advance);
+  const bool wb = a.w_dt == DT_BF16, gb = a.g_dt == DT_BF16;
+  if (a.has_master) {
+    if (gb) launch_step<true, true, true>(a, advance, s);
+    else launch_step<true, false, true>(a, advance, s);
+  } else if (wb) {
+    if (gb) launch_step<true, true, false>(a, advance, s);
+    else launch_step<true, false, false>(a, advance, s);
+  } else {
+    if (gb) launch_step<false, true, false>(a, advance, s);
+    else launch_step<false, false, false>(a, advance, s);
+  }
   return hipGetLastError();
 }
 
@@ -255,13 +533,29 @@ hipError_t launch_adamw_ctl(AdamCtl* ctl, const AdamCtl& value, bool set_step, h
 
 hipError_t launch_adamw_get(const AdamArgs& a, void* m, void* v, int32_t dt, hipStream_t s) {
   if (!a.npieces) return hipSuccess;
-  hipLaunchKernelGGL(k_get, dim3(grid_of(a)), dim3(kAdamThreads), 0, s, a, m, v, dt);
+  const dim3 grid(grid_of(a, kGridState)), threads(kAdamThreads);
+  const bool bf16 = dt == DT_BF16;
+  if (a.block8) {
+    if (bf16) hipLaunchKernelGGL((k_get<true, true>), grid, threads, 0, s, a, m, v);
+    else hipLaunchKernelGGL((k_get<true, false>), grid, threads, 0, s, a, m, v);
+  } else {
+    if (bf16) hipLaunchKernelGGL((k_get<false, true>), grid, threads, 0, s, a, m, v);
+    else hipLaunchKernelGGL((k_get<false, false>), grid, threads, 0, s, a, m, v);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int32_t dt, hipStream_t s) {
   if (!a.npieces) return hipSuccess;
-  hipLaunchKernelGGL(k_set, dim3(grid_of(a)), dim3(kAdamThreads), 0, s, a, m, v, dt);
+  const dim3 grid(grid_of(a, kGridState)), threads(kAdamThreads);
+  const bool bf16 = dt == DT_BF16;
+  if (a.block8) {
+    if (bf16) hipLaunchKernelGGL((k_set<true, true>), grid, threads, 0, s, a, m, v);
+    else hipLaunchKernelGGL((k_set<true, false>), grid, threads, 0, s, a, m, v);
+  } else {
+    if (bf16) hipLaunchKernelGGL((k_set<false, true>), grid, threads, 0, s, a, m, v);
+    else hipLaunchKernelGGL((k_set<false, false>), grid, threads, 0, s, a, m, v);
+  }
   return hipGetLastError();
 }
 

@@ -4,7 +4,7 @@
 namespace muon {
 namespace {
 
-// Sum over the workgroup, in a fixed order; thread 0 has the result.
+// Sum over the workgroup, in a fixed order; every thread has the result.
 __device__ __forceinline__ double block_sum(double v, double* red) {
   v = wave_sum_f64(v);
   __syncthreads();
@@ -17,23 +17,68 @@ __device__ __forceinline__ double load_partial(const double* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+__device__ __forceinline__ void add_square(double& s, float x) {
+  const double d = x;
+  s = __builtin_fma(d, d, s);
+}
+
+// Squares of the V = 16 bytes' worth of elements in one load.
+template <bool BF16>
+__device__ __forceinline__ void add_vector(double (&s)[2], uint4 u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF16) {
+      add_square(s[0], __uint_as_float(w[k] << 16));
+      add_square(s[1], __uint_as_float(w[k] & 0xffff0000u));
+    } else {
+      add_square(s[k & 1], __uint_as_float(w[k]));
+    }
+  }
+}
+
+// This thread's share of a run: 16-byte vectors threadIdx.x + k * threads,
+// four in flight, then the elements behind the last whole vector.
+template <bool BF16>
+__device__ __forceinline__ double run_sum(const void* g, int64_t begin, int64_t count) {
+  constexpr int V = BF16 ? 8 : 4, U = 4;
+  const char* base = static_cast<const char*>(g) + begin * (BF16 ? 2 : 4);
+  const MUON_GLOBAL uint4* q = reinterpret_cast<const MUON_GLOBAL uint4*>(gmem(base));
+  const int64_t nv = count / V;
+  double s[2] = {0.0, 0.0};
+  int64_t i = threadIdx.x;
+  for (; i + (U - 1) * kNormThreads < nv; i += U * kNormThreads) {
+    uint4 u[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) u[k] = q[i + k * kNormThreads];
+#pragma unroll
+    for (int k = 0; k < U; ++k) add_vector<BF16>(s, u[k]);
+  }
+  for (; i < nv; i += kNormThreads) add_vector<BF16>(s, q[i]);
+  const int64_t e = nv * V + threadIdx.x;
+  if (e < count) add_square(s[0], load_elem(base, e, BF16 ? DT_BF16 : DT_F32));
+  return s[0] + s[1];
+}
+
 __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
   __shared__ double red[4];
   __shared__ bool last;
   for (uint32_t r = a.first_run[blockIdx.x]; r < a.first_run[blockIdx.x + 1]; ++r) {
     const NormRun run = a.runs[r];
     const NormTensor& t = a.tensors[run.tensor];
-    double sum = 0.0;
-    for (int64_t i = threadIdx.x; i < run.count; i += kNormThreads) {
-      const double x = load_elem(t.g, run.begin + i, t.dt);
-      sum = __builtin_fma(x, x, sum);
-    }
-    sum = block_sum(sum, red);
+    const double part = t.dt == DT_BF16 ? run_sum<true>(t.g, run.begin, run.count)
+                                        : run_sum<false>(t.g, run.begin, run.count);
+    const double sum = block_sum(part, red);
     if (threadIdx.x == 0) __hip_atomic_store(&a.partial[r], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  // The last workgroup to store its sums adds them all up.
-  if (threadIdx.x == 0)
-    last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  // The last workgroup to store its sums adds them all up.  The sums are
+  // stored and loaded at agent scope, past the XCD's own L2, and each is
+  // complete before its workgroup counts itself; so the counter needs no
+  // release, which would write back the whole L2.
+  if (threadIdx.x == 0) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  }
   __syncthreads();
   if (!last) return;
   double sum = 0.0;

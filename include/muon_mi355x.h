@@ -281,7 +281,8 @@ void muon_plan_destroy(muon_plan_t* plan);
  * A block holds one float32 per moment and one byte per element and moment:
  *   m  = e4m3(code) * m_scale     m_scale = max|m| / 256 over the block.
  *        The code is OCP float8 e4m3 (torch.float8_e4m3fn); the block's
- *        largest |m| has the code of 256.
+ *        largest |m| has the code of 256.  A block whose largest |m| is below
+ *        2^-118 is stored as zeros, its scale too.
  *   v  = u(code) * v_scale        v_scale = max v over the block.
  *        u is an unsigned float with 5 exponent and 3 mantissa bits: u(0) = 0,
  *        u(255) = NaN, and u(c) is the binary32 with the bits

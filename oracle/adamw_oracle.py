@@ -68,7 +68,8 @@ def scales(m, v):
     m, v = np.asarray(m, np.float64), np.asarray(v, np.float64)
     am = np.where(np.isfinite(m), np.abs(m), 0.0)
     av = np.where(np.isfinite(v) & (v > 0), v, 0.0)
-    return _blocks(am).max(axis=1) / 256, _blocks(av).max(axis=1)
+    top = _blocks(am).max(axis=1)
+    return np.where(top >= 2.0 ** -118, top / 256, 0.0), _blocks(av).max(axis=1)
 
 
 def _spread(scale, n):
