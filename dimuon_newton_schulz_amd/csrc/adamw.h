@@ -56,6 +56,7 @@ struct AdamArgs {
   const float* grad_scale;  // or NULL
   double beta1, beta2;
   uint64_t seed;
+  float c1, root_c2;      // 1 - beta1, sqrt(1 - beta2)
   float eps;
   int32_t w_dt, g_dt;
   int32_t block8;         // 8-bit moments

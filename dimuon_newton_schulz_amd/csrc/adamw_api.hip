@@ -206,6 +206,8 @@ AdamArgs adam_args(const AdamTable& t, const adamw_config_t& cfg, void* ws) {
   a.beta1 = cfg.beta1;
   a.beta2 = cfg.beta2;
   a.seed = cfg.seed;
+  a.c1 = static_cast<float>(1.0 - cfg.beta1);
+  a.root_c2 = static_cast<float>(std::sqrt(1.0 - cfg.beta2));
   a.eps = cfg.eps;
   a.w_dt = cfg.w_dtype;
   a.g_dt = cfg.g_dtype;

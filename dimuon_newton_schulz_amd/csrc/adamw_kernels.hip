@@ -93,7 +93,6 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int cnt, uint2 c
 // four DPP steps and one exchange of 16-lane rows).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kInfBits = 0x7F800000u;
-constexpr uint32_t kNearestAdd = 0x80000u;   // half of the 20 mantissa bits that a code drops
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
@@ -115,7 +114,7 @@ __device__ __forceinline__ uint32_t half_max(uint32_t v) {
 // normal numbers: v is encoded as y * 2^40 or y * 2^-24, its code's offset
 // following (y = v / vs, whose bits give the code).
 struct BlockScale {
-  float ms, vs, minv, vinv, vtop;
+  float ms, vs, minv, vinv;
   uint32_t voff;   // code offset << 20
 };
 
@@ -128,30 +127,36 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t mbits, uint32_t vbits
   const bool big = b.vs >= 1.0f;
   b.vinv = big ? __builtin_amdgcn_rcpf(b.vs * 0x1p-40f) : __builtin_amdgcn_rcpf(b.vs * 0x1p32f) * 0x1p8f;
   if (vbits == 0) b.vinv = 0.0f;
-  b.vtop = big ? 0x1p40f : 0x1p-24f;
   b.voff = big ? 1088u << 20 : 576u << 20;
   return b;
 }
 
-// e4m3 value of |m| / ms with the sign of m.  Below 2^-6 the step of e4m3
-// stays 2^-9, which is its step in [2^-6, 2^-5): those values are rounded
-// after adding 2^-6.
-__device__ __forceinline__ float round_m(float m, const BlockScale& b, uint32_t add) {
-  const float y = fminf(fabsf(m) * b.minv, 256.0f);
-  const float off = y < 0x1p-6f ? 0x1p-6f : 0.0f;
-  const float q = __uint_as_float((__float_as_uint(y + off) + add) & 0xFFF00000u) - off;
-  return copysignf(q, m);
+// 16 * (upper half of h) + t, one instruction.
+__device__ __forceinline__ uint32_t add_upper16(uint32_t h, uint32_t t) {
+  uint32_t r;
+  asm("v_mad_u32_u16 %0, %1, 16, %2 op_sel:[1,0,0,0]" : "=v"(r) : "v"(h), "v"(t));
+  return r;
 }
 
-// Code of v >= 0; at least 1 if v > 0.
-__device__ __forceinline__ uint32_t code_v(float v, const BlockScale& b, uint32_t add) {
-  const float y = fminf(v * b.vinv, b.vtop);
-  const int c = static_cast<int>(__float_as_uint(y) + add - b.voff) >> 20;
-  return static_cast<uint32_t>(max(c, static_cast<int>(min(__float_as_uint(v), 1u))));
+// 1 if x is not zero.  (As a minimum: the compiler makes a compare and a
+// select of it.)
+__device__ __forceinline__ int nonzero(float x) {
+  int r;
+  asm("v_min_u32 %0, 1, %1" : "=v"(r) : "v"(x));
+  return r;
 }
 
-// Rounds eight elements to codes, of which `cnt` exist (the others are zero).
-// idx is the first one's index in the batch.
+// Rounds eight elements to codes (those that do not exist are zero).  idx is
+// the first one's index in the batch.
+//
+// Rounding adds to the 20 float32 mantissa bits that a code drops: 16 r + 8
+// (stochastic) or half of their range (nearest), then cuts.  For m,
+// v_cvt_sr_fp8_f32 does that with the upper 20 bits of its random operand,
+// subnormal codes included (checked against the addition written out, over
+// 4M values: equal in the normal range, and within 2^-20 of a code step of
+// the border below it).  The block's largest |m| and v are a few ulp off
+// their code's value at most, which neither rounding can carry to the next
+// code.
 template <bool STOCHASTIC>
 __device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8], uint32_t key, int64_t idx,
                                         uint2& mc, uint2& vc, float& ms, float& vs) {
@@ -182,40 +187,41 @@ __device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8]
   const BlockScale b = block_scale(mmax, vmax);
   ms = b.ms;
   vs = b.vs;
+  const uint32_t vadd = (STOCHASTIC ? 8u : 0x80000u) - b.voff;
   uint32_t hi = 0;
-  if constexpr (STOCHASTIC) hi = adam_mix(key + static_cast<uint32_t>(static_cast<uint64_t>(idx) >> 32));
-  float q[8];
+  if constexpr (STOCHASTIC)
+    hi = adam_mix(key + static_cast<uint32_t>(static_cast<uint64_t>(idx) >> 32)) + static_cast<uint32_t>(idx);
+  int q[2] = {0, 0};
   uint32_t c[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    uint32_t am = kNearestAdd, av = kNearestAdd;
+    uint32_t rm = 0x80000000u, t = __float_as_uint(v[e] * b.vinv) + vadd;
     if constexpr (STOCHASTIC) {
-      const uint32_t h = adam_mix(static_cast<uint32_t>(idx) + e + hi);
-      am = (h & 0xFFFFu) << 4 | 8u;
-      av = (h >> 16) << 4 | 8u;
+      const uint32_t h = adam_mix(hi + e);
+      rm = h << 16 | 0x8000u;
+      t = add_upper16(h, t);
     }
-    q[e] = round_m(m[e], b, am);
-    c[e] = code_v(v[e], b, av);
+    const float y = m[e] * b.minv;
+    int& w = q[e >> 2];
+    switch (e & 3) {
+      case 0: w = __builtin_amdgcn_cvt_sr_fp8_f32(y, rm, w, 0); break;
+      case 1: w = __builtin_amdgcn_cvt_sr_fp8_f32(y, rm, w, 1); break;
+      case 2: w = __builtin_amdgcn_cvt_sr_fp8_f32(y, rm, w, 2); break;
+      default: w = __builtin_amdgcn_cvt_sr_fp8_f32(y, rm, w, 3); break;
+    }
+    c[e] = static_cast<uint32_t>(max(static_cast<int>(t) >> 20, nonzero(v[e])));   // v > 0 has a code above 0
   }
+  mc = make_uint2(static_cast<uint32_t>(q[0]), static_cast<uint32_t>(q[1]));
   if (odd) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (mbad >> e & 1) q[e] = 0.0f;
+      const uint32_t byte = 0xFFu << (8 * (e & 3)), nan = 0x7Fu << (8 * (e & 3));
+      uint32_t& w = e < 4 ? mc.x : mc.y;
+      if (mbad >> e & 1) w = (w & ~byte) | nan;
       if (vbad >> e & 1) c[e] = 255;
     }
   }
-  int lo0 = 0, lo1 = 0;
-  lo0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], lo0, false);   // exact: q is an e4m3 value
-  lo0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo0, true);
-  lo1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], lo1, false);
-  lo1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], lo1, true);
-  mc = make_uint2(static_cast<uint32_t>(lo0), static_cast<uint32_t>(lo1));
   vc = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
-  if (odd) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (mbad >> e & 1) (e < 4 ? mc.x : mc.y) |= 0x7Fu << (8 * (e & 3));   // the code was zero
-  }
 }
 
 // Unscaled values of eight codes.
@@ -227,18 +233,23 @@ __device__ __forceinline__ void decode8(uint2 mc, uint2 vc, float (&m)[8], float
   const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(mc.y), true);
   m[0] = a.x; m[1] = a.y; m[2] = b.x; m[3] = b.y;
   m[4] = c.x; m[5] = c.y; m[6] = d.x; m[7] = d.y;
+  // u(c) has the bits (c << 20) + 768 << 20, but for c = 0 and 255, which few
+  // waves hold.  A zero byte of x has the upper bit of
+  // (x - 0x01010101) & ~x & 0x80808080 set, a byte 255 is one of ~x.
   const uint32_t w[2] = {vc.x, vc.y};
+  uint32_t rare = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t k = w[e >> 2] >> (8 * (e & 3)) & 0xFFu;
-    v[e] = k ? __uint_as_float((k << 20) + 0x30000000u) : 0.0f;
-  }
-  // A byte 255 (NaN): a zero byte of the complement.
-  const uint32_t nan = ((~w[0] - 0x01010101u) & w[0] & 0x80808080u) | ((~w[1] - 0x01010101u) & w[1] & 0x80808080u);
-  if (__any(nan != 0)) {
+  for (int k = 0; k < 2; ++k)
+    rare |= (((w[k] - 0x01010101u) & ~w[k]) | ((~w[k] - 0x01010101u) & w[k])) & 0x80808080u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if ((w[e >> 2] >> (8 * (e & 3)) & 0xFFu) == 255u) v[e] = __builtin_nanf("");
+  for (int e = 0; e < 8; ++e)
+    v[e] = __uint_as_float(((w[e >> 2] >> (8 * (e & 3)) & 0xFFu) << 20) + 0x30000000u);
+  if (__any(rare != 0)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t k = w[e >> 2] >> (8 * (e & 3)) & 0xFFu;
+      v[e] = k == 0 ? 0.0f : k == 255 ? __builtin_nanf("") : v[e];
+    }
   }
 }
 
@@ -246,22 +257,23 @@ __device__ __forceinline__ void decode8(uint2 mc, uint2 vc, float (&m)[8], float
 // One step
 // ---------------------------------------------------------------------------
 struct StepValues {
-  float b1, c1, b2, c2, eps, lr, rb1, rb2, gs;
+  float b1, b2, eps, lr, rb1, rb2;
+  float cm, cv;   // factors of the gradient in m, and of its square's root in v
   uint32_t key;
 };
 
 __device__ __forceinline__ StepValues step_values(const AdamArgs& a) {
   StepValues s;
   s.b1 = static_cast<float>(a.beta1);
-  s.c1 = static_cast<float>(1.0 - a.beta1);
   s.b2 = static_cast<float>(a.beta2);
-  s.c2 = static_cast<float>(1.0 - a.beta2);
   s.eps = a.eps;
   s.lr = a.ctl->lr;
   s.rb1 = a.ctl->rb1;
   s.rb2 = a.ctl->rb2;
   s.key = a.ctl->key;
-  s.gs = a.grad_scale ? *a.grad_scale : 1.0f;
+  const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+  s.cm = a.c1 * gs;
+  s.cv = a.root_c2 * gs;
   return s;
 }
 
@@ -271,9 +283,9 @@ __device__ __forceinline__ StepValues step_values(const AdamArgs& a) {
 // lr * weight_decay.  Square root and reciprocal are the 1 ulp instructions.
 __device__ __forceinline__ float update(const StepValues& s, float g, float w, float fm, float fv, float adam,
                                         float decay, float& m, float& v) {
-  const float y = g * s.gs;
-  m = fm * m + s.c1 * y;
-  v = fv * v + s.c2 * (y * y);
+  m = fm * m + s.cm * g;
+  const float z = s.cv * g;
+  v = fv * v + z * z;
   const float den = __builtin_amdgcn_sqrtf(v) * s.rb2 + s.eps;
   const float upd = (m * adam) * __builtin_amdgcn_rcpf(den);
   return w - (upd + decay * w);
