@@ -10,10 +10,13 @@
 
 namespace muon {
 
-// A tensor is worked on in pieces of kAdamPiece elements (a multiple of
-// ADAMW_BLOCK, so that a block of the 8-bit moments never spans two pieces).
+// Work is dealt in units of kAdamUnit elements of one tensor (256 threads of
+// eight elements; the last unit of a tensor may be shorter).  A unit is a
+// multiple of ADAMW_BLOCK, so a block of the 8-bit moments never spans two.
 constexpr int kAdamThreads = 256;
-constexpr int kAdamPiece = 4096;
+constexpr int kAdamUnit = 8 * kAdamThreads;
+constexpr int kAdamGrid = 1024;   // most workgroups of a step
+constexpr int kStateGrid = 2048;  // and of a pass over the moments
 
 // Per-tensor descriptor (uploaded once per batch into the workspace).
 struct alignas(16) AdamDesc {
@@ -30,9 +33,11 @@ struct alignas(16) AdamDesc {
   float weight_decay;
 };
 
-// One piece of a tensor.
-struct alignas(8) AdamPiece {
-  uint32_t tensor, piece;
+// One unit of work.  The whole units of all tensors come first, then the
+// tensors' short last ones.  Workgroup b takes units b, b + nwg, b + 2 nwg,
+// ...: the workgroups running at once stream through neighbouring memory.
+struct alignas(8) AdamUnit {
+  uint32_t tensor, unit;
 };
 
 // State of a plan's step sequence, in the workspace.  b1t, b2t and the values
@@ -45,14 +50,30 @@ struct alignas(16) AdamCtl {
   float rb1;              // 1 / (1 - beta1^t)
   float rb2;              // 1 / sqrt(1 - beta2^t)
   uint32_t key;           // key of the rounding hash for step t
-  uint32_t ticket;        // workgroups of the running step that have read the values above
+};
+
+// Counts the workgroups of a launch, to find the last one.  An agent-scope
+// add to one address takes about 14 ns whoever issues it (measured: 2048 of
+// them held a launch back by 25 us), so the workgroups are spread over groups
+// of kTicketGroup, each with a counter in a line of its own, and the last one
+// of a group counts the group.
+constexpr int kTicketGroup = 64;
+constexpr int kTicketGroups = 32;   // most groups: 2048 workgroups
+struct alignas(128) Ticket {
+  uint32_t count;
+};
+static_assert(kAdamGrid <= kTicketGroup * kTicketGroups, "more workgroups than tickets");
+struct Tickets {
+  Ticket group[kTicketGroups];
+  Ticket root;
 };
 
 struct AdamArgs {
   const AdamDesc* desc;
-  const AdamPiece* pieces;
-  int64_t npieces;
+  const AdamUnit* units;
+  uint32_t nunits, nwhole;   // all units, whole units
   AdamCtl* ctl;
+  Tickets* tickets;
   const float* grad_scale;  // or NULL
   double beta1, beta2;
   uint64_t seed;
@@ -84,6 +105,28 @@ __host__ __device__ inline uint32_t adam_key(uint64_t seed, int64_t t) {
   return adam_mix(static_cast<uint32_t>(seed) ^ k);
 }
 
+#if defined(__HIPCC__)
+// Adds this workgroup to its group; one thread calls it.  The counter's value
+// before says whether it is the group's last.
+__device__ __forceinline__ uint32_t ticket_take(Tickets* t) {
+  const uint32_t groups = (gridDim.x + kTicketGroup - 1) / kTicketGroup;
+  return __hip_atomic_fetch_add(&t->group[blockIdx.x % groups].count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Whether the workgroup that took `seen` is the launch's last.  The counters
+// are zero again after the last one's call.
+__device__ __forceinline__ bool ticket_last(Tickets* t, uint32_t seen) {
+  const uint32_t groups = (gridDim.x + kTicketGroup - 1) / kTicketGroup, mine = blockIdx.x % groups;
+  const uint32_t members = (gridDim.x - mine + groups - 1) / groups;
+  if (seen != members - 1) return false;
+  __hip_atomic_store(&t->group[mine].count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (__hip_atomic_fetch_add(&t->root.count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != groups - 1)
+    return false;
+  __hip_atomic_store(&t->root.count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return true;
+}
+#endif
+
 // Values of the step t = ctl.t, from b1t and b2t.
 __host__ __device__ inline void adam_derive(AdamCtl& c, uint64_t seed) {
   c.rb1 = static_cast<float>(1.0 / (1.0 - c.b1t));
@@ -102,6 +145,7 @@ hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;
 constexpr int kNormGrid = 2048;        // most workgroups of one launch
+static_assert(kNormGrid <= kTicketGroup * kTicketGroups, "more workgroups than tickets");
 constexpr int kNormUnitBytes = 8192;   // smallest share of work
 
 struct alignas(16) NormTensor {
@@ -124,7 +168,7 @@ struct NormArgs {
   const NormRun* runs;
   const uint32_t* first_run;   // per workgroup, nwg + 1 entries
   double* partial;             // one per run
-  uint32_t* ticket;
+  Tickets* tickets;
   float* out;
   float* tensor_norms;         // or NULL
   float max_norm;

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int64_t kMaxTensors = int64_t{1} << 20;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
-constexpr int64_t kMaxPieces = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxUnits = (int64_t{1} << 32) - 1 - kStateGrid;
 
 // Makes a plan's device current for one call.
 struct DeviceGuard {
@@ -82,10 +82,10 @@ muon_status_t add_buffer(std::vector<Range>& rs, int64_t i, const void* p, size_
 // ---------------------------------------------------------------------------
 struct AdamTable {
   std::vector<AdamDesc> desc;
-  std::vector<AdamPiece> pieces;
-  int64_t npieces = 0, elems = 0;
+  std::vector<AdamUnit> units;
+  int64_t nunits = 0, nwhole = 0, elems = 0;
   bool has_master = false;
-  size_t desc_off = 0, piece_off = 0, bytes = 0;
+  size_t ticket_off = 0, desc_off = 0, unit_off = 0, bytes = 0;
   std::vector<Range> buffers;
 };
 
@@ -125,13 +125,15 @@ muon_status_t adam_layout(const adamw_tensor_t* ts, int64_t count, AdamTable& t)
   muon_status_t st;
   if ((st = check_count(ts, count)) != MUON_OK) return st;
   for (int64_t i = 0; i < count; ++i) {
-    t.npieces += ceil_div(ts[i].n, kAdamPiece);
+    t.nunits += ceil_div(ts[i].n, kAdamUnit);
+    t.nwhole += ts[i].n / kAdamUnit;
     t.elems += round_up(ts[i].n, ADAMW_BLOCK);
-    if (t.npieces > kMaxPieces) return fail(MUON_ERR_UNSUPPORTED, "the batch is too large");
   }
-  t.desc_off = round_up(sizeof(AdamCtl), kAlign);
-  t.piece_off = round_up(t.desc_off + sizeof(AdamDesc) * count, kAlign);
-  t.bytes = round_up(t.piece_off + sizeof(AdamPiece) * t.npieces, kAlign);
+  if (t.nunits > kMaxUnits) return fail(MUON_ERR_UNSUPPORTED, "the batch is too large");
+  t.ticket_off = round_up(sizeof(AdamCtl), kAlign);
+  t.desc_off = round_up(t.ticket_off + sizeof(Tickets), kAlign);
+  t.unit_off = round_up(t.desc_off + sizeof(AdamDesc) * count, kAlign);
+  t.bytes = round_up(t.unit_off + sizeof(AdamUnit) * t.nunits, kAlign);
   return MUON_OK;
 }
 
@@ -142,18 +144,18 @@ muon_status_t adam_prepare(const adamw_tensor_t* ts, int64_t count, const adamw_
   if ((st = adam_layout(ts, count, t)) != MUON_OK) return st;
   const bool block8 = cfg->state == ADAMW_STATE_BLOCK8;
   const size_t wsz = dtype_size(cfg->w_dtype), gsz = dtype_size(cfg->g_dtype), ssz = block8 ? 1 : 4;
-  t.desc.resize(count);
-  t.pieces.reserve(t.npieces);
   t.buffers.reserve(count * 7 + 1);
+  t.desc.resize(count);
+  t.units.reserve(t.nunits);
   int64_t first = 0;
   bool any = false;
   for (int64_t i = 0; i < count; ++i) {
     const adamw_tensor_t& x = ts[i];
     if (!finite(x.lr_scale) || !finite(x.weight_decay))
       return fail(MUON_ERR_INVALID_ARG, "tensor %lld: lr_scale and weight_decay must be finite", (long long)i);
-    AdamDesc& d = t.desc[i];
-    d = AdamDesc{x.w, x.g, x.m, x.v, x.m_scale, x.v_scale, x.master, x.n, first, x.lr_scale, x.weight_decay};
+    t.desc[i] = AdamDesc{x.w, x.g, x.m, x.v, x.m_scale, x.v_scale, x.master, x.n, first, x.lr_scale, x.weight_decay};
     first += round_up(x.n, ADAMW_BLOCK);
+    for (int64_t u = 0; u < x.n / kAdamUnit; ++u) t.units.push_back({static_cast<uint32_t>(i), static_cast<uint32_t>(u)});
     if (x.n == 0) continue;
     const size_t n = static_cast<size_t>(x.n), blocks = ceil_div(x.n, ADAMW_BLOCK);
     if ((st = add_buffer(t.buffers, i, x.w, n * wsz, 16, "w", true)) != MUON_OK ||
@@ -172,9 +174,10 @@ muon_status_t adam_prepare(const adamw_tensor_t* ts, int64_t count, const adamw_
     t.has_master = master;
     any = true;
     if (master && (st = add_buffer(t.buffers, i, x.master, n * 4, 16, "master", true)) != MUON_OK) return st;
-    for (int64_t p = 0; p < ceil_div(x.n, kAdamPiece); ++p)
-      t.pieces.push_back({static_cast<uint32_t>(i), static_cast<uint32_t>(p)});
   }
+  for (int64_t i = 0; i < count; ++i)
+    if (ts[i].n % kAdamUnit)
+      t.units.push_back({static_cast<uint32_t>(i), static_cast<uint32_t>(ts[i].n / kAdamUnit)});
   if (cfg->grad_scale) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(cfg->grad_scale);
     t.buffers.push_back({lo, lo + 4, 0, "grad_scale", false});
@@ -191,7 +194,7 @@ muon_status_t adam_prepare(const adamw_tensor_t* ts, int64_t count, const adamw_
   table.assign(t.bytes, 0);
   std::memcpy(table.data(), &ctl, sizeof(ctl));
   std::memcpy(table.data() + t.desc_off, t.desc.data(), sizeof(AdamDesc) * count);
-  if (t.npieces) std::memcpy(table.data() + t.piece_off, t.pieces.data(), sizeof(AdamPiece) * t.npieces);
+  if (t.nunits) std::memcpy(table.data() + t.unit_off, t.units.data(), sizeof(AdamUnit) * t.nunits);
   return MUON_OK;
 }
 
@@ -199,9 +202,11 @@ AdamArgs adam_args(const AdamTable& t, const adamw_config_t& cfg, void* ws) {
   char* base = static_cast<char*>(ws);
   AdamArgs a{};
   a.desc = reinterpret_cast<const AdamDesc*>(base + t.desc_off);
-  a.pieces = reinterpret_cast<const AdamPiece*>(base + t.piece_off);
-  a.npieces = t.npieces;
+  a.units = reinterpret_cast<const AdamUnit*>(base + t.unit_off);
+  a.nunits = static_cast<uint32_t>(t.nunits);
+  a.nwhole = static_cast<uint32_t>(t.nwhole);
   a.ctl = reinterpret_cast<AdamCtl*>(base);
+  a.tickets = reinterpret_cast<Tickets*>(base + t.ticket_off);
   a.grad_scale = cfg.grad_scale;
   a.beta1 = cfg.beta1;
   a.beta2 = cfg.beta2;
@@ -272,7 +277,7 @@ muon_status_t norm_layout(const muon_grad_t* gs, int64_t count, NormTable& t) {
   }
   t.tensors[count] = NormTensor{nullptr, 0, 0, static_cast<uint32_t>(t.runs.size())};
   t.first_run.push_back(static_cast<uint32_t>(t.runs.size()));
-  t.tensor_off = kAlign;   // the first 256 bytes hold the ticket
+  t.tensor_off = round_up(sizeof(Tickets), kAlign);   // the tickets come first
   t.run_off = round_up(t.tensor_off + sizeof(NormTensor) * t.tensors.size(), kAlign);
   t.first_off = round_up(t.run_off + sizeof(NormRun) * t.runs.size(), kAlign);
   t.table_bytes = round_up(t.first_off + sizeof(uint32_t) * t.first_run.size(), kAlign);
@@ -315,7 +320,7 @@ NormArgs norm_args(const NormTable& t, float max_norm, float* out, float* tensor
   a.runs = reinterpret_cast<const NormRun*>(base + t.run_off);
   a.first_run = reinterpret_cast<const uint32_t*>(base + t.first_off);
   a.partial = reinterpret_cast<double*>(base + t.partial_off);
-  a.ticket = reinterpret_cast<uint32_t*>(base);
+  a.tickets = reinterpret_cast<Tickets*>(base);
   a.out = out;
   a.tensor_norms = tensor_norms;
   a.max_norm = max_norm;

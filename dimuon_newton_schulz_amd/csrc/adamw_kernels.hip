@@ -1,90 +1,144 @@
 // AdamW over many tensors: the step with 32- and 8-bit moments, and the
 // moments as values.
+#include <algorithm>
+
 #include "adamw.h"
 
 namespace muon {
 namespace {
 
-// A workgroup walks pieces blockIdx.x, blockIdx.x + gridDim.x, ...; the
-// workgroups running at once stream through neighbouring memory.
-constexpr int kGrid32 = 2048, kGrid8 = 2048, kGridState = 2048;
+// ---------------------------------------------------------------------------
+// Eight consecutive elements per thread, raw as loaded: 16 bytes of bf16 or 32
+// of float32, eight code bytes.  p is the unit's base (the same for the whole
+// workgroup) and `lane` the thread in it.  In a unit that is not WHOLE, only
+// `cnt` of the eight exist; the others read as zero and are not written.
+// ---------------------------------------------------------------------------
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// ---------------------------------------------------------------------------
-// Groups of N consecutive elements, element index a multiple of N and the
-// base 16-byte aligned; `cnt` of them exist (the others read as zero and are
-// not written).
-// ---------------------------------------------------------------------------
-template <bool BF16, int N>
-__device__ __forceinline__ void load_group(const void* p, int64_t i, int cnt, float (&out)[N]) {
-  if (cnt >= N) {
-#pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      float t[4];
-      if constexpr (BF16 && N == 8) {
-        if (e != 0) continue;
-        const uint4 u = *reinterpret_cast<const MUON_GLOBAL uint4*>(gmem(static_cast<const uint16_t*>(p)) + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          out[2 * k] = __uint_as_float(w[k] << 16);
-          out[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
-      } else {
-        load4_aligned(p, i + e, BF16 ? DT_BF16 : DT_F32, t);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[e + k] = t[k];
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < N; ++e) out[e] = e < cnt ? load_elem(p, i + e, BF16 ? DT_BF16 : DT_F32) : 0.0f;
+template <typename V>
+__device__ __forceinline__ V load_vec(const void* p, int k) {
+  return reinterpret_cast<const MUON_GLOBAL V*>(gmem(static_cast<const char*>(p)))[k];
 }
 
-template <bool BF16, int N>
-__device__ __forceinline__ void store_group(void* p, int64_t i, int cnt, const float (&v)[N]) {
-  if (cnt >= N) {
-    if constexpr (BF16 && N == 8) {
-      uint4 u;
-      u.x = pack_bf16x2(v[0], v[1]);
-      u.y = pack_bf16x2(v[2], v[3]);
-      u.z = pack_bf16x2(v[4], v[5]);
-      u.w = pack_bf16x2(v[6], v[7]);
-      *reinterpret_cast<MUON_GLOBAL uint4*>(gmem(static_cast<uint16_t*>(p)) + i) = u;
+template <typename V>
+__device__ __forceinline__ void store_vec(void* p, int k, V v) {
+  reinterpret_cast<MUON_GLOBAL V*>(gmem(static_cast<char*>(p)))[k] = v;
+}
+
+template <bool BF16>
+struct Raw8;
+template <>
+struct Raw8<true> {
+  u32x4 a;
+};
+template <>
+struct Raw8<false> {
+  u32x4 a, b;
+};
+
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ Raw8<BF16> load8(const void* p, int lane, int cnt) {
+  Raw8<BF16> r;
+  if (WHOLE || cnt == 8) {
+    if constexpr (BF16) {
+      r.a = load_vec<u32x4>(p, lane);
     } else {
+      r.a = load_vec<u32x4>(p, 2 * lane);
+      r.b = load_vec<u32x4>(p, 2 * lane + 1);
+    }
+    return r;
+  }
+  uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < N; e += 4) {
-        const float t[4] = {v[e], v[e + 1], v[e + 2], v[e + 3]};
-        store4_aligned(p, i + e, BF16 ? DT_BF16 : DT_F32, t);
+  for (int e = 0; e < 8; ++e) {
+    w[e] = 0;
+    if (e >= cnt) continue;
+    if constexpr (BF16) w[e] = gmem(static_cast<const uint16_t*>(p))[8 * lane + e];
+    else w[e] = gmem(static_cast<const uint32_t*>(p))[8 * lane + e];
+  }
+  if constexpr (BF16) {
+    r.a = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+  } else {
+    r.a = u32x4{w[0], w[1], w[2], w[3]};
+    r.b = u32x4{w[4], w[5], w[6], w[7]};
+  }
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void floats8(const Raw8<BF16>& r, float (&out)[8]) {
+  if constexpr (BF16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      out[2 * k] = __uint_as_float(r.a[k] << 16);
+      out[2 * k + 1] = __uint_as_float(r.a[k] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      out[k] = __uint_as_float(r.a[k]);
+      out[4 + k] = __uint_as_float(r.b[k]);
+    }
+  }
+}
+
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void store8(void* p, int lane, int cnt, const float (&v)[8]) {
+  if (WHOLE || cnt == 8) {
+    if constexpr (BF16) {
+      store_vec(p, lane, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7])});
+    } else {
+      u32x4 a, b;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[k] = __float_as_uint(v[k]);
+        b[k] = __float_as_uint(v[4 + k]);
       }
+      store_vec(p, 2 * lane, a);
+      store_vec(p, 2 * lane + 1, b);
     }
     return;
   }
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (e < cnt) store_elem(p, i + e, BF16 ? DT_BF16 : DT_F32, v[e]);
+  for (int e = 0; e < 8; ++e)
+    if (e < cnt) store_elem(p, 8 * lane + e, BF16 ? DT_BF16 : DT_F32, v[e]);
 }
 
-__device__ __forceinline__ uint2 load_codes(const void* p, int64_t i, int cnt) {
-  const MUON_GLOBAL uint8_t* q = gmem(static_cast<const uint8_t*>(p)) + i;
-  if (cnt >= 8) return *reinterpret_cast<const MUON_GLOBAL uint2*>(q);
-  uint32_t w[2] = {0, 0};
+template <bool WHOLE>
+__device__ __forceinline__ u32x2 load_codes(const void* p, int lane, int cnt) {
+  if (WHOLE || cnt == 8) return load_vec<u32x2>(p, lane);
+  u32x2 w = {0, 0};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (e < cnt) w[e >> 2] |= static_cast<uint32_t>(q[e]) << (8 * (e & 3));
-  return make_uint2(w[0], w[1]);
+    if (e < cnt) w[e >> 2] |= static_cast<uint32_t>(gmem(static_cast<const uint8_t*>(p))[8 * lane + e]) << (8 * (e & 3));
+  return w;
 }
 
-__device__ __forceinline__ void store_codes(void* p, int64_t i, int cnt, uint2 c) {
-  MUON_GLOBAL uint8_t* q = gmem(static_cast<uint8_t*>(p)) + i;
-  if (cnt >= 8) {
-    *reinterpret_cast<MUON_GLOBAL uint2*>(q) = c;
+template <bool WHOLE>
+__device__ __forceinline__ void store_codes(void* p, int lane, int cnt, u32x2 c) {
+  if (WHOLE || cnt == 8) {
+    store_vec(p, lane, c);
     return;
   }
-  const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (e < cnt) q[e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+    if (e < cnt) gmem(static_cast<uint8_t*>(p))[8 * lane + e] = static_cast<uint8_t>(c[e >> 2] >> (8 * (e & 3)));
+}
+
+// Elements of this thread in a unit of `left` elements.
+__device__ __forceinline__ int count_of(int left) {
+  const int k = left - 8 * static_cast<int>(threadIdx.x);
+  return k < 0 ? 0 : k > 8 ? 8 : k;
+}
+
+// Address of unit u of a run.
+__device__ __forceinline__ void* at_unit(void* p, int64_t u, int size) {
+  return static_cast<char*>(p) + u * kAdamUnit * size;
+}
+__device__ __forceinline__ const void* at_unit(const void* p, int64_t u, int size) {
+  return static_cast<const char*>(p) + u * kAdamUnit * size;
 }
 
 // ---------------------------------------------------------------------------
@@ -146,8 +200,8 @@ __device__ __forceinline__ int nonzero(float x) {
   return r;
 }
 
-// Rounds eight elements to codes (those that do not exist are zero).  idx is
-// the first one's index in the batch.
+// Rounds eight elements to codes (those that do not exist are zero).  `hash0`
+// is what the first one's hash mixes; the next ones follow it.
 //
 // Rounding adds to the 20 float32 mantissa bits that a code drops: 16 r + 8
 // (stochastic) or half of their range (nearest), then cuts.  For m,
@@ -158,8 +212,8 @@ __device__ __forceinline__ int nonzero(float x) {
 // their code's value at most, which neither rounding can carry to the next
 // code.
 template <bool STOCHASTIC>
-__device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8], uint32_t key, int64_t idx,
-                                        uint2& mc, uint2& vc, float& ms, float& vs) {
+__device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8], uint32_t hash0, u32x2& mc,
+                                        u32x2& vc, float& ms, float& vs) {
   uint32_t mmax = 0, vmax = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -188,16 +242,13 @@ __device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8]
   ms = b.ms;
   vs = b.vs;
   const uint32_t vadd = (STOCHASTIC ? 8u : 0x80000u) - b.voff;
-  uint32_t hi = 0;
-  if constexpr (STOCHASTIC)
-    hi = adam_mix(key + static_cast<uint32_t>(static_cast<uint64_t>(idx) >> 32)) + static_cast<uint32_t>(idx);
   int q[2] = {0, 0};
   uint32_t c[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     uint32_t rm = 0x80000000u, t = __float_as_uint(v[e] * b.vinv) + vadd;
     if constexpr (STOCHASTIC) {
-      const uint32_t h = adam_mix(hi + e);
+      const uint32_t h = adam_mix(hash0 + e);
       rm = h << 16 | 0x8000u;
       t = add_upper16(h, t);
     }
@@ -211,21 +262,20 @@ __device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8]
     }
     c[e] = static_cast<uint32_t>(max(static_cast<int>(t) >> 20, nonzero(v[e])));   // v > 0 has a code above 0
   }
-  mc = make_uint2(static_cast<uint32_t>(q[0]), static_cast<uint32_t>(q[1]));
+  mc = u32x2{static_cast<uint32_t>(q[0]), static_cast<uint32_t>(q[1])};
   if (odd) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint32_t byte = 0xFFu << (8 * (e & 3)), nan = 0x7Fu << (8 * (e & 3));
-      uint32_t& w = e < 4 ? mc.x : mc.y;
-      if (mbad >> e & 1) w = (w & ~byte) | nan;
+      if (mbad >> e & 1) mc[e >> 2] = (mc[e >> 2] & ~byte) | nan;
       if (vbad >> e & 1) c[e] = 255;
     }
   }
-  vc = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+  vc = u32x2{c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
 }
 
 // Unscaled values of eight codes.
-__device__ __forceinline__ void decode8(uint2 mc, uint2 vc, float (&m)[8], float (&v)[8]) {
+__device__ __forceinline__ void decode8(u32x2 mc, u32x2 vc, float (&m)[8], float (&v)[8]) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(mc.x), false);
   const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(mc.x), true);
@@ -291,126 +341,182 @@ __device__ __forceinline__ float update(const StepValues& s, float g, float w, f
   return w - (upd + decay * w);
 }
 
-// The last workgroup to have read the step's values writes the next step's.
-__device__ __forceinline__ void finish_step(const AdamArgs& a, bool advance) {
+// Called by every thread once it holds the step's values: counts the
+// workgroups that do (the count is looked at after the step's work).
+__device__ __forceinline__ uint32_t have_values(const AdamArgs& a) {
   __syncthreads();
-  if (!advance || threadIdx.x != 0) return;
-  const uint32_t seen = __hip_atomic_fetch_add(&a.ctl->ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (seen != gridDim.x - 1) return;
+  return threadIdx.x == 0 ? ticket_take(a.tickets) : 0;
+}
+
+// The last workgroup to have read the step's values writes the next step's.
+__device__ __forceinline__ void advance_step(const AdamArgs& a, uint32_t seen) {
+  if (threadIdx.x != 0 || !ticket_last(a.tickets, seen)) return;
   AdamCtl c = *a.ctl;
   c.t += 1;
   c.b1t *= a.beta1;
   c.b2t *= a.beta2;
-  c.ticket = 0;
   adam_derive(c, a.seed);
   *a.ctl = c;
 }
 
-// Elements of the group of N from `i` on that lie below n.
-template <bool FULL, int N>
-__device__ __forceinline__ int count_of(int64_t i, int64_t n) {
-  if constexpr (FULL) return N;
-  const int64_t k = n - i;
-  return k < 0 ? 0 : k > N ? N : static_cast<int>(k);
+// One unit's operands as loaded.  The next unit's are loaded before this
+// one's results are stored: loads and stores share one in-order counter, so
+// a load issued behind a store would wait for it.
+template <bool WB, bool GB, bool MASTER>
+struct Unit32 {
+  Raw8<GB> g;
+  Raw8<WB && !MASTER> w;
+  Raw8<false> m, v;
+};
+
+template <bool WB, bool GB, bool MASTER, bool WHOLE>
+__device__ __forceinline__ Unit32<WB, GB, MASTER> load_unit32(const AdamDesc& d, int64_t u, int left) {
+  const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
+  Unit32<WB, GB, MASTER> x;
+  x.g = load8<GB, WHOLE>(at_unit(d.g, u, GB ? 2 : 4), lane, cnt);
+  if constexpr (MASTER) x.w = load8<false, WHOLE>(at_unit(d.master, u, 4), lane, cnt);
+  else x.w = load8<WB, WHOLE>(at_unit(d.w, u, WB ? 2 : 4), lane, cnt);
+  x.m = load8<false, WHOLE>(at_unit(d.m, u, 4), lane, cnt);
+  x.v = load8<false, WHOLE>(at_unit(d.v, u, 4), lane, cnt);
+  return x;
 }
 
-// 32-bit moments.  Four groups of four elements per thread and piece (FULL:
-// the piece is whole, and no access is guarded).
-template <bool WB, bool GB, bool MASTER, bool FULL>
-__device__ __forceinline__ void piece32(const StepValues& s, const AdamDesc& d, int64_t base) {
-  constexpr int G = kAdamPiece / (4 * kAdamThreads);
+template <bool WB, bool GB, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void step_unit32(const StepValues& s, const AdamDesc& d, int64_t u, int left,
+                                            const Unit32<WB, GB, MASTER>& x) {
+  const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
   const float adam = s.lr * d.lr_scale * s.rb1, decay = s.lr * d.weight_decay;
-  float g[G][4], w[G][4], m[G][4], v[G][4];
-  int cnt[G];
+  float g[8], w[8], m[8], v[8];
+  floats8(x.g, g);
+  floats8(x.w, w);
+  floats8(x.m, m);
+  floats8(x.v, v);
 #pragma unroll
-  for (int j = 0; j < G; ++j) {
-    const int64_t i = base + j * 4 * kAdamThreads;
-    cnt[j] = count_of<FULL, 4>(i, d.n);
-    load_group<GB>(d.g, i, cnt[j], g[j]);
-    load_group<false>(d.m, i, cnt[j], m[j]);
-    load_group<false>(d.v, i, cnt[j], v[j]);
-    if constexpr (MASTER) load_group<false>(d.master, i, cnt[j], w[j]);
-    else load_group<WB>(d.w, i, cnt[j], w[j]);
+  for (int e = 0; e < 8; ++e) w[e] = update(s, g[e], w[e], s.b1, s.b2, adam, decay, m[e], v[e]);
+  if constexpr (MASTER) store8<false, WHOLE>(at_unit(d.master, u, 4), lane, cnt, w);
+  store8<WB, WHOLE>(at_unit(d.w, u, WB ? 2 : 4), lane, cnt, w);
+  store8<false, WHOLE>(at_unit(d.m, u, 4), lane, cnt, m);
+  store8<false, WHOLE>(at_unit(d.v, u, 4), lane, cnt, v);
+}
+
+// Walks this workgroup's units: the operands of the next whole unit are loaded
+// before step() stores the current one's results.
+template <typename LoadWhole, typename StepWhole, typename Short>
+__device__ __forceinline__ void walk_units(const AdamArgs& a, LoadWhole load, StepWhole step, Short short_unit) {
+  uint32_t k = blockIdx.x;
+  if (k < a.nwhole) {
+    AdamUnit u = a.units[k];
+    AdamDesc d = a.desc[u.tensor];
+    auto x = load(d, u.unit);
+    for (;;) {
+      k += gridDim.x;
+      if (k >= a.nwhole) break;
+      const AdamUnit u1 = a.units[k];
+      const AdamDesc d1 = a.desc[u1.tensor];
+      const auto y = load(d1, u1.unit);
+      step(d, u.unit, x);
+      u = u1;
+      d = d1;
+      x = y;
+    }
+    step(d, u.unit, x);
   }
-#pragma unroll
-  for (int j = 0; j < G; ++j) {
-    const int64_t i = base + j * 4 * kAdamThreads;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[j][e] = update(s, g[j][e], w[j][e], s.b1, s.b2, adam, decay, m[j][e], v[j][e]);
-    store_group<false>(d.m, i, cnt[j], m[j]);
-    store_group<false>(d.v, i, cnt[j], v[j]);
-    if constexpr (MASTER) store_group<false>(d.master, i, cnt[j], w[j]);
-    store_group<WB>(d.w, i, cnt[j], w[j]);
+  for (; k < a.nunits; k += gridDim.x) {
+    const AdamUnit u = a.units[k];
+    const AdamDesc& d = a.desc[u.tensor];
+    short_unit(d, u.unit, static_cast<int>(d.n - static_cast<int64_t>(u.unit) * kAdamUnit));
   }
 }
 
 template <bool WB, bool GB, bool MASTER>
 __global__ __launch_bounds__(kAdamThreads) void k_adamw32(AdamArgs a, bool advance) {
   const StepValues s = step_values(a);
-  for (int64_t p = blockIdx.x; p < a.npieces; p += gridDim.x) {
-    const AdamPiece pc = a.pieces[p];
-    const AdamDesc& d = a.desc[pc.tensor];
-    const int64_t at = static_cast<int64_t>(pc.piece) * kAdamPiece;
-    if (d.n - at >= kAdamPiece) piece32<WB, GB, MASTER, true>(s, d, at + 4 * threadIdx.x);
-    else piece32<WB, GB, MASTER, false>(s, d, at + 4 * threadIdx.x);
-  }
-  finish_step(a, advance);
+  const uint32_t seen = have_values(a);
+  typedef Unit32<WB, GB, MASTER> Unit;
+  walk_units(
+      a, [&](const AdamDesc& d, int64_t u) { return load_unit32<WB, GB, MASTER, true>(d, u, kAdamUnit); },
+      [&](const AdamDesc& d, int64_t u, const Unit& x) { step_unit32<WB, GB, MASTER, true>(s, d, u, kAdamUnit, x); },
+      [&](const AdamDesc& d, int64_t u, int left) {
+        step_unit32<WB, GB, MASTER, false>(s, d, u, left, load_unit32<WB, GB, MASTER, false>(d, u, left));
+      });
+  if (advance) advance_step(a, seen);
 }
 
-// 8-bit moments.  Two groups of eight elements per thread and piece.
-template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, bool FULL>
-__device__ __forceinline__ void piece8(const StepValues& s, const AdamDesc& d, int64_t base) {
-  constexpr int G = kAdamPiece / (8 * kAdamThreads);
+template <bool WB, bool GB, bool MASTER>
+struct Unit8 {
+  Raw8<GB> g;
+  Raw8<WB && !MASTER> w;
+  u32x2 m, v;
+  float ms, vs;
+};
+
+template <bool WB, bool GB, bool MASTER, bool WHOLE>
+__device__ __forceinline__ Unit8<WB, GB, MASTER> load_unit8(const AdamDesc& d, int64_t u, int left) {
+  const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
+  constexpr int kBlocks = kAdamUnit / ADAMW_BLOCK;
+  Unit8<WB, GB, MASTER> x;
+  x.g = load8<GB, WHOLE>(at_unit(d.g, u, GB ? 2 : 4), lane, cnt);
+  if constexpr (MASTER) x.w = load8<false, WHOLE>(at_unit(d.master, u, 4), lane, cnt);
+  else x.w = load8<WB, WHOLE>(at_unit(d.w, u, WB ? 2 : 4), lane, cnt);
+  x.m = load_codes<WHOLE>(at_unit(d.m, u, 1), lane, cnt);
+  x.v = load_codes<WHOLE>(at_unit(d.v, u, 1), lane, cnt);
+  // A lane without elements takes the scale of the tensor's last block.
+  const int blk = (WHOLE || cnt > 0 ? 8 * lane : left - 1) / ADAMW_BLOCK;
+  x.ms = gmem(d.m_scale + u * kBlocks)[blk];
+  x.vs = gmem(d.v_scale + u * kBlocks)[blk];
+  return x;
+}
+
+// What the hash of this thread's first element of unit u mixes.
+__device__ __forceinline__ uint32_t hash_base(const StepValues& s, const AdamDesc& d, int64_t u) {
+  const uint64_t at = static_cast<uint64_t>(d.first + u * kAdamUnit);
+  const uint32_t lo = static_cast<uint32_t>(at), hi = static_cast<uint32_t>(at >> 32);
+  uint32_t k = adam_mix(s.key + hi);   // the same for the whole unit, unless it passes a multiple of 2^32
+  const uint32_t mine = lo + 8 * threadIdx.x;
+  if (lo > 0xFFFFFFFFu - kAdamUnit && mine < lo) k = adam_mix(s.key + hi + 1);
+  return mine + k;
+}
+
+template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, bool WHOLE>
+__device__ __forceinline__ void step_unit8(const StepValues& s, const AdamDesc& d, int64_t u, int left,
+                                           const Unit8<WB, GB, MASTER>& x) {
+  const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
+  constexpr int kBlocks = kAdamUnit / ADAMW_BLOCK;
   const float adam = s.lr * d.lr_scale * s.rb1, decay = s.lr * d.weight_decay;
-  float g[G][8], w[G][8], ms[G], vs[G];
-  uint2 mc[G], vc[G];
-  int cnt[G];
+  float g[8], w[8], m[8], v[8];
+  floats8(x.g, g);
+  floats8(x.w, w);
+  decode8(x.m, x.v, m, v);
+  const float fm = s.b1 * x.ms, fv = s.b2 * x.vs;
 #pragma unroll
-  for (int j = 0; j < G; ++j) {
-    const int64_t i = base + j * 8 * kAdamThreads;
-    cnt[j] = count_of<FULL, 8>(i, d.n);
-    // Lanes of a block without elements read the scale of the last block.
-    const int64_t blk = (cnt[j] > 0 ? i : d.n - 1) / ADAMW_BLOCK;
-    ms[j] = gmem(d.m_scale)[blk];
-    vs[j] = gmem(d.v_scale)[blk];
-    mc[j] = load_codes(d.m, i, cnt[j]);
-    vc[j] = load_codes(d.v, i, cnt[j]);
-    load_group<GB>(d.g, i, cnt[j], g[j]);
-    if constexpr (MASTER) load_group<false>(d.master, i, cnt[j], w[j]);
-    else load_group<WB>(d.w, i, cnt[j], w[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < G; ++j) {
-    const int64_t i = base + j * 8 * kAdamThreads;
-    float m[8], v[8];
-    decode8(mc[j], vc[j], m, v);
-    const float fm = s.b1 * ms[j], fv = s.b2 * vs[j];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[j][e] = update(s, g[j][e], w[j][e], fm, fv, adam, decay, m[e], v[e]);
-    if constexpr (MASTER) store_group<false>(d.master, i, cnt[j], w[j]);
-    store_group<WB>(d.w, i, cnt[j], w[j]);
-    float ms1, vs1;
-    encode8<STOCHASTIC>(m, v, s.key, d.first + i, mc[j], vc[j], ms1, vs1);
-    store_codes(d.m, i, cnt[j], mc[j]);
-    store_codes(d.v, i, cnt[j], vc[j]);
-    if ((threadIdx.x & 31) == 0 && cnt[j] > 0) {
-      gmem(d.m_scale)[i / ADAMW_BLOCK] = ms1;
-      gmem(d.v_scale)[i / ADAMW_BLOCK] = vs1;
-    }
+  for (int e = 0; e < 8; ++e) w[e] = update(s, g[e], w[e], fm, fv, adam, decay, m[e], v[e]);
+  if constexpr (MASTER) store8<false, WHOLE>(at_unit(d.master, u, 4), lane, cnt, w);
+  store8<WB, WHOLE>(at_unit(d.w, u, WB ? 2 : 4), lane, cnt, w);
+  u32x2 mc, vc;
+  float ms, vs;
+  encode8<STOCHASTIC>(m, v, STOCHASTIC ? hash_base(s, d, u) : 0, mc, vc, ms, vs);
+  store_codes<WHOLE>(at_unit(d.m, u, 1), lane, cnt, mc);
+  store_codes<WHOLE>(at_unit(d.v, u, 1), lane, cnt, vc);
+  if ((lane & 31) == 0 && (WHOLE || cnt > 0)) {
+    gmem(d.m_scale + u * kBlocks)[lane >> 5] = ms;
+    gmem(d.v_scale + u * kBlocks)[lane >> 5] = vs;
   }
 }
 
 template <bool WB, bool GB, bool MASTER, bool STOCHASTIC>
 __global__ __launch_bounds__(kAdamThreads) void k_adamw8(AdamArgs a, bool advance) {
   const StepValues s = step_values(a);
-  for (int64_t p = blockIdx.x; p < a.npieces; p += gridDim.x) {
-    const AdamPiece pc = a.pieces[p];
-    const AdamDesc& d = a.desc[pc.tensor];
-    const int64_t at = static_cast<int64_t>(pc.piece) * kAdamPiece;
-    if (d.n - at >= kAdamPiece) piece8<WB, GB, MASTER, STOCHASTIC, true>(s, d, at + 8 * threadIdx.x);
-    else piece8<WB, GB, MASTER, STOCHASTIC, false>(s, d, at + 8 * threadIdx.x);
-  }
-  finish_step(a, advance);
+  const uint32_t seen = have_values(a);
+  typedef Unit8<WB, GB, MASTER> Unit;
+  walk_units(
+      a, [&](const AdamDesc& d, int64_t u) { return load_unit8<WB, GB, MASTER, true>(d, u, kAdamUnit); },
+      [&](const AdamDesc& d, int64_t u, const Unit& x) {
+        step_unit8<WB, GB, MASTER, STOCHASTIC, true>(s, d, u, kAdamUnit, x);
+      },
+      [&](const AdamDesc& d, int64_t u, int left) {
+        step_unit8<WB, GB, MASTER, STOCHASTIC, false>(s, d, u, left, load_unit8<WB, GB, MASTER, false>(d, u, left));
+      });
+  if (advance) advance_step(a, seen);
 }
 
 __global__ void k_ctl(AdamCtl* ctl, AdamCtl value, bool set_step) {
@@ -429,101 +535,100 @@ __global__ void k_ctl(AdamCtl* ctl, AdamCtl value, bool set_step) {
 // ---------------------------------------------------------------------------
 // The moments as values
 // ---------------------------------------------------------------------------
-template <bool BLOCK8, bool BF16, bool FULL>
-__device__ __forceinline__ void piece_get(const AdamDesc& d, int64_t base, void* m_out, void* v_out) {
+template <bool BLOCK8, bool BF16, bool WHOLE>
+__device__ __forceinline__ void get_unit(const AdamDesc& d, int64_t u, int left, void* m_out, void* v_out) {
+  const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
+  constexpr int kBlocks = kAdamUnit / ADAMW_BLOCK, size = BF16 ? 2 : 4;
+  float m[8], v[8];
+  if constexpr (BLOCK8) {
+    const int blk = (WHOLE || cnt > 0 ? 8 * lane : left - 1) / ADAMW_BLOCK;
+    const float ms = gmem(d.m_scale + u * kBlocks)[blk], vs = gmem(d.v_scale + u * kBlocks)[blk];
+    decode8(load_codes<WHOLE>(at_unit(d.m, u, 1), lane, cnt), load_codes<WHOLE>(at_unit(d.v, u, 1), lane, cnt), m, v);
 #pragma unroll
-  for (int j = 0; j < kAdamPiece / (8 * kAdamThreads); ++j) {
-    const int64_t i = base + j * 8 * kAdamThreads;
-    const int cnt = count_of<FULL, 8>(i, d.n);
-    float m[8], v[8];
-    if constexpr (BLOCK8) {
-      const int64_t blk = (cnt > 0 ? i : d.n - 1) / ADAMW_BLOCK;
-      const float ms = gmem(d.m_scale)[blk], vs = gmem(d.v_scale)[blk];
-      decode8(load_codes(d.m, i, cnt), load_codes(d.v, i, cnt), m, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        m[e] *= ms;
-        v[e] *= vs;
-      }
-    } else {
-      load_group<false>(d.m, i, cnt, m);
-      load_group<false>(d.v, i, cnt, v);
+    for (int e = 0; e < 8; ++e) {
+      m[e] *= ms;
+      v[e] *= vs;
     }
-    store_group<BF16>(m_out, d.first + i, cnt, m);
-    store_group<BF16>(v_out, d.first + i, cnt, v);
+  } else {
+    floats8(load8<false, WHOLE>(at_unit(d.m, u, 4), lane, cnt), m);
+    floats8(load8<false, WHOLE>(at_unit(d.v, u, 4), lane, cnt), v);
+  }
+  store8<BF16, WHOLE>(at_unit(static_cast<char*>(m_out) + d.first * size, u, size), lane, cnt, m);
+  store8<BF16, WHOLE>(at_unit(static_cast<char*>(v_out) + d.first * size, u, size), lane, cnt, v);
+}
+
+template <bool BLOCK8, bool BF16, bool WHOLE>
+__device__ __forceinline__ void set_unit(const AdamDesc& d, int64_t u, int left, const void* m_in, const void* v_in) {
+  const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
+  constexpr int kBlocks = kAdamUnit / ADAMW_BLOCK, size = BF16 ? 2 : 4;
+  float m[8], v[8];
+  floats8(load8<BF16, WHOLE>(at_unit(static_cast<const char*>(m_in) + d.first * size, u, size), lane, cnt), m);
+  floats8(load8<BF16, WHOLE>(at_unit(static_cast<const char*>(v_in) + d.first * size, u, size), lane, cnt), v);
+  if constexpr (BLOCK8) {
+    u32x2 mc, vc;
+    float ms, vs;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += 0.0f;   // -0 becomes +0
+    encode8<false>(m, v, 0, mc, vc, ms, vs);
+    store_codes<WHOLE>(at_unit(d.m, u, 1), lane, cnt, mc);
+    store_codes<WHOLE>(at_unit(d.v, u, 1), lane, cnt, vc);
+    if ((lane & 31) == 0 && cnt > 0) {
+      gmem(d.m_scale + u * kBlocks)[lane >> 5] = ms;
+      gmem(d.v_scale + u * kBlocks)[lane >> 5] = vs;
+    }
+  } else {
+    store8<false, WHOLE>(at_unit(d.m, u, 4), lane, cnt, m);
+    store8<false, WHOLE>(at_unit(d.v, u, 4), lane, cnt, v);
+  }
+}
+
+template <typename Whole, typename Short>
+__device__ __forceinline__ void each_unit(const AdamArgs& a, Whole whole, Short short_unit) {
+  uint32_t k = blockIdx.x;
+  for (; k < a.nwhole; k += gridDim.x) {
+    const AdamUnit u = a.units[k];
+    whole(a.desc[u.tensor], u.unit);
+  }
+  for (; k < a.nunits; k += gridDim.x) {
+    const AdamUnit u = a.units[k];
+    const AdamDesc& d = a.desc[u.tensor];
+    short_unit(d, u.unit, static_cast<int>(d.n - static_cast<int64_t>(u.unit) * kAdamUnit));
   }
 }
 
 template <bool BLOCK8, bool BF16>
-__global__ __launch_bounds__(kAdamThreads) void k_get(AdamArgs a, void* m_out, void* v_out) {
-  for (int64_t p = blockIdx.x; p < a.npieces; p += gridDim.x) {
-    const AdamPiece pc = a.pieces[p];
-    const AdamDesc& d = a.desc[pc.tensor];
-    const int64_t at = static_cast<int64_t>(pc.piece) * kAdamPiece;
-    if (d.n - at >= kAdamPiece) piece_get<BLOCK8, BF16, true>(d, at + 8 * threadIdx.x, m_out, v_out);
-    else piece_get<BLOCK8, BF16, false>(d, at + 8 * threadIdx.x, m_out, v_out);
-  }
-}
-
-template <bool BLOCK8, bool BF16, bool FULL>
-__device__ __forceinline__ void piece_set(const AdamDesc& d, int64_t base, const void* m_in, const void* v_in) {
-#pragma unroll
-  for (int j = 0; j < kAdamPiece / (8 * kAdamThreads); ++j) {
-    const int64_t i = base + j * 8 * kAdamThreads;
-    const int cnt = count_of<FULL, 8>(i, d.n);
-    float m[8], v[8];
-    load_group<BF16>(m_in, d.first + i, cnt, m);
-    load_group<BF16>(v_in, d.first + i, cnt, v);
-    if constexpr (BLOCK8) {
-      uint2 mc, vc;
-      float ms, vs;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += 0.0f;   // -0 becomes +0
-      encode8<false>(m, v, 0, 0, mc, vc, ms, vs);
-      store_codes(d.m, i, cnt, mc);
-      store_codes(d.v, i, cnt, vc);
-      if ((threadIdx.x & 31) == 0 && cnt > 0) {
-        gmem(d.m_scale)[i / ADAMW_BLOCK] = ms;
-        gmem(d.v_scale)[i / ADAMW_BLOCK] = vs;
-      }
-    } else {
-      store_group<false>(d.m, i, cnt, m);
-      store_group<false>(d.v, i, cnt, v);
-    }
-  }
+__global__ __launch_bounds__(kAdamThreads) void k_get(AdamArgs a, void* m, void* v) {
+  each_unit(
+      a, [&](const AdamDesc& d, int64_t u) { get_unit<BLOCK8, BF16, true>(d, u, kAdamUnit, m, v); },
+      [&](const AdamDesc& d, int64_t u, int left) { get_unit<BLOCK8, BF16, false>(d, u, left, m, v); });
 }
 
 template <bool BLOCK8, bool BF16>
-__global__ __launch_bounds__(kAdamThreads) void k_set(AdamArgs a, const void* m_in, const void* v_in) {
-  for (int64_t p = blockIdx.x; p < a.npieces; p += gridDim.x) {
-    const AdamPiece pc = a.pieces[p];
-    const AdamDesc& d = a.desc[pc.tensor];
-    const int64_t at = static_cast<int64_t>(pc.piece) * kAdamPiece;
-    if (d.n - at >= kAdamPiece) piece_set<BLOCK8, BF16, true>(d, at + 8 * threadIdx.x, m_in, v_in);
-    else piece_set<BLOCK8, BF16, false>(d, at + 8 * threadIdx.x, m_in, v_in);
-  }
+__global__ __launch_bounds__(kAdamThreads) void k_set(AdamArgs a, const void* m, const void* v) {
+  each_unit(
+      a, [&](const AdamDesc& d, int64_t u) { set_unit<BLOCK8, BF16, true>(d, u, kAdamUnit, m, v); },
+      [&](const AdamDesc& d, int64_t u, int left) { set_unit<BLOCK8, BF16, false>(d, u, left, m, v); });
 }
 
-// At most `most` workgroups; a batch without elements still takes its step
-// (the step number advances).
-unsigned grid_of(const AdamArgs& a, int most) {
-  return static_cast<unsigned>(a.npieces < 1 ? 1 : a.npieces < most ? a.npieces : most);
-}
+// A batch without elements still takes its step: one thread advances the
+// step number.
+__global__ void k_adamw_empty(AdamArgs a) { advance_step(a, ticket_take(a.tickets)); }
 
 template <bool WB, bool GB, bool MASTER>
 void launch_step(const AdamArgs& a, bool advance, hipStream_t s) {
-  const dim3 threads(kAdamThreads);
-  if (!a.block8)
-    hipLaunchKernelGGL((k_adamw32<WB, GB, MASTER>), dim3(grid_of(a, kGrid32)), threads, 0, s, a, advance);
-  else if (a.stochastic)
-    hipLaunchKernelGGL((k_adamw8<WB, GB, MASTER, true>), dim3(grid_of(a, kGrid8)), threads, 0, s, a, advance);
-  else
-    hipLaunchKernelGGL((k_adamw8<WB, GB, MASTER, false>), dim3(grid_of(a, kGrid8)), threads, 0, s, a, advance);
+  const dim3 grid(std::min<uint32_t>(a.nunits, kAdamGrid)), threads(kAdamThreads);
+  if (!a.block8) hipLaunchKernelGGL((k_adamw32<WB, GB, MASTER>), grid, threads, 0, s, a, advance);
+  else if (a.stochastic) hipLaunchKernelGGL((k_adamw8<WB, GB, MASTER, true>), grid, threads, 0, s, a, advance);
+  else hipLaunchKernelGGL((k_adamw8<WB, GB, MASTER, false>), grid, threads, 0, s, a, advance);
 }
 
 }  // namespace
 
 hipError_t launch_adamw(const AdamArgs& a, bool advance, hipStream_t s) {
+  if (a.nunits == 0) {
+    if (advance) hipLaunchKernelGGL(k_adamw_empty, dim3(1), dim3(1), 0, s, a);
+    return hipGetLastError();
+  }
   const bool wb = a.w_dt == DT_BF16, gb = a.g_dt == DT_BF16;
   if (a.has_master) {
     if (gb) launch_step<true, true, true>(a, advance, s);
@@ -544,8 +649,8 @@ hipError_t launch_adamw_ctl(AdamCtl* ctl, const AdamCtl& value, bool set_step, h
 }
 
 hipError_t launch_adamw_get(const AdamArgs& a, void* m, void* v, int32_t dt, hipStream_t s) {
-  if (!a.npieces) return hipSuccess;
-  const dim3 grid(grid_of(a, kGridState)), threads(kAdamThreads);
+  if (a.nunits == 0) return hipSuccess;
+  const dim3 grid(std::min<uint32_t>(a.nunits, kStateGrid)), threads(kAdamThreads);
   const bool bf16 = dt == DT_BF16;
   if (a.block8) {
     if (bf16) hipLaunchKernelGGL((k_get<true, true>), grid, threads, 0, s, a, m, v);
@@ -558,8 +663,8 @@ hipError_t launch_adamw_get(const AdamArgs& a, void* m, void* v, int32_t dt, hip
 }
 
 hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int32_t dt, hipStream_t s) {
-  if (!a.npieces) return hipSuccess;
-  const dim3 grid(grid_of(a, kGridState)), threads(kAdamThreads);
+  if (a.nunits == 0) return hipSuccess;
+  const dim3 grid(std::min<uint32_t>(a.nunits, kStateGrid)), threads(kAdamThreads);
   const bool bf16 = dt == DT_BF16;
   if (a.block8) {
     if (bf16) hipLaunchKernelGGL((k_set<true, true>), grid, threads, 0, s, a, m, v);

@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
   // release, which would write back the whole L2.
   if (threadIdx.x == 0) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    last = ticket_last(a.tickets, ticket_take(a.tickets));
   }
   __syncthreads();
   if (!last) return;
@@ -88,7 +88,6 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
     const double norm = sqrt(sum);
     a.out[0] = static_cast<float>(norm);
     a.out[1] = norm <= a.max_norm ? 1.0f : static_cast<float>(a.max_norm / norm);
-    *a.ticket = 0;
   }
   if (a.tensor_norms)
     for (uint32_t t = threadIdx.x; t < a.ntensors; t += kNormThreads) {

@@ -189,7 +189,7 @@ def test_state_elems_and_workspace():
     arr[0].n, arr[1].n, arr[2].n = 1, 0, 257
     assert lib.adamw_state_elems(arr, 3, ctypes.byref(out)) == 0 and out.value == 256 + 512
     assert lib.adamw_workspace_bytes(arr, 3, ctypes.byref(fake_cfg()), ctypes.byref(nbytes)) == 0
-    assert 0 < nbytes.value < 4096
+    assert 0 < nbytes.value < 8192   # counters (33 lines of 128 bytes), three descriptors, two units
     # gradients may share memory: the NULL workspace is what is refused
     arr = fake(2)
     arr[1].g = arr[0].g
