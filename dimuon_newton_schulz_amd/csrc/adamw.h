@@ -10,13 +10,14 @@
 
 namespace muon {
 
-// Work is dealt in units of kAdamUnit elements of one tensor (256 threads of
-// eight elements; the last unit of a tensor may be shorter).  A unit is a
-// multiple of ADAMW_BLOCK, so a block of the 8-bit moments never spans two.
+// Work is dealt in units of kAdamUnit elements of one tensor, a workgroup
+// each (256 threads, kAdamGroups times eight elements per thread; the last
+// unit of a tensor may be shorter).  A unit is a multiple of ADAMW_BLOCK, so a
+// block of the 8-bit moments never spans two.
 constexpr int kAdamThreads = 256;
-constexpr int kAdamUnit = 8 * kAdamThreads;
-constexpr int kAdamGrid = 1024;   // most workgroups of a step
-constexpr int kStateGrid = 2048;  // and of a pass over the moments
+constexpr int kAdamGroups = 2;
+constexpr int kAdamGroup = 8 * kAdamThreads;
+constexpr int kAdamUnit = kAdamGroups * kAdamGroup;
 
 // Per-tensor descriptor (uploaded once per batch into the workspace).
 struct alignas(16) AdamDesc {
@@ -33,9 +34,8 @@ struct alignas(16) AdamDesc {
   float weight_decay;
 };
 
-// One unit of work.  The whole units of all tensors come first, then the
-// tensors' short last ones.  Workgroup b takes units b, b + nwg, b + 2 nwg,
-// ...: the workgroups running at once stream through neighbouring memory.
+// One unit of work.  The whole units of all tensors come first, in memory
+// order, then the tensors' short last ones.
 struct alignas(8) AdamUnit {
   uint32_t tensor, unit;
 };
@@ -56,24 +56,19 @@ struct alignas(16) AdamCtl {
 // add to one address takes about 14 ns whoever issues it (measured: 2048 of
 // them held a launch back by 25 us), so the workgroups are spread over groups
 // of kTicketGroup, each with a counter in a line of its own, and the last one
-// of a group counts the group.
+// of a group counts the group.  Ticket 0 counts the groups.
 constexpr int kTicketGroup = 64;
-constexpr int kTicketGroups = 32;   // most groups: 2048 workgroups
 struct alignas(128) Ticket {
   uint32_t count;
 };
-static_assert(kAdamGrid <= kTicketGroup * kTicketGroups, "more workgroups than tickets");
-struct Tickets {
-  Ticket group[kTicketGroups];
-  Ticket root;
-};
+inline int64_t tickets_of(int64_t workgroups) { return 1 + (workgroups + kTicketGroup - 1) / kTicketGroup; }
 
 struct AdamArgs {
   const AdamDesc* desc;
   const AdamUnit* units;
   uint32_t nunits, nwhole;   // all units, whole units
   AdamCtl* ctl;
-  Tickets* tickets;
+  Ticket* tickets;
   const float* grad_scale;  // or NULL
   double beta1, beta2;
   uint64_t seed;
@@ -108,21 +103,20 @@ __host__ __device__ inline uint32_t adam_key(uint64_t seed, int64_t t) {
 #if defined(__HIPCC__)
 // Adds this workgroup to its group; one thread calls it.  The counter's value
 // before says whether it is the group's last.
-__device__ __forceinline__ uint32_t ticket_take(Tickets* t) {
-  const uint32_t groups = (gridDim.x + kTicketGroup - 1) / kTicketGroup;
-  return __hip_atomic_fetch_add(&t->group[blockIdx.x % groups].count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ uint32_t ticket_take(Ticket* t) {
+  return __hip_atomic_fetch_add(&t[1 + blockIdx.x / kTicketGroup].count, 1u, __ATOMIC_RELAXED,
+                                __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Whether the workgroup that took `seen` is the launch's last.  The counters
 // are zero again after the last one's call.
-__device__ __forceinline__ bool ticket_last(Tickets* t, uint32_t seen) {
-  const uint32_t groups = (gridDim.x + kTicketGroup - 1) / kTicketGroup, mine = blockIdx.x % groups;
-  const uint32_t members = (gridDim.x - mine + groups - 1) / groups;
+__device__ __forceinline__ bool ticket_last(Ticket* t, uint32_t seen) {
+  const uint32_t groups = (gridDim.x + kTicketGroup - 1) / kTicketGroup, mine = blockIdx.x / kTicketGroup;
+  const uint32_t members = mine + 1 < groups ? kTicketGroup : gridDim.x - mine * kTicketGroup;
   if (seen != members - 1) return false;
-  __hip_atomic_store(&t->group[mine].count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (__hip_atomic_fetch_add(&t->root.count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != groups - 1)
-    return false;
-  __hip_atomic_store(&t->root.count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(&t[1 + mine].count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (__hip_atomic_fetch_add(&t[0].count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != groups - 1) return false;
+  __hip_atomic_store(&t[0].count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return true;
 }
 #endif
@@ -145,7 +139,6 @@ hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;
 constexpr int kNormGrid = 2048;        // most workgroups of one launch
-static_assert(kNormGrid <= kTicketGroup * kTicketGroups, "more workgroups than tickets");
 constexpr int kNormUnitBytes = 8192;   // smallest share of work
 
 struct alignas(16) NormTensor {
@@ -168,7 +161,7 @@ struct NormArgs {
   const NormRun* runs;
   const uint32_t* first_run;   // per workgroup, nwg + 1 entries
   double* partial;             // one per run
-  Tickets* tickets;
+  Ticket* tickets;
   float* out;
   float* tensor_norms;         // or NULL
   float max_norm;

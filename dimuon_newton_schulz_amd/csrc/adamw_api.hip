@@ -14,7 +14,7 @@ namespace {
 
 constexpr int64_t kMaxTensors = int64_t{1} << 20;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
-constexpr int64_t kMaxUnits = (int64_t{1} << 32) - 1 - kStateGrid;
+constexpr int64_t kMaxUnits = (int64_t{1} << 31) - 1;   // workgroups of one launch
 
 // Makes a plan's device current for one call.
 struct DeviceGuard {
@@ -131,7 +131,7 @@ muon_status_t adam_layout(const adamw_tensor_t* ts, int64_t count, AdamTable& t)
   }
   if (t.nunits > kMaxUnits) return fail(MUON_ERR_UNSUPPORTED, "the batch is too large");
   t.ticket_off = round_up(sizeof(AdamCtl), kAlign);
-  t.desc_off = round_up(t.ticket_off + sizeof(Tickets), kAlign);
+  t.desc_off = round_up(t.ticket_off + sizeof(Ticket) * tickets_of(t.nunits), kAlign);
   t.unit_off = round_up(t.desc_off + sizeof(AdamDesc) * count, kAlign);
   t.bytes = round_up(t.unit_off + sizeof(AdamUnit) * t.nunits, kAlign);
   return MUON_OK;
@@ -206,7 +206,7 @@ AdamArgs adam_args(const AdamTable& t, const adamw_config_t& cfg, void* ws) {
   a.nunits = static_cast<uint32_t>(t.nunits);
   a.nwhole = static_cast<uint32_t>(t.nwhole);
   a.ctl = reinterpret_cast<AdamCtl*>(base);
-  a.tickets = reinterpret_cast<Tickets*>(base + t.ticket_off);
+  a.tickets = reinterpret_cast<Ticket*>(base + t.ticket_off);
   a.grad_scale = cfg.grad_scale;
   a.beta1 = cfg.beta1;
   a.beta2 = cfg.beta2;
@@ -277,7 +277,7 @@ muon_status_t norm_layout(const muon_grad_t* gs, int64_t count, NormTable& t) {
   }
   t.tensors[count] = NormTensor{nullptr, 0, 0, static_cast<uint32_t>(t.runs.size())};
   t.first_run.push_back(static_cast<uint32_t>(t.runs.size()));
-  t.tensor_off = round_up(sizeof(Tickets), kAlign);   // the tickets come first
+  t.tensor_off = round_up(sizeof(Ticket) * tickets_of(t.nwg), kAlign);   // the tickets come first
   t.run_off = round_up(t.tensor_off + sizeof(NormTensor) * t.tensors.size(), kAlign);
   t.first_off = round_up(t.run_off + sizeof(NormRun) * t.runs.size(), kAlign);
   t.table_bytes = round_up(t.first_off + sizeof(uint32_t) * t.first_run.size(), kAlign);
@@ -320,7 +320,7 @@ NormArgs norm_args(const NormTable& t, float max_norm, float* out, float* tensor
   a.runs = reinterpret_cast<const NormRun*>(base + t.run_off);
   a.first_run = reinterpret_cast<const uint32_t*>(base + t.first_off);
   a.partial = reinterpret_cast<double*>(base + t.partial_off);
-  a.tickets = reinterpret_cast<Tickets*>(base);
+  a.tickets = reinterpret_cast<Ticket*>(base);
   a.out = out;
   a.tensor_norms = tensor_norms;
   a.max_norm = max_norm;

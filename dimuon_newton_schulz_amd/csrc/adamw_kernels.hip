@@ -1,7 +1,5 @@
 // AdamW over many tensors: the step with 32- and 8-bit moments, and the
 // moments as values.
-#include <algorithm>
-
 #include "adamw.h"
 
 namespace muon {
@@ -9,8 +7,8 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Eight consecutive elements per thread, raw as loaded: 16 bytes of bf16 or 32
-// of float32, eight code bytes.  p is the unit's base (the same for the whole
-// workgroup) and `lane` the thread in it.  In a unit that is not WHOLE, only
+// of float32, eight code bytes.  p is the group's base (the same for the
+// whole workgroup) and `lane` the thread in it.  In a group that is not WHOLE, only
 // `cnt` of the eight exist; the others read as zero and are not written.
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -127,18 +125,16 @@ __device__ __forceinline__ void store_codes(void* p, int lane, int cnt, u32x2 c)
     if (e < cnt) gmem(static_cast<uint8_t*>(p))[8 * lane + e] = static_cast<uint8_t>(c[e >> 2] >> (8 * (e & 3)));
 }
 
-// Elements of this thread in a unit of `left` elements.
+// Elements of this thread in a group of `left` elements.
 __device__ __forceinline__ int count_of(int left) {
   const int k = left - 8 * static_cast<int>(threadIdx.x);
   return k < 0 ? 0 : k > 8 ? 8 : k;
 }
 
-// Address of unit u of a run.
-__device__ __forceinline__ void* at_unit(void* p, int64_t u, int size) {
-  return static_cast<char*>(p) + u * kAdamUnit * size;
-}
-__device__ __forceinline__ const void* at_unit(const void* p, int64_t u, int size) {
-  return static_cast<const char*>(p) + u * kAdamUnit * size;
+// Address of element `at` of a tensor.
+__device__ __forceinline__ void* elem_at(void* p, int64_t at, int size) { return static_cast<char*>(p) + at * size; }
+__device__ __forceinline__ const void* elem_at(const void* p, int64_t at, int size) {
+  return static_cast<const char*>(p) + at * size;
 }
 
 // ---------------------------------------------------------------------------
@@ -359,31 +355,28 @@ __device__ __forceinline__ void advance_step(const AdamArgs& a, uint32_t seen) {
   *a.ctl = c;
 }
 
-// One unit's operands as loaded.  The next unit's are loaded before this
-// one's results are stored: loads and stores share one in-order counter, so
-// a load issued behind a store would wait for it.
+// A group's operands as loaded (kAdamGroup elements from element `at` of its
+// tensor on, `left` of them in a group that is not WHOLE).
 template <bool WB, bool GB, bool MASTER>
-struct Unit32 {
+struct Group32 {
   Raw8<GB> g;
   Raw8<WB && !MASTER> w;
   Raw8<false> m, v;
 };
 
 template <bool WB, bool GB, bool MASTER, bool WHOLE>
-__device__ __forceinline__ Unit32<WB, GB, MASTER> load_unit32(const AdamDesc& d, int64_t u, int left) {
+__device__ __forceinline__ void load_group(const AdamDesc& d, int64_t at, int left, Group32<WB, GB, MASTER>& x) {
   const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
-  Unit32<WB, GB, MASTER> x;
-  x.g = load8<GB, WHOLE>(at_unit(d.g, u, GB ? 2 : 4), lane, cnt);
-  if constexpr (MASTER) x.w = load8<false, WHOLE>(at_unit(d.master, u, 4), lane, cnt);
-  else x.w = load8<WB, WHOLE>(at_unit(d.w, u, WB ? 2 : 4), lane, cnt);
-  x.m = load8<false, WHOLE>(at_unit(d.m, u, 4), lane, cnt);
-  x.v = load8<false, WHOLE>(at_unit(d.v, u, 4), lane, cnt);
-  return x;
+  x.g = load8<GB, WHOLE>(elem_at(d.g, at, GB ? 2 : 4), lane, cnt);
+  if constexpr (MASTER) x.w = load8<false, WHOLE>(elem_at(d.master, at, 4), lane, cnt);
+  else x.w = load8<WB, WHOLE>(elem_at(d.w, at, WB ? 2 : 4), lane, cnt);
+  x.m = load8<false, WHOLE>(elem_at(d.m, at, 4), lane, cnt);
+  x.v = load8<false, WHOLE>(elem_at(d.v, at, 4), lane, cnt);
 }
 
-template <bool WB, bool GB, bool MASTER, bool WHOLE>
-__device__ __forceinline__ void step_unit32(const StepValues& s, const AdamDesc& d, int64_t u, int left,
-                                            const Unit32<WB, GB, MASTER>& x) {
+template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, bool WHOLE>
+__device__ __forceinline__ void step_group(const StepValues& s, const AdamDesc& d, int64_t at, int left,
+                                           const Group32<WB, GB, MASTER>& x) {
   const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
   const float adam = s.lr * d.lr_scale * s.rb1, decay = s.lr * d.weight_decay;
   float g[8], w[8], m[8], v[8];
@@ -393,57 +386,14 @@ __device__ __forceinline__ void step_unit32(const StepValues& s, const AdamDesc&
   floats8(x.v, v);
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] = update(s, g[e], w[e], s.b1, s.b2, adam, decay, m[e], v[e]);
-  if constexpr (MASTER) store8<false, WHOLE>(at_unit(d.master, u, 4), lane, cnt, w);
-  store8<WB, WHOLE>(at_unit(d.w, u, WB ? 2 : 4), lane, cnt, w);
-  store8<false, WHOLE>(at_unit(d.m, u, 4), lane, cnt, m);
-  store8<false, WHOLE>(at_unit(d.v, u, 4), lane, cnt, v);
-}
-
-// Walks this workgroup's units: the operands of the next whole unit are loaded
-// before step() stores the current one's results.
-template <typename LoadWhole, typename StepWhole, typename Short>
-__device__ __forceinline__ void walk_units(const AdamArgs& a, LoadWhole load, StepWhole step, Short short_unit) {
-  uint32_t k = blockIdx.x;
-  if (k < a.nwhole) {
-    AdamUnit u = a.units[k];
-    AdamDesc d = a.desc[u.tensor];
-    auto x = load(d, u.unit);
-    for (;;) {
-      k += gridDim.x;
-      if (k >= a.nwhole) break;
-      const AdamUnit u1 = a.units[k];
-      const AdamDesc d1 = a.desc[u1.tensor];
-      const auto y = load(d1, u1.unit);
-      step(d, u.unit, x);
-      u = u1;
-      d = d1;
-      x = y;
-    }
-    step(d, u.unit, x);
-  }
-  for (; k < a.nunits; k += gridDim.x) {
-    const AdamUnit u = a.units[k];
-    const AdamDesc& d = a.desc[u.tensor];
-    short_unit(d, u.unit, static_cast<int>(d.n - static_cast<int64_t>(u.unit) * kAdamUnit));
-  }
+  if constexpr (MASTER) store8<false, WHOLE>(elem_at(d.master, at, 4), lane, cnt, w);
+  store8<WB, WHOLE>(elem_at(d.w, at, WB ? 2 : 4), lane, cnt, w);
+  store8<false, WHOLE>(elem_at(d.m, at, 4), lane, cnt, m);
+  store8<false, WHOLE>(elem_at(d.v, at, 4), lane, cnt, v);
 }
 
 template <bool WB, bool GB, bool MASTER>
-__global__ __launch_bounds__(kAdamThreads) void k_adamw32(AdamArgs a, bool advance) {
-  const StepValues s = step_values(a);
-  const uint32_t seen = have_values(a);
-  typedef Unit32<WB, GB, MASTER> Unit;
-  walk_units(
-      a, [&](const AdamDesc& d, int64_t u) { return load_unit32<WB, GB, MASTER, true>(d, u, kAdamUnit); },
-      [&](const AdamDesc& d, int64_t u, const Unit& x) { step_unit32<WB, GB, MASTER, true>(s, d, u, kAdamUnit, x); },
-      [&](const AdamDesc& d, int64_t u, int left) {
-        step_unit32<WB, GB, MASTER, false>(s, d, u, left, load_unit32<WB, GB, MASTER, false>(d, u, left));
-      });
-  if (advance) advance_step(a, seen);
-}
-
-template <bool WB, bool GB, bool MASTER>
-struct Unit8 {
+struct Group8 {
   Raw8<GB> g;
   Raw8<WB && !MASTER> w;
   u32x2 m, v;
@@ -451,37 +401,33 @@ struct Unit8 {
 };
 
 template <bool WB, bool GB, bool MASTER, bool WHOLE>
-__device__ __forceinline__ Unit8<WB, GB, MASTER> load_unit8(const AdamDesc& d, int64_t u, int left) {
+__device__ __forceinline__ void load_group(const AdamDesc& d, int64_t at, int left, Group8<WB, GB, MASTER>& x) {
   const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
-  constexpr int kBlocks = kAdamUnit / ADAMW_BLOCK;
-  Unit8<WB, GB, MASTER> x;
-  x.g = load8<GB, WHOLE>(at_unit(d.g, u, GB ? 2 : 4), lane, cnt);
-  if constexpr (MASTER) x.w = load8<false, WHOLE>(at_unit(d.master, u, 4), lane, cnt);
-  else x.w = load8<WB, WHOLE>(at_unit(d.w, u, WB ? 2 : 4), lane, cnt);
-  x.m = load_codes<WHOLE>(at_unit(d.m, u, 1), lane, cnt);
-  x.v = load_codes<WHOLE>(at_unit(d.v, u, 1), lane, cnt);
+  x.g = load8<GB, WHOLE>(elem_at(d.g, at, GB ? 2 : 4), lane, cnt);
+  if constexpr (MASTER) x.w = load8<false, WHOLE>(elem_at(d.master, at, 4), lane, cnt);
+  else x.w = load8<WB, WHOLE>(elem_at(d.w, at, WB ? 2 : 4), lane, cnt);
+  x.m = load_codes<WHOLE>(elem_at(d.m, at, 1), lane, cnt);
+  x.v = load_codes<WHOLE>(elem_at(d.v, at, 1), lane, cnt);
   // A lane without elements takes the scale of the tensor's last block.
   const int blk = (WHOLE || cnt > 0 ? 8 * lane : left - 1) / ADAMW_BLOCK;
-  x.ms = gmem(d.m_scale + u * kBlocks)[blk];
-  x.vs = gmem(d.v_scale + u * kBlocks)[blk];
-  return x;
+  x.ms = gmem(d.m_scale + at / ADAMW_BLOCK)[blk];
+  x.vs = gmem(d.v_scale + at / ADAMW_BLOCK)[blk];
 }
 
-// What the hash of this thread's first element of unit u mixes.
-__device__ __forceinline__ uint32_t hash_base(const StepValues& s, const AdamDesc& d, int64_t u) {
-  const uint64_t at = static_cast<uint64_t>(d.first + u * kAdamUnit);
-  const uint32_t lo = static_cast<uint32_t>(at), hi = static_cast<uint32_t>(at >> 32);
-  uint32_t k = adam_mix(s.key + hi);   // the same for the whole unit, unless it passes a multiple of 2^32
+// What the hash of this thread's first element of the group mixes.
+__device__ __forceinline__ uint32_t hash_base(const StepValues& s, const AdamDesc& d, int64_t at) {
+  const uint64_t id = static_cast<uint64_t>(d.first + at);
+  const uint32_t lo = static_cast<uint32_t>(id), hi = static_cast<uint32_t>(id >> 32);
+  uint32_t k = adam_mix(s.key + hi);   // the same for the whole group, unless it passes a multiple of 2^32
   const uint32_t mine = lo + 8 * threadIdx.x;
-  if (lo > 0xFFFFFFFFu - kAdamUnit && mine < lo) k = adam_mix(s.key + hi + 1);
+  if (lo > 0xFFFFFFFFu - kAdamGroup && mine < lo) k = adam_mix(s.key + hi + 1);
   return mine + k;
 }
 
 template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, bool WHOLE>
-__device__ __forceinline__ void step_unit8(const StepValues& s, const AdamDesc& d, int64_t u, int left,
-                                           const Unit8<WB, GB, MASTER>& x) {
+__device__ __forceinline__ void step_group(const StepValues& s, const AdamDesc& d, int64_t at, int left,
+                                           const Group8<WB, GB, MASTER>& x) {
   const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
-  constexpr int kBlocks = kAdamUnit / ADAMW_BLOCK;
   const float adam = s.lr * d.lr_scale * s.rb1, decay = s.lr * d.weight_decay;
   float g[8], w[8], m[8], v[8];
   floats8(x.g, g);
@@ -490,33 +436,54 @@ __device__ __forceinline__ void step_unit8(const StepValues& s, const AdamDesc& 
   const float fm = s.b1 * x.ms, fv = s.b2 * x.vs;
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] = update(s, g[e], w[e], fm, fv, adam, decay, m[e], v[e]);
-  if constexpr (MASTER) store8<false, WHOLE>(at_unit(d.master, u, 4), lane, cnt, w);
-  store8<WB, WHOLE>(at_unit(d.w, u, WB ? 2 : 4), lane, cnt, w);
+  if constexpr (MASTER) store8<false, WHOLE>(elem_at(d.master, at, 4), lane, cnt, w);
+  store8<WB, WHOLE>(elem_at(d.w, at, WB ? 2 : 4), lane, cnt, w);
   u32x2 mc, vc;
   float ms, vs;
-  encode8<STOCHASTIC>(m, v, STOCHASTIC ? hash_base(s, d, u) : 0, mc, vc, ms, vs);
-  store_codes<WHOLE>(at_unit(d.m, u, 1), lane, cnt, mc);
-  store_codes<WHOLE>(at_unit(d.v, u, 1), lane, cnt, vc);
+  encode8<STOCHASTIC>(m, v, STOCHASTIC ? hash_base(s, d, at) : 0, mc, vc, ms, vs);
+  store_codes<WHOLE>(elem_at(d.m, at, 1), lane, cnt, mc);
+  store_codes<WHOLE>(elem_at(d.v, at, 1), lane, cnt, vc);
   if ((lane & 31) == 0 && (WHOLE || cnt > 0)) {
-    gmem(d.m_scale + u * kBlocks)[lane >> 5] = ms;
-    gmem(d.v_scale + u * kBlocks)[lane >> 5] = vs;
+    gmem(d.m_scale + at / ADAMW_BLOCK)[lane >> 5] = ms;
+    gmem(d.v_scale + at / ADAMW_BLOCK)[lane >> 5] = vs;
   }
+}
+
+// One workgroup per unit, in the order of memory: measured against workgroups
+// that walk several units each (1024 to 16384 of them, interleaved), which
+// reach 4.6 to 5.1 TB/s with these streams where this reaches 5.3.
+template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, typename Group>
+__device__ __forceinline__ void adamw_unit(const AdamArgs& a, bool advance) {
+  const StepValues s = step_values(a);
+  const AdamUnit u = a.units[blockIdx.x];
+  const uint32_t seen = have_values(a);
+  const AdamDesc d = a.desc[u.tensor];
+  const int64_t at = static_cast<int64_t>(u.unit) * kAdamUnit;
+  Group x[kAdamGroups];
+  if (blockIdx.x < a.nwhole) {
+#pragma unroll
+    for (int j = 0; j < kAdamGroups; ++j)
+      load_group<WB, GB, MASTER, true>(d, at + j * kAdamGroup, kAdamGroup, x[j]);
+#pragma unroll
+    for (int j = 0; j < kAdamGroups; ++j)
+      step_group<WB, GB, MASTER, STOCHASTIC, true>(s, d, at + j * kAdamGroup, kAdamGroup, x[j]);
+  } else {
+    for (int left = static_cast<int>(d.n - at), j = 0; left > 0; left -= kAdamGroup, ++j) {
+      load_group<WB, GB, MASTER, false>(d, at + j * kAdamGroup, left, x[0]);
+      step_group<WB, GB, MASTER, STOCHASTIC, false>(s, d, at + j * kAdamGroup, left, x[0]);
+    }
+  }
+  if (advance) advance_step(a, seen);
+}
+
+template <bool WB, bool GB, bool MASTER>
+__global__ __launch_bounds__(kAdamThreads) void k_adamw32(AdamArgs a, bool advance) {
+  adamw_unit<WB, GB, MASTER, false, Group32<WB, GB, MASTER>>(a, advance);
 }
 
 template <bool WB, bool GB, bool MASTER, bool STOCHASTIC>
 __global__ __launch_bounds__(kAdamThreads) void k_adamw8(AdamArgs a, bool advance) {
-  const StepValues s = step_values(a);
-  const uint32_t seen = have_values(a);
-  typedef Unit8<WB, GB, MASTER> Unit;
-  walk_units(
-      a, [&](const AdamDesc& d, int64_t u) { return load_unit8<WB, GB, MASTER, true>(d, u, kAdamUnit); },
-      [&](const AdamDesc& d, int64_t u, const Unit& x) {
-        step_unit8<WB, GB, MASTER, STOCHASTIC, true>(s, d, u, kAdamUnit, x);
-      },
-      [&](const AdamDesc& d, int64_t u, int left) {
-        step_unit8<WB, GB, MASTER, STOCHASTIC, false>(s, d, u, left, load_unit8<WB, GB, MASTER, false>(d, u, left));
-      });
-  if (advance) advance_step(a, seen);
+  adamw_unit<WB, GB, MASTER, STOCHASTIC, Group8<WB, GB, MASTER>>(a, advance);
 }
 
 __global__ void k_ctl(AdamCtl* ctl, AdamCtl value, bool set_step) {
@@ -536,78 +503,80 @@ __global__ void k_ctl(AdamCtl* ctl, AdamCtl value, bool set_step) {
 // The moments as values
 // ---------------------------------------------------------------------------
 template <bool BLOCK8, bool BF16, bool WHOLE>
-__device__ __forceinline__ void get_unit(const AdamDesc& d, int64_t u, int left, void* m_out, void* v_out) {
+__device__ __forceinline__ void get_group(const AdamDesc& d, int64_t at, int left, void* m_out, void* v_out) {
   const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
-  constexpr int kBlocks = kAdamUnit / ADAMW_BLOCK, size = BF16 ? 2 : 4;
+  constexpr int size = BF16 ? 2 : 4;
   float m[8], v[8];
   if constexpr (BLOCK8) {
     const int blk = (WHOLE || cnt > 0 ? 8 * lane : left - 1) / ADAMW_BLOCK;
-    const float ms = gmem(d.m_scale + u * kBlocks)[blk], vs = gmem(d.v_scale + u * kBlocks)[blk];
-    decode8(load_codes<WHOLE>(at_unit(d.m, u, 1), lane, cnt), load_codes<WHOLE>(at_unit(d.v, u, 1), lane, cnt), m, v);
+    const float ms = gmem(d.m_scale + at / ADAMW_BLOCK)[blk], vs = gmem(d.v_scale + at / ADAMW_BLOCK)[blk];
+    decode8(load_codes<WHOLE>(elem_at(d.m, at, 1), lane, cnt), load_codes<WHOLE>(elem_at(d.v, at, 1), lane, cnt), m, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       m[e] *= ms;
       v[e] *= vs;
     }
   } else {
-    floats8(load8<false, WHOLE>(at_unit(d.m, u, 4), lane, cnt), m);
-    floats8(load8<false, WHOLE>(at_unit(d.v, u, 4), lane, cnt), v);
+    floats8(load8<false, WHOLE>(elem_at(d.m, at, 4), lane, cnt), m);
+    floats8(load8<false, WHOLE>(elem_at(d.v, at, 4), lane, cnt), v);
   }
-  store8<BF16, WHOLE>(at_unit(static_cast<char*>(m_out) + d.first * size, u, size), lane, cnt, m);
-  store8<BF16, WHOLE>(at_unit(static_cast<char*>(v_out) + d.first * size, u, size), lane, cnt, v);
+  store8<BF16, WHOLE>(elem_at(m_out, d.first + at, size), lane, cnt, m);
+  store8<BF16, WHOLE>(elem_at(v_out, d.first + at, size), lane, cnt, v);
 }
 
 template <bool BLOCK8, bool BF16, bool WHOLE>
-__device__ __forceinline__ void set_unit(const AdamDesc& d, int64_t u, int left, const void* m_in, const void* v_in) {
+__device__ __forceinline__ void set_group(const AdamDesc& d, int64_t at, int left, const void* m_in, const void* v_in) {
   const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
-  constexpr int kBlocks = kAdamUnit / ADAMW_BLOCK, size = BF16 ? 2 : 4;
+  constexpr int size = BF16 ? 2 : 4;
   float m[8], v[8];
-  floats8(load8<BF16, WHOLE>(at_unit(static_cast<const char*>(m_in) + d.first * size, u, size), lane, cnt), m);
-  floats8(load8<BF16, WHOLE>(at_unit(static_cast<const char*>(v_in) + d.first * size, u, size), lane, cnt), v);
+  floats8(load8<BF16, WHOLE>(elem_at(m_in, d.first + at, size), lane, cnt), m);
+  floats8(load8<BF16, WHOLE>(elem_at(v_in, d.first + at, size), lane, cnt), v);
   if constexpr (BLOCK8) {
     u32x2 mc, vc;
     float ms, vs;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += 0.0f;   // -0 becomes +0
     encode8<false>(m, v, 0, mc, vc, ms, vs);
-    store_codes<WHOLE>(at_unit(d.m, u, 1), lane, cnt, mc);
-    store_codes<WHOLE>(at_unit(d.v, u, 1), lane, cnt, vc);
+    store_codes<WHOLE>(elem_at(d.m, at, 1), lane, cnt, mc);
+    store_codes<WHOLE>(elem_at(d.v, at, 1), lane, cnt, vc);
     if ((lane & 31) == 0 && cnt > 0) {
-      gmem(d.m_scale + u * kBlocks)[lane >> 5] = ms;
-      gmem(d.v_scale + u * kBlocks)[lane >> 5] = vs;
+      gmem(d.m_scale + at / ADAMW_BLOCK)[lane >> 5] = ms;
+      gmem(d.v_scale + at / ADAMW_BLOCK)[lane >> 5] = vs;
     }
   } else {
-    store8<false, WHOLE>(at_unit(d.m, u, 4), lane, cnt, m);
-    store8<false, WHOLE>(at_unit(d.v, u, 4), lane, cnt, v);
+    store8<false, WHOLE>(elem_at(d.m, at, 4), lane, cnt, m);
+    store8<false, WHOLE>(elem_at(d.v, at, 4), lane, cnt, v);
   }
 }
 
-template <typename Whole, typename Short>
-__device__ __forceinline__ void each_unit(const AdamArgs& a, Whole whole, Short short_unit) {
-  uint32_t k = blockIdx.x;
-  for (; k < a.nwhole; k += gridDim.x) {
-    const AdamUnit u = a.units[k];
-    whole(a.desc[u.tensor], u.unit);
-  }
-  for (; k < a.nunits; k += gridDim.x) {
-    const AdamUnit u = a.units[k];
-    const AdamDesc& d = a.desc[u.tensor];
-    short_unit(d, u.unit, static_cast<int>(d.n - static_cast<int64_t>(u.unit) * kAdamUnit));
+// Calls whole(desc, at) or part(desc, at, left) for each group of this
+// workgroup's unit.
+template <typename Whole, typename Part>
+__device__ __forceinline__ void each_group(const AdamArgs& a, Whole whole, Part part) {
+  const AdamUnit u = a.units[blockIdx.x];
+  const AdamDesc& d = a.desc[u.tensor];
+  const int64_t at = static_cast<int64_t>(u.unit) * kAdamUnit;
+  if (blockIdx.x < a.nwhole) {
+#pragma unroll
+    for (int j = 0; j < kAdamGroups; ++j) whole(d, at + j * kAdamGroup);
+  } else {
+    for (int left = static_cast<int>(d.n - at), j = 0; left > 0; left -= kAdamGroup, ++j)
+      part(d, at + j * kAdamGroup, left);
   }
 }
 
 template <bool BLOCK8, bool BF16>
 __global__ __launch_bounds__(kAdamThreads) void k_get(AdamArgs a, void* m, void* v) {
-  each_unit(
-      a, [&](const AdamDesc& d, int64_t u) { get_unit<BLOCK8, BF16, true>(d, u, kAdamUnit, m, v); },
-      [&](const AdamDesc& d, int64_t u, int left) { get_unit<BLOCK8, BF16, false>(d, u, left, m, v); });
+  each_group(
+      a, [&](const AdamDesc& d, int64_t at) { get_group<BLOCK8, BF16, true>(d, at, kAdamGroup, m, v); },
+      [&](const AdamDesc& d, int64_t at, int left) { get_group<BLOCK8, BF16, false>(d, at, left, m, v); });
 }
 
 template <bool BLOCK8, bool BF16>
 __global__ __launch_bounds__(kAdamThreads) void k_set(AdamArgs a, const void* m, const void* v) {
-  each_unit(
-      a, [&](const AdamDesc& d, int64_t u) { set_unit<BLOCK8, BF16, true>(d, u, kAdamUnit, m, v); },
-      [&](const AdamDesc& d, int64_t u, int left) { set_unit<BLOCK8, BF16, false>(d, u, left, m, v); });
+  each_group(
+      a, [&](const AdamDesc& d, int64_t at) { set_group<BLOCK8, BF16, true>(d, at, kAdamGroup, m, v); },
+      [&](const AdamDesc& d, int64_t at, int left) { set_group<BLOCK8, BF16, false>(d, at, left, m, v); });
 }
 
 // A batch without elements still takes its step: one thread advances the
@@ -616,7 +585,7 @@ __global__ void k_adamw_empty(AdamArgs a) { advance_step(a, ticket_take(a.ticket
 
 template <bool WB, bool GB, bool MASTER>
 void launch_step(const AdamArgs& a, bool advance, hipStream_t s) {
-  const dim3 grid(std::min<uint32_t>(a.nunits, kAdamGrid)), threads(kAdamThreads);
+  const dim3 grid(a.nunits), threads(kAdamThreads);
   if (!a.block8) hipLaunchKernelGGL((k_adamw32<WB, GB, MASTER>), grid, threads, 0, s, a, advance);
   else if (a.stochastic) hipLaunchKernelGGL((k_adamw8<WB, GB, MASTER, true>), grid, threads, 0, s, a, advance);
   else hipLaunchKernelGGL((k_adamw8<WB, GB, MASTER, false>), grid, threads, 0, s, a, advance);
@@ -650,7 +619,7 @@ hipError_t launch_adamw_ctl(AdamCtl* ctl, const AdamCtl& value, bool set_step, h
 
 hipError_t launch_adamw_get(const AdamArgs& a, void* m, void* v, int32_t dt, hipStream_t s) {
   if (a.nunits == 0) return hipSuccess;
-  const dim3 grid(std::min<uint32_t>(a.nunits, kStateGrid)), threads(kAdamThreads);
+  const dim3 grid(a.nunits), threads(kAdamThreads);
   const bool bf16 = dt == DT_BF16;
   if (a.block8) {
     if (bf16) hipLaunchKernelGGL((k_get<true, true>), grid, threads, 0, s, a, m, v);
@@ -664,7 +633,7 @@ hipError_t launch_adamw_get(const AdamArgs& a, void* m, void* v, int32_t dt, hip
 
 hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int32_t dt, hipStream_t s) {
   if (a.nunits == 0) return hipSuccess;
-  const dim3 grid(std::min<uint32_t>(a.nunits, kStateGrid)), threads(kAdamThreads);
+  const dim3 grid(a.nunits), threads(kAdamThreads);
   const bool bf16 = dt == DT_BF16;
   if (a.block8) {
     if (bf16) hipLaunchKernelGGL((k_set<true, true>), grid, threads, 0, s, a, m, v);
