@@ -137,35 +137,40 @@ hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int
 // ---------------------------------------------------------------------------
 // Global gradient norm
 // ---------------------------------------------------------------------------
+// Every workgroup sums a stretch of one tensor (a leaf).  The sums meet in a
+// tree of nodes with at most 64 children: the last child to store its sum
+// adds up its siblings', one per lane, and goes on to the parent.  A tensor's
+// sum is the value of one leaf or node.
 constexpr int kNormThreads = 256;
-constexpr int kNormGrid = 2048;        // most workgroups of one launch
-constexpr int kNormUnitBytes = 8192;   // smallest share of work
+constexpr int kNormLeafBytes = 32768;
+constexpr int kNormChildren = 64;
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 
-struct alignas(16) NormTensor {
-  const void* g;
-  int64_t n;
+struct alignas(32) NormLeaf {
+  const void* g;          // first element of the stretch
+  uint32_t count;         // elements
   int32_t dt;
-  uint32_t run0;          // this tensor's runs are run0 .. (next tensor's run0) - 1
+  uint32_t slot;          // where its sum goes
+  uint32_t parent;        // node, or kNone
+  uint32_t tensor;        // the tensor whose whole sum this is, or kNone
+  uint32_t reserved0;
 };
 
-// A stretch of one tensor that one workgroup sums; its sum goes to
-// partial[index of the run].
-struct alignas(16) NormRun {
-  int64_t begin, count;   // elements
-  uint32_t tensor;
-  uint32_t pad[3];
+struct alignas(32) NormNode {
+  uint32_t first, children;   // slots of the children's sums
+  uint32_t slot, parent, tensor;
+  uint32_t reserved0[3];
 };
 
 struct NormArgs {
-  const NormTensor* tensors;   // ntensors + 1 entries (the last closes run0)
-  const NormRun* runs;
-  const uint32_t* first_run;   // per workgroup, nwg + 1 entries
-  double* partial;             // one per run
-  Ticket* tickets;
+  const NormLeaf* leaves;
+  const NormNode* nodes;
+  Ticket* arrived;             // per node: children that have stored their sums
+  double* sums;                // by slot
   float* out;
   float* tensor_norms;         // or NULL
   float max_norm;
-  uint32_t ntensors, nruns, nwg;
+  uint32_t nleaves;
 };
 
 hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s);

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int64_t kMaxTensors = int64_t{1} << 20;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
-constexpr int64_t kMaxUnits = (int64_t{1} << 31) - 1;   // workgroups of one launch
+constexpr int64_t kMaxUnits = (int64_t{1} << 31) - 1, kMaxLeaves = kMaxUnits;   // workgroups of one launch
 
 // Makes a plan's device current for one call.
 struct DeviceGuard {
@@ -235,54 +235,87 @@ AdamArgs adam_args(const AdamTable& t, const adamw_config_t& cfg, void* ws) {
 // Gradient norm
 // ---------------------------------------------------------------------------
 struct NormTable {
-  std::vector<NormTensor> tensors;
-  std::vector<NormRun> runs;
-  std::vector<uint32_t> first_run;
-  uint32_t nwg = 1;
-  size_t tensor_off = 0, run_off = 0, first_off = 0, partial_off = 0, table_bytes = 0, bytes = 0;
+  std::vector<NormLeaf> leaves;
+  std::vector<NormNode> nodes;
+  size_t nslots = 0;
+  size_t leaf_off = 0, node_off = 0, arrived_off = 0, sum_off = 0, table_bytes = 0, bytes = 0;
 };
 
-// Work is dealt in units of kNormUnitBytes of one tensor (the last unit of a
-// tensor may be shorter); every workgroup takes a contiguous stretch of
-// units, and the part of it in one tensor is a run.
+// Links `count` sums in slots first .. first + count - 1, whose owners write
+// their parent through set_parent(i, node), under one node (or, for one sum,
+// no new node), whose sum goes to slot `top` of `tensor`.
+template <typename SetParent>
+void norm_tree(NormTable& t, uint32_t first, uint32_t count, uint32_t top, uint32_t tensor, SetParent set_parent) {
+  std::vector<uint32_t> below;   // nodes of the level below; empty: the owners themselves
+  for (;;) {
+    const uint32_t groups = static_cast<uint32_t>(ceil_div(count, kNormChildren));
+    std::vector<uint32_t> level;
+    const uint32_t slots = static_cast<uint32_t>(t.nslots);
+    if (groups > 1) t.nslots += groups;
+    for (uint32_t k = 0; k < groups; ++k) {
+      const uint32_t id = static_cast<uint32_t>(t.nodes.size()), c0 = k * kNormChildren;
+      const uint32_t n = std::min<uint32_t>(kNormChildren, count - c0);
+      NormNode node{first + c0, n, groups > 1 ? slots + k : top, kNone, groups > 1 ? kNone : tensor, {0, 0, 0}};
+      t.nodes.push_back(node);
+      for (uint32_t c = c0; c < c0 + n; ++c) {
+        if (below.empty()) set_parent(c, id);
+        else t.nodes[below[c]].parent = id;
+      }
+      level.push_back(id);
+    }
+    if (groups == 1) return;
+    first = slots;
+    count = groups;
+    below.swap(level);
+  }
+}
+
 muon_status_t norm_layout(const muon_grad_t* gs, int64_t count, NormTable& t) {
   muon_status_t st;
   if ((st = check_count(gs, count)) != MUON_OK) return st;
-  int64_t units = 0;
+  int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (gs[i].dtype != MUON_F32 && gs[i].dtype != MUON_BF16)
       return fail(MUON_ERR_DTYPE, "tensor %lld: unknown dtype %d", (long long)i, static_cast<int>(gs[i].dtype));
-    units += ceil_div(gs[i].n, kNormUnitBytes / static_cast<int64_t>(dtype_size(gs[i].dtype)));
+    total += std::max<int64_t>(1, ceil_div(gs[i].n, kNormLeafBytes / static_cast<int64_t>(dtype_size(gs[i].dtype))));
   }
-  const int64_t per = std::max<int64_t>(1, ceil_div(units, kNormGrid));
-  t.nwg = static_cast<uint32_t>(std::max<int64_t>(1, ceil_div(units, per)));
-  t.tensors.resize(count + 1);
-  int64_t left = per;   // units the current workgroup still takes
-  t.first_run.push_back(0);
+  if (total > kMaxLeaves) return fail(MUON_ERR_UNSUPPORTED, "the batch is too large");
+  t.leaves.reserve(total);
+  // Slots 0 .. count - 1 hold the tensors' sums.
+  t.nslots = count;
+  struct Owner { uint32_t leaf, node; };   // what writes a tensor's sum
+  std::vector<Owner> owner(count);
   for (int64_t i = 0; i < count; ++i) {
-    const int64_t unit = kNormUnitBytes / static_cast<int64_t>(dtype_size(gs[i].dtype));
-    t.tensors[i] = NormTensor{gs[i].g, gs[i].n, static_cast<int32_t>(gs[i].dtype),
-                              static_cast<uint32_t>(t.runs.size())};
-    for (int64_t at = 0; at < gs[i].n;) {
-      if (left == 0) {
-        t.first_run.push_back(static_cast<uint32_t>(t.runs.size()));
-        left = per;
-      }
-      const int64_t take = std::min(left, ceil_div(gs[i].n - at, unit));
-      const int64_t cnt = std::min(take * unit, gs[i].n - at);
-      t.runs.push_back({at, cnt, static_cast<uint32_t>(i), {0, 0, 0}});
-      at += cnt;
-      left -= take;
+    const int64_t size = dtype_size(gs[i].dtype), most = kNormLeafBytes / size;
+    const uint32_t n = static_cast<uint32_t>(std::max<int64_t>(1, ceil_div(gs[i].n, most)));
+    const uint32_t leaf0 = static_cast<uint32_t>(t.leaves.size()), slot0 = static_cast<uint32_t>(t.nslots);
+    const uint32_t ti = static_cast<uint32_t>(i);
+    if (n > 1) t.nslots += n;
+    for (uint32_t k = 0; k < n; ++k) {
+      const int64_t at = k * most;
+      t.leaves.push_back({static_cast<const char*>(gs[i].g) + at * size,
+                          static_cast<uint32_t>(std::min(most, gs[i].n - at)), static_cast<int32_t>(gs[i].dtype),
+                          n > 1 ? slot0 + k : ti, kNone, n > 1 ? kNone : ti, 0});
+    }
+    owner[i] = {leaf0, kNone};
+    if (n > 1) {
+      norm_tree(t, slot0, n, ti, ti, [&](uint32_t c, uint32_t node) { t.leaves[leaf0 + c].parent = node; });
+      owner[i].node = static_cast<uint32_t>(t.nodes.size() - 1);
     }
   }
-  t.tensors[count] = NormTensor{nullptr, 0, 0, static_cast<uint32_t>(t.runs.size())};
-  t.first_run.push_back(static_cast<uint32_t>(t.runs.size()));
-  t.tensor_off = round_up(sizeof(Ticket) * tickets_of(t.nwg), kAlign);   // the tickets come first
-  t.run_off = round_up(t.tensor_off + sizeof(NormTensor) * t.tensors.size(), kAlign);
-  t.first_off = round_up(t.run_off + sizeof(NormRun) * t.runs.size(), kAlign);
-  t.table_bytes = round_up(t.first_off + sizeof(uint32_t) * t.first_run.size(), kAlign);
-  t.partial_off = t.table_bytes;
-  t.bytes = round_up(t.partial_off + sizeof(double) * t.runs.size(), kAlign);
+  if (count > 1) {
+    const uint32_t top = static_cast<uint32_t>(t.nslots++);
+    norm_tree(t, 0, static_cast<uint32_t>(count), top, kNone, [&](uint32_t c, uint32_t node) {
+      if (owner[c].node != kNone) t.nodes[owner[c].node].parent = node;
+      else t.leaves[owner[c].leaf].parent = node;
+    });
+  }
+  t.arrived_off = 0;
+  t.leaf_off = round_up(t.arrived_off + sizeof(Ticket) * t.nodes.size(), kAlign);
+  t.node_off = round_up(t.leaf_off + sizeof(NormLeaf) * t.leaves.size(), kAlign);
+  t.table_bytes = round_up(t.node_off + sizeof(NormNode) * t.nodes.size(), kAlign);
+  t.sum_off = t.table_bytes;
+  t.bytes = round_up(t.sum_off + sizeof(double) * t.nslots, kAlign);
   return MUON_OK;
 }
 
@@ -307,26 +340,22 @@ muon_status_t norm_prepare(const muon_grad_t* gs, int64_t count, float max_norm,
   if ((st = check_overlaps(rs, "tensor")) != MUON_OK) return st;
   if ((st = check_workspace(ws, ws_bytes, t.bytes, rs)) != MUON_OK) return st;
   table.assign(t.table_bytes, 0);
-  std::memcpy(table.data() + t.tensor_off, t.tensors.data(), sizeof(NormTensor) * t.tensors.size());
-  if (!t.runs.empty()) std::memcpy(table.data() + t.run_off, t.runs.data(), sizeof(NormRun) * t.runs.size());
-  std::memcpy(table.data() + t.first_off, t.first_run.data(), sizeof(uint32_t) * t.first_run.size());
+  std::memcpy(table.data() + t.leaf_off, t.leaves.data(), sizeof(NormLeaf) * t.leaves.size());
+  if (!t.nodes.empty()) std::memcpy(table.data() + t.node_off, t.nodes.data(), sizeof(NormNode) * t.nodes.size());
   return MUON_OK;
 }
 
 NormArgs norm_args(const NormTable& t, float max_norm, float* out, float* tensor_norms, void* ws) {
   char* base = static_cast<char*>(ws);
   NormArgs a{};
-  a.tensors = reinterpret_cast<const NormTensor*>(base + t.tensor_off);
-  a.runs = reinterpret_cast<const NormRun*>(base + t.run_off);
-  a.first_run = reinterpret_cast<const uint32_t*>(base + t.first_off);
-  a.partial = reinterpret_cast<double*>(base + t.partial_off);
-  a.tickets = reinterpret_cast<Ticket*>(base);
+  a.leaves = reinterpret_cast<const NormLeaf*>(base + t.leaf_off);
+  a.nodes = reinterpret_cast<const NormNode*>(base + t.node_off);
+  a.arrived = reinterpret_cast<Ticket*>(base + t.arrived_off);
+  a.sums = reinterpret_cast<double*>(base + t.sum_off);
   a.out = out;
   a.tensor_norms = tensor_norms;
   a.max_norm = max_norm;
-  a.ntensors = static_cast<uint32_t>(t.tensors.size() - 1);
-  a.nruns = static_cast<uint32_t>(t.runs.size());
-  a.nwg = t.nwg;
+  a.nleaves = static_cast<uint32_t>(t.leaves.size());
   return a;
 }
 

@@ -37,70 +37,70 @@ __device__ __forceinline__ void add_vector(double (&s)[2], uint4 u) {
   }
 }
 
-// This thread's share of a run: 16-byte vectors threadIdx.x + k * threads,
-// four in flight, then the elements behind the last whole vector.
+// This thread's share of a leaf: 16-byte vectors threadIdx.x + k * threads,
+// eight in flight, then the elements behind the last whole vector.
 template <bool BF16>
-__device__ __forceinline__ double run_sum(const void* g, int64_t begin, int64_t count) {
-  constexpr int V = BF16 ? 8 : 4, U = 4;
-  const char* base = static_cast<const char*>(g) + begin * (BF16 ? 2 : 4);
-  const MUON_GLOBAL uint4* q = reinterpret_cast<const MUON_GLOBAL uint4*>(gmem(base));
-  const int64_t nv = count / V;
+__device__ __forceinline__ double leaf_sum(const void* g, int count) {
+  constexpr int V = BF16 ? 8 : 4, U = kNormLeafBytes / (16 * kNormThreads);
+  const MUON_GLOBAL uint4* q = reinterpret_cast<const MUON_GLOBAL uint4*>(gmem(static_cast<const char*>(g)));
+  const int nv = count / V;
   double s[2] = {0.0, 0.0};
-  int64_t i = threadIdx.x;
-  for (; i + (U - 1) * kNormThreads < nv; i += U * kNormThreads) {
+  if (nv == U * kNormThreads) {
     uint4 u[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) u[k] = q[i + k * kNormThreads];
+    for (int k = 0; k < U; ++k) u[k] = q[threadIdx.x + k * kNormThreads];
 #pragma unroll
     for (int k = 0; k < U; ++k) add_vector<BF16>(s, u[k]);
+  } else {
+    for (int i = threadIdx.x; i < nv; i += kNormThreads) add_vector<BF16>(s, q[i]);
+    const int e = nv * V + threadIdx.x;
+    if (e < count) add_square(s[0], load_elem(g, e, BF16 ? DT_BF16 : DT_F32));
   }
-  for (; i < nv; i += kNormThreads) add_vector<BF16>(s, q[i]);
-  const int64_t e = nv * V + threadIdx.x;
-  if (e < count) add_square(s[0], load_elem(base, e, BF16 ? DT_BF16 : DT_F32));
   return s[0] + s[1];
 }
 
 __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
   __shared__ double red[4];
-  __shared__ bool last;
-  for (uint32_t r = a.first_run[blockIdx.x]; r < a.first_run[blockIdx.x + 1]; ++r) {
-    const NormRun run = a.runs[r];
-    const NormTensor& t = a.tensors[run.tensor];
-    const double part = t.dt == DT_BF16 ? run_sum<true>(t.g, run.begin, run.count)
-                                        : run_sum<false>(t.g, run.begin, run.count);
-    const double sum = block_sum(part, red);
-    if (threadIdx.x == 0) __hip_atomic_store(&a.partial[r], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const NormLeaf leaf = a.leaves[blockIdx.x];
+  const int count = static_cast<int>(leaf.count);
+  double sum = block_sum(leaf.dt == DT_BF16 ? leaf_sum<true>(leaf.g, count) : leaf_sum<false>(leaf.g, count), red);
+  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x;
+  uint32_t slot = leaf.slot, parent = leaf.parent, tensor = leaf.tensor;
+  for (;;) {
+    if (lane == 0 && tensor != kNone && a.tensor_norms) a.tensor_norms[tensor] = static_cast<float>(sqrt(sum));
+    if (parent == kNone) break;
+    // Sums are stored and loaded at agent scope, past the XCD's own L2, and
+    // each is complete before its owner counts itself; so the counter needs no
+    // release, which would write back the whole L2.
+    const NormNode node = a.nodes[parent];
+    uint32_t before = 0;
+    if (lane == 0) {
+      __hip_atomic_store(&a.sums[slot], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      before = __hip_atomic_fetch_add(&a.arrived[parent].count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    before = __builtin_amdgcn_readfirstlane(before);
+    if (before != node.children - 1) return;
+    asm volatile("" ::: "memory");
+    if (lane == 0) __hip_atomic_store(&a.arrived[parent].count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const double own = lane < static_cast<int>(node.children) ? load_partial(&a.sums[node.first + lane]) : 0.0;
+    sum = wave_sum_f64(own);
+    slot = node.slot;
+    parent = node.parent;
+    tensor = node.tensor;
   }
-  // The last workgroup to store its sums adds them all up.  The sums are
-  // stored and loaded at agent scope, past the XCD's own L2, and each is
-  // complete before its workgroup counts itself; so the counter needs no
-  // release, which would write back the whole L2.
-  if (threadIdx.x == 0) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    last = ticket_last(a.tickets, ticket_take(a.tickets));
-  }
-  __syncthreads();
-  if (!last) return;
-  double sum = 0.0;
-  for (uint32_t r = threadIdx.x; r < a.nruns; r += kNormThreads) sum += load_partial(&a.partial[r]);
-  sum = block_sum(sum, red);
-  if (threadIdx.x == 0) {
+  if (lane == 0) {
     const double norm = sqrt(sum);
     a.out[0] = static_cast<float>(norm);
     a.out[1] = norm <= a.max_norm ? 1.0f : static_cast<float>(a.max_norm / norm);
   }
-  if (a.tensor_norms)
-    for (uint32_t t = threadIdx.x; t < a.ntensors; t += kNormThreads) {
-      double own = 0.0;
-      for (uint32_t r = a.tensors[t].run0; r < a.tensors[t + 1].run0; ++r) own += load_partial(&a.partial[r]);
-      a.tensor_norms[t] = static_cast<float>(sqrt(own));
-    }
 }
 
 }  // namespace
 
 hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(k_grad_norm, dim3(a.nwg), dim3(kNormThreads), 0, s, a);
+  hipLaunchKernelGGL(k_grad_norm, dim3(a.nleaves), dim3(kNormThreads), 0, s, a);
   return hipGetLastError();
 }
 

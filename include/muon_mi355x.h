@@ -421,7 +421,8 @@ void adamw_plan_destroy(adamw_plan_t* plan);
  * Squares and sums are binary64 in an order that depends only on the sizes
  * and dtypes, so no float32 gradient overflows the sum and results repeat bit
  * for bit.  NaN gives N = NaN and out[1] = NaN; Inf gives N = Inf and 0.
- * A tensor with n = 0 has norm 0.  max_norm > 0; +Inf measures only.
+ * A tensor with n = 0 has norm 0.  max_norm > 0; +Inf measures only (out[1]
+ * is 1, or NaN).  At most 2^20 tensors, and 2^31 - 1 pieces of 32 KB.
  * The gradients may share memory; out and tensor_norms overlap no other
  * buffer.  Workspace, stream and capture rules are those of adamw_step and
  * of its plan.
