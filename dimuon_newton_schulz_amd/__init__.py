@@ -387,8 +387,15 @@ class LaunchTimer:
         return n
 
 
+# The current stream's handle without a Stream object around it (0.1 instead
+# of 2 us, of the 6 that a small step took), where torch has it.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream, device):
     if stream is None:
+        if _current_raw_stream is not None and device.index is not None:
+            return _current_raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

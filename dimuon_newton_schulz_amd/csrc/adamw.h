@@ -115,6 +115,7 @@ __device__ __forceinline__ bool ticket_last(Ticket* t, uint32_t seen) {
   const uint32_t members = mine + 1 < groups ? kTicketGroup : gridDim.x - mine * kTicketGroup;
   if (seen != members - 1) return false;
   __hip_atomic_store(&t[1 + mine].count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (groups == 1) return true;
   if (__hip_atomic_fetch_add(&t[0].count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != groups - 1) return false;
   __hip_atomic_store(&t[0].count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return true;
