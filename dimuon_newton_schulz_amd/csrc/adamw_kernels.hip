@@ -21,7 +21,7 @@ __device__ __forceinline__ V load_vec(const void* p, int k) {
 
 template <typename V>
 __device__ __forceinline__ void store_vec(void* p, int k, V v) {
-  reinterpret_cast<MUON_GLOBAL V*>(gmem(static_cast<char*>(p)))[k] = v;
+  __builtin_nontemporal_store(v, reinterpret_cast<MUON_GLOBAL V*>(gmem(static_cast<char*>(p))) + k);
 }
 
 template <bool BF16>
@@ -35,9 +35,19 @@ struct Raw8<false> {
   u32x4 a, b;
 };
 
-template <bool BF16, bool WHOLE>
+template <bool BF16, bool WHOLE, bool SPLIT = false>
 __device__ __forceinline__ Raw8<BF16> load8(const void* p, int lane, int cnt) {
   Raw8<BF16> r;
+  if constexpr (WHOLE && SPLIT) {
+    if constexpr (BF16) {
+      const u32x2 x = load_vec<u32x2>(p, lane), y = load_vec<u32x2>(p, lane + kAdamThreads);
+      r.a = u32x4{x[0], x[1], y[0], y[1]};
+    } else {
+      r.a = load_vec<u32x4>(p, lane);
+      r.b = load_vec<u32x4>(p, lane + kAdamThreads);
+    }
+    return r;
+  }
   if (WHOLE || cnt == 8) {
     if constexpr (BF16) {
       r.a = load_vec<u32x4>(p, lane);
@@ -81,10 +91,13 @@ __device__ __forceinline__ void floats8(const Raw8<BF16>& r, float (&out)[8]) {
   }
 }
 
-template <bool BF16, bool WHOLE>
+template <bool BF16, bool WHOLE, bool SPLIT = false>
 __device__ __forceinline__ void store8(void* p, int lane, int cnt, const float (&v)[8]) {
   if (WHOLE || cnt == 8) {
-    if constexpr (BF16) {
+    if constexpr (BF16 && WHOLE && SPLIT) {
+      store_vec(p, lane, u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+      store_vec(p, lane + kAdamThreads, u32x2{pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])});
+    } else if constexpr (BF16) {
       store_vec(p, lane, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                pack_bf16x2(v[6], v[7])});
     } else {
@@ -94,8 +107,8 @@ __device__ __forceinline__ void store8(void* p, int lane, int cnt, const float (
         a[k] = __float_as_uint(v[k]);
         b[k] = __float_as_uint(v[4 + k]);
       }
-      store_vec(p, 2 * lane, a);
-      store_vec(p, 2 * lane + 1, b);
+      store_vec(p, WHOLE && SPLIT ? lane : 2 * lane, a);
+      store_vec(p, WHOLE && SPLIT ? lane + kAdamThreads : 2 * lane + 1, b);
     }
     return;
   }
@@ -366,11 +379,11 @@ struct Group32 {
 template <bool WB, bool GB, bool MASTER, bool WHOLE>
 __device__ __forceinline__ void load_group(const AdamDesc& d, int64_t at, int left, Group32<WB, GB, MASTER>& x) {
   const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
-  x.g = load8<GB, WHOLE>(elem_at(d.g, at, GB ? 2 : 4), lane, cnt);
-  if constexpr (MASTER) x.w = load8<false, WHOLE>(elem_at(d.master, at, 4), lane, cnt);
-  else x.w = load8<WB, WHOLE>(elem_at(d.w, at, WB ? 2 : 4), lane, cnt);
-  x.m = load8<false, WHOLE>(elem_at(d.m, at, 4), lane, cnt);
-  x.v = load8<false, WHOLE>(elem_at(d.v, at, 4), lane, cnt);
+  x.g = load8<GB, WHOLE, true>(elem_at(d.g, at, GB ? 2 : 4), lane, cnt);
+  if constexpr (MASTER) x.w = load8<false, WHOLE, true>(elem_at(d.master, at, 4), lane, cnt);
+  else x.w = load8<WB, WHOLE, true>(elem_at(d.w, at, WB ? 2 : 4), lane, cnt);
+  x.m = load8<false, WHOLE, true>(elem_at(d.m, at, 4), lane, cnt);
+  x.v = load8<false, WHOLE, true>(elem_at(d.v, at, 4), lane, cnt);
 }
 
 template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, bool WHOLE>
@@ -385,10 +398,10 @@ __device__ __forceinline__ void step_group(const StepValues& s, const AdamDesc& 
   floats8(x.v, v);
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] = update(s, g[e], w[e], s.b1, s.b2, adam, decay, m[e], v[e]);
-  if constexpr (MASTER) store8<false, WHOLE>(elem_at(d.master, at, 4), lane, cnt, w);
-  store8<WB, WHOLE>(elem_at(d.w, at, WB ? 2 : 4), lane, cnt, w);
-  store8<false, WHOLE>(elem_at(d.m, at, 4), lane, cnt, m);
-  store8<false, WHOLE>(elem_at(d.v, at, 4), lane, cnt, v);
+  if constexpr (MASTER) store8<false, WHOLE, true>(elem_at(d.master, at, 4), lane, cnt, w);
+  store8<WB, WHOLE, true>(elem_at(d.w, at, WB ? 2 : 4), lane, cnt, w);
+  store8<false, WHOLE, true>(elem_at(d.m, at, 4), lane, cnt, m);
+  store8<false, WHOLE, true>(elem_at(d.v, at, 4), lane, cnt, v);
 }
 
 template <bool WB, bool GB, bool MASTER>
@@ -506,22 +519,39 @@ template <bool BLOCK8, bool BF16, bool WHOLE>
 __device__ __forceinline__ void get_group(const AdamDesc& d, int64_t at, int left, void* m_out, void* v_out) {
   const int lane = threadIdx.x, cnt = WHOLE ? 8 : count_of(left);
   constexpr int size = BF16 ? 2 : 4;
+  constexpr bool kSplit = !BF16;   // float32 values: four elements in each half of the group
   float m[8], v[8];
   if constexpr (BLOCK8) {
-    const int blk = (WHOLE || cnt > 0 ? 8 * lane : left - 1) / ADAMW_BLOCK;
-    const float ms = gmem(d.m_scale + at / ADAMW_BLOCK)[blk], vs = gmem(d.v_scale + at / ADAMW_BLOCK)[blk];
-    decode8(load_codes<WHOLE>(elem_at(d.m, at, 1), lane, cnt), load_codes<WHOLE>(elem_at(d.v, at, 1), lane, cnt), m, v);
+    const float *msp = d.m_scale + at / ADAMW_BLOCK, *vsp = d.v_scale + at / ADAMW_BLOCK;
+    float ms[2], vs[2];
+    if constexpr (WHOLE && kSplit) {
+      const void *mp = elem_at(d.m, at, 1), *vp = elem_at(d.v, at, 1);
+      decode8(u32x2{load_vec<uint32_t>(mp, lane), load_vec<uint32_t>(mp, lane + kAdamThreads)},
+              u32x2{load_vec<uint32_t>(vp, lane), load_vec<uint32_t>(vp, lane + kAdamThreads)}, m, v);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int blk = 4 * (lane + h * kAdamThreads) / ADAMW_BLOCK;
+        ms[h] = gmem(msp)[blk];
+        vs[h] = gmem(vsp)[blk];
+      }
+    } else {
+      decode8(load_codes<WHOLE>(elem_at(d.m, at, 1), lane, cnt), load_codes<WHOLE>(elem_at(d.v, at, 1), lane, cnt), m,
+              v);
+      const int blk = (WHOLE || cnt > 0 ? 8 * lane : left - 1) / ADAMW_BLOCK;
+      ms[0] = ms[1] = gmem(msp)[blk];
+      vs[0] = vs[1] = gmem(vsp)[blk];
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      m[e] *= ms;
-      v[e] *= vs;
+      m[e] *= ms[e >> 2];
+      v[e] *= vs[e >> 2];
     }
   } else {
-    floats8(load8<false, WHOLE>(elem_at(d.m, at, 4), lane, cnt), m);
-    floats8(load8<false, WHOLE>(elem_at(d.v, at, 4), lane, cnt), v);
+    floats8(load8<false, WHOLE, kSplit>(elem_at(d.m, at, 4), lane, cnt), m);
+    floats8(load8<false, WHOLE, kSplit>(elem_at(d.v, at, 4), lane, cnt), v);
   }
-  store8<BF16, WHOLE>(elem_at(m_out, d.first + at, size), lane, cnt, m);
-  store8<BF16, WHOLE>(elem_at(v_out, d.first + at, size), lane, cnt, v);
+  store8<BF16, WHOLE, kSplit>(elem_at(m_out, d.first + at, size), lane, cnt, m);
+  store8<BF16, WHOLE, kSplit>(elem_at(v_out, d.first + at, size), lane, cnt, v);
 }
 
 template <bool BLOCK8, bool BF16, bool WHOLE>
