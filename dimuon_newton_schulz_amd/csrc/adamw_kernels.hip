@@ -178,6 +178,7 @@ __device__ __forceinline__ uint32_t half_max(uint32_t v) {
 // following (y = v / vs, whose bits give the code).
 struct BlockScale {
   float ms, vs, minv, vinv;
+  float vden;      // 1 / vinv: vs * 2^-40 or vs * 2^24
   uint32_t voff;   // code offset << 20
 };
 
@@ -188,10 +189,20 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t mbits, uint32_t vbits
   b.minv = b.ms > 0.0f ? __builtin_amdgcn_rcpf(b.ms) : 0.0f;
   b.vs = __uint_as_float(vbits);
   const bool big = b.vs >= 1.0f;
-  b.vinv = big ? __builtin_amdgcn_rcpf(b.vs * 0x1p-40f) : __builtin_amdgcn_rcpf(b.vs * 0x1p32f) * 0x1p8f;
+  b.vden = b.vs * (big ? 0x1p-40f : 0x1p24f);
+  b.vinv = big ? __builtin_amdgcn_rcpf(b.vden) : __builtin_amdgcn_rcpf(b.vs * 0x1p32f) * 0x1p8f;
   if (vbits == 0) b.vinv = 0.0f;
   b.voff = big ? 1088u << 20 : 576u << 20;
   return b;
+}
+
+// x * inv, and with EXACT the quotient x / den that it stands for, to the last
+// bit but for rare halfway cases (one correction by the remainder).
+template <bool EXACT>
+__device__ __forceinline__ float quotient(float x, float den, float inv) {
+  const float q = x * inv;
+  if constexpr (!EXACT) return q;
+  return copysignf(__builtin_fmaf(__builtin_fmaf(-q, den, x), inv, q), x);   // -0 stays -0
 }
 
 // 16 * (upper half of h) + t, one instruction.
@@ -219,7 +230,9 @@ __device__ __forceinline__ int nonzero(float x) {
 // 4M values: equal in the normal range, and within 2^-20 of a code step of
 // the border below it).  The block's largest |m| and v are a few ulp off
 // their code's value at most, which neither rounding can carry to the next
-// code.
+// code.  A stochastic rounding may take quotients that are an ulp off
+// (its random number is coarser); nearest rounding takes exact ones, so that
+// values halfway between two codes (bf16 ones often are) round as stated.
 template <bool STOCHASTIC>
 __device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8], uint32_t hash0, u32x2& mc,
                                         u32x2& vc, float& ms, float& vs) {
@@ -255,13 +268,13 @@ __device__ __forceinline__ void encode8(const float (&m)[8], const float (&v)[8]
   uint32_t c[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    uint32_t rm = 0x80000000u, t = __float_as_uint(v[e] * b.vinv) + vadd;
+    uint32_t rm = 0x80000000u, t = __float_as_uint(quotient<!STOCHASTIC>(v[e], b.vden, b.vinv)) + vadd;
     if constexpr (STOCHASTIC) {
       const uint32_t h = adam_mix(hash0 + e);
       rm = h << 16 | 0x8000u;
       t = add_upper16(h, t);
     }
-    const float y = m[e] * b.minv;
+    const float y = quotient<!STOCHASTIC>(m[e], b.ms, b.minv);
     int& w = q[e >> 2];
     switch (e & 3) {
       case 0: w = __builtin_amdgcn_cvt_sr_fp8_f32(y, rm, w, 0); break;

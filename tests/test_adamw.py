@@ -580,6 +580,32 @@ def test_state_values(state, dtype):
 
 
 @gpu
+def test_loading_rounds_halfway_values_up():
+    """Every pair of bf16 mantissas as a block's largest value and an element:
+    quotients halfway between two codes, and next to halfway, at several
+    magnitudes.  Quotients of 8-bit mantissas that are not halfway differ from
+    it by 2^-16 of their value at least, so float32 quotients decide them all."""
+    announce("adamw halfway values")
+    mant = 1 + np.arange(128) / 128
+    for exp in (-60, -3, 0, 20):
+        # One block per largest value: 127 elements below it, from each of two binades.
+        rows = []
+        for top in mant:
+            below = np.concatenate([mant[mant < top], mant / 2, [0.0] * 128])[:255]
+            rows.append(np.concatenate([[top], below]))
+        x = np.ldexp(np.concatenate(rows), exp)
+        m = torch.from_numpy(np.where(np.arange(len(x)) % 3 == 0, -x, x)).to(torch.bfloat16).cuda()
+        v = torch.from_numpy(x).to(torch.bfloat16).cuda()
+        assert np.array_equal(host(v), x)
+        p = D.adamw_param(torch.zeros(len(x), device="cuda"), torch.zeros(len(x), device="cuda"), state="block8")
+        D.AdamWPlan([p], D.adamw_config_for([p])).set_state(m, v)
+        ms, vs = O.scales(host(m), host(v))
+        np.testing.assert_array_equal(host(p.m_scale), ms)
+        np.testing.assert_array_equal(host(p.m), O.encode_m(host(m), ms, 0.5))
+        np.testing.assert_array_equal(host(p.v), O.encode_v(host(v), vs, 0.5))
+
+
+@gpu
 def test_moving_between_32_and_8_bits():
     """A run with 32-bit moments goes on with 8-bit ones: every value within half a code step."""
     announce("adamw 32 to 8 bits")
