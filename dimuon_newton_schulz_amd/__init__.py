@@ -274,6 +274,12 @@ def _check_dtypes(params: Sequence[Param], cfg: StepConfig):
             t = getattr(p, name)
             if _DT_CODE.get(t.dtype) != code:
                 raise ValueError(f"matrix {i}: {name} is {t.dtype}, config says {getattr(cfg, name + '_dtype')}")
+    _check_scale_device(params, cfg)
+
+
+def _check_scale_device(params, cfg):
+    if cfg.grad_scale is not None and params and cfg.grad_scale.device != params[0].w.device:
+        raise ValueError(f"grad_scale is on {cfg.grad_scale.device}, the batch on {params[0].w.device}")
 
 
 def muon_workspace_bytes(params: Sequence[Param], cfg: StepConfig) -> int:
@@ -546,24 +552,28 @@ def _marshal_adamw(params: Sequence[AdamWParam], cfg: AdamWConfig):
                 raise ValueError(f"tensor {i}: {name} is {t.dtype}, expected {state_dt.get(name, torch.float32)}")
             setattr(arr[i], name, t.data_ptr())
         arr[i].n, arr[i].lr_scale, arr[i].weight_decay = n, float(p.lr_scale), float(p.weight_decay)
-    if cfg.grad_scale is not None and params and cfg.grad_scale.device != params[0].w.device:
-        raise ValueError(f"grad_scale is on {cfg.grad_scale.device}, the batch on {params[0].w.device}")
+    _check_scale_device(params, cfg)
     return arr
 
 
-def _workspace_tensor(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-
-
-def _stateless_workspace(workspace, nbytes, device, ts):
-    """The caller's workspace, or a new one that the allocator keeps until `ts` is done with it."""
+def _workspace_on(workspace, nbytes, device, ts):
+    """The caller's workspace, or a new one that the allocator keeps until
+    `ts` is done with it.  `ts` first waits for the current stream, where a new
+    block may have been in use a moment ago."""
+    current = torch.cuda.current_stream(device)
+    if ts != current:
+        ts.wait_stream(current)
     if workspace is None:
-        workspace = _workspace_tensor(nbytes, device)
-        if ts != torch.cuda.current_stream(device):
-            # The block may have been freed on the current stream a moment ago.
-            ts.wait_stream(torch.cuda.current_stream(device))
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if ts != current:
             workspace.record_stream(ts)
     return workspace
+
+
+def _gpu_device(device) -> torch.device:
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}: they must be on the GPU")
+    return device
 
 
 def adamw_workspace_bytes(params: Sequence[AdamWParam], cfg: AdamWConfig) -> int:
@@ -579,11 +589,12 @@ def adamw_step(params: Sequence[AdamWParam], cfg: AdamWConfig, step: int,
     ``stream``.  Returns the workspace.  Refused under stream capture."""
     lib = load_library()
     arr, c = _marshal_adamw(params, cfg), cfg.to_c()
-    device = params[0].w.device if params else None
     nbytes = ctypes.c_size_t(0)
     _check(lib.adamw_workspace_bytes(arr, len(params), ctypes.byref(c), ctypes.byref(nbytes)))
+    device = _gpu_device(params[0].w.device)
     ts = _torch_stream(stream, device)
-    workspace = _stateless_workspace(workspace, nbytes.value, device, ts)
+    if workspace is None:
+        workspace = _workspace_on(None, nbytes.value, device, ts)
     with torch.cuda.device(device):
         _check(lib.adamw_step(arr, len(params), ctypes.byref(c), step, workspace.data_ptr(), workspace.numel(),
                               ts.cuda_stream))
@@ -605,10 +616,10 @@ class AdamWPlan:
         _check(lib.adamw_workspace_bytes(arr, len(params), ctypes.byref(c), ctypes.byref(nbytes)))
         _check(lib.adamw_state_elems(arr, len(params), ctypes.byref(elems)))
         self.params, self.cfg = list(params), cfg
-        self.device = params[0].w.device
+        self.device = _gpu_device(params[0].w.device)
         self.state_elems = elems.value
         ts = _torch_stream(stream, self.device)
-        self.workspace = _stateless_workspace(workspace, nbytes.value, self.device, ts)
+        self.workspace = _workspace_on(workspace, nbytes.value, self.device, ts)
         with torch.cuda.device(self.device):
             _check(lib.adamw_plan_create(arr, len(params), ctypes.byref(c), step, self.workspace.data_ptr(),
                                          self.workspace.numel(), ts.cuda_stream, ctypes.byref(self._handle)))
@@ -692,7 +703,7 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = float("inf"), out
     grad_scale to the steps.  Refused under stream capture."""
     if not grads:
         raise ValueError("no gradients")
-    device = grads[0].device
+    device = _gpu_device(grads[0].device)
     ts = _torch_stream(stream, device)
     if out is None:
         with torch.cuda.stream(ts):
@@ -700,7 +711,8 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = float("inf"), out
     lib = load_library()
     arr, nbytes = _marshal_grads(grads, out, tensor_norms), ctypes.c_size_t(0)
     _check(lib.muon_grad_norm_workspace_bytes(arr, len(grads), ctypes.byref(nbytes)))
-    workspace = _stateless_workspace(workspace, nbytes.value, device, ts)
+    if workspace is None:
+        workspace = _workspace_on(None, nbytes.value, device, ts)
     with torch.cuda.device(device):
         _check(lib.muon_grad_norm(arr, len(grads), max_norm, out.data_ptr(), _ptr(tensor_norms),
                                   workspace.data_ptr(), workspace.numel(), ts.cuda_stream))
@@ -719,13 +731,13 @@ class GradNormPlan:
             raise ValueError("no gradients")
         self._handle = ctypes.c_void_p(0)
         self._lib = lib = load_library()
-        self.device = grads[0].device
+        self.device = _gpu_device(grads[0].device)
         self.grads, self.tensor_norms = list(grads), tensor_norms
         self.out = out if out is not None else torch.zeros(2, device=self.device)
         arr, nbytes = _marshal_grads(grads, self.out, tensor_norms), ctypes.c_size_t(0)
         _check(lib.muon_grad_norm_workspace_bytes(arr, len(grads), ctypes.byref(nbytes)))
         ts = _torch_stream(stream, self.device)
-        self.workspace = _stateless_workspace(workspace, nbytes.value, self.device, ts)
+        self.workspace = _workspace_on(workspace, nbytes.value, self.device, ts)
         with torch.cuda.device(self.device):
             _check(lib.muon_grad_norm_plan_create(arr, len(grads), max_norm, self.out.data_ptr(),
                                                   _ptr(tensor_norms), self.workspace.data_ptr(),

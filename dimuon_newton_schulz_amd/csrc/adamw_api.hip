@@ -14,7 +14,9 @@ namespace {
 
 constexpr int64_t kMaxTensors = int64_t{1} << 20;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
-constexpr int64_t kMaxUnits = (int64_t{1} << 31) - 1, kMaxLeaves = kMaxUnits;   // workgroups of one launch
+// Workgroups of one launch: its threads, 256 times as many, are below 2^32.
+constexpr int64_t kMaxUnits = (int64_t{1} << 24) - 1, kMaxLeaves = kMaxUnits;
+constexpr int64_t kMaxStep = int64_t{1} << 62;
 
 // Makes a plan's device current for one call.
 struct DeviceGuard {
@@ -131,7 +133,7 @@ muon_status_t adam_layout(const adamw_tensor_t* ts, int64_t count, AdamTable& t)
   }
   if (t.nunits > kMaxUnits) return fail(MUON_ERR_UNSUPPORTED, "the batch is too large");
   t.ticket_off = round_up(sizeof(AdamCtl), kAlign);
-  t.desc_off = round_up(t.ticket_off + sizeof(Ticket) * tickets_of(t.nunits), kAlign);
+  t.desc_off = round_up(t.ticket_off + sizeof(Ticket) * tickets_of(std::max<int64_t>(1, t.nunits)), kAlign);
   t.unit_off = round_up(t.desc_off + sizeof(AdamDesc) * count, kAlign);
   t.bytes = round_up(t.unit_off + sizeof(AdamUnit) * t.nunits, kAlign);
   return MUON_OK;
@@ -145,17 +147,11 @@ muon_status_t adam_prepare(const adamw_tensor_t* ts, int64_t count, const adamw_
   const bool block8 = cfg->state == ADAMW_STATE_BLOCK8;
   const size_t wsz = dtype_size(cfg->w_dtype), gsz = dtype_size(cfg->g_dtype), ssz = block8 ? 1 : 4;
   t.buffers.reserve(count * 7 + 1);
-  t.desc.resize(count);
-  t.units.reserve(t.nunits);
-  int64_t first = 0;
   bool any = false;
   for (int64_t i = 0; i < count; ++i) {
     const adamw_tensor_t& x = ts[i];
     if (!finite(x.lr_scale) || !finite(x.weight_decay))
       return fail(MUON_ERR_INVALID_ARG, "tensor %lld: lr_scale and weight_decay must be finite", (long long)i);
-    t.desc[i] = AdamDesc{x.w, x.g, x.m, x.v, x.m_scale, x.v_scale, x.master, x.n, first, x.lr_scale, x.weight_decay};
-    first += round_up(x.n, ADAMW_BLOCK);
-    for (int64_t u = 0; u < x.n / kAdamUnit; ++u) t.units.push_back({static_cast<uint32_t>(i), static_cast<uint32_t>(u)});
     if (x.n == 0) continue;
     const size_t n = static_cast<size_t>(x.n), blocks = ceil_div(x.n, ADAMW_BLOCK);
     if ((st = add_buffer(t.buffers, i, x.w, n * wsz, 16, "w", true)) != MUON_OK ||
@@ -175,15 +171,25 @@ muon_status_t adam_prepare(const adamw_tensor_t* ts, int64_t count, const adamw_
     any = true;
     if (master && (st = add_buffer(t.buffers, i, x.master, n * 4, 16, "master", true)) != MUON_OK) return st;
   }
-  for (int64_t i = 0; i < count; ++i)
-    if (ts[i].n % kAdamUnit)
-      t.units.push_back({static_cast<uint32_t>(i), static_cast<uint32_t>(ts[i].n / kAdamUnit)});
   if (cfg->grad_scale) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(cfg->grad_scale);
     t.buffers.push_back({lo, lo + 4, 0, "grad_scale", false});
   }
   if ((st = check_overlaps(t.buffers, "tensor")) != MUON_OK) return st;
   if ((st = check_workspace(ws, ws_bytes, t.bytes, t.buffers)) != MUON_OK) return st;
+
+  t.desc.reserve(count);
+  t.units.reserve(t.nunits);
+  int64_t first = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const adamw_tensor_t& x = ts[i];
+    t.desc.push_back({x.w, x.g, x.m, x.v, x.m_scale, x.v_scale, x.master, x.n, first, x.lr_scale, x.weight_decay});
+    first += round_up(x.n, ADAMW_BLOCK);
+    for (int64_t u = 0; u < x.n / kAdamUnit; ++u) t.units.push_back({static_cast<uint32_t>(i), static_cast<uint32_t>(u)});
+  }
+  for (int64_t i = 0; i < count; ++i)
+    if (ts[i].n % kAdamUnit)
+      t.units.push_back({static_cast<uint32_t>(i), static_cast<uint32_t>(ts[i].n / kAdamUnit)});
 
   ctl = AdamCtl{};
   ctl.t = done + 1;
@@ -449,7 +455,7 @@ muon_status_t adamw_step(const adamw_tensor_t* tensors, int64_t count, const ada
                          void* workspace, size_t workspace_bytes, void* stream) {
   using namespace muon;
   return guarded([&]() -> muon_status_t {
-    if (step < 1) return fail(MUON_ERR_INVALID_ARG, "step %lld < 1", (long long)step);
+    if (step < 1 || step > kMaxStep) return fail(MUON_ERR_INVALID_ARG, "step %lld outside [1, 2^62]", (long long)step);
     AdamTable t;
     AdamCtl ctl;
     std::vector<unsigned char> table;
@@ -470,7 +476,8 @@ muon_status_t adamw_plan_create(const adamw_tensor_t* tensors, int64_t count, co
   return guarded([&]() -> muon_status_t {
     if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
     *plan = nullptr;
-    if (steps_done < 0) return fail(MUON_ERR_INVALID_ARG, "steps_done %lld < 0", (long long)steps_done);
+    if (steps_done < 0 || steps_done >= kMaxStep)
+      return fail(MUON_ERR_INVALID_ARG, "steps_done %lld outside [0, 2^62)", (long long)steps_done);
     AdamTable t;
     AdamCtl ctl;
     std::vector<unsigned char> table;
@@ -527,7 +534,8 @@ muon_status_t adamw_plan_set_step(adamw_plan_t* plan, int64_t steps_done, void* 
   using namespace muon;
   return guarded([&]() -> muon_status_t {
     if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
-    if (steps_done < 0) return fail(MUON_ERR_INVALID_ARG, "steps_done %lld < 0", (long long)steps_done);
+    if (steps_done < 0 || steps_done >= kMaxStep)
+      return fail(MUON_ERR_INVALID_ARG, "steps_done %lld outside [0, 2^62)", (long long)steps_done);
     const DeviceGuard dev(plan->device);
     MUON_HIP_TRY(dev.err);
     AdamCtl c{};

@@ -366,7 +366,8 @@ __device__ __forceinline__ float update(const StepValues& s, float g, float w, f
 // Counts the workgroups that hold the step's values: called by every thread
 // (a barrier that waits for scalar loads only).  The count is looked at after
 // the step's work.
-__device__ __forceinline__ uint32_t have_values(const AdamArgs& a, const AdamCtl& c) {
+__device__ __forceinline__ uint32_t have_values(const AdamArgs& a, const AdamCtl& c, bool advance) {
+  if (!advance) return 0;   // nobody will write the next step's
   asm volatile("s_waitcnt lgkmcnt(0)" ::"s"(c.lr), "s"(c.rb1), "s"(c.rb2), "s"(c.key) : "memory");
   __builtin_amdgcn_s_barrier();
   return threadIdx.x == 0 ? ticket_take(a.tickets) : 0;
@@ -495,12 +496,12 @@ __device__ __forceinline__ void adamw_unit(const AdamArgs& a, bool advance) {
   // against 18.1 us with the moments' values).
   constexpr bool kLate = !Group::kBlock8;
   uint32_t seen = 0;
-  if constexpr (!kLate) seen = have_values(a, ctl);
+  if constexpr (!kLate) seen = have_values(a, ctl, advance);
   if (blockIdx.x < a.nwhole) {
 #pragma unroll
     for (int j = 0; j < kAdamGroups; ++j)
       load_group<WB, GB, MASTER, true>(d, at + j * kAdamGroup, kAdamGroup, x[j]);
-    if constexpr (kLate) seen = have_values(a, ctl);
+    if constexpr (kLate) seen = have_values(a, ctl, advance);
 #pragma unroll
     for (int j = 0; j < kAdamGroups; ++j)
       step_group<WB, GB, MASTER, STOCHASTIC, true>(s, d, at + j * kAdamGroup, kAdamGroup, x[j]);
@@ -508,7 +509,7 @@ __device__ __forceinline__ void adamw_unit(const AdamArgs& a, bool advance) {
     int64_t from = at;
     int left = static_cast<int>(d.n - at);
     load_group<WB, GB, MASTER, false>(d, from, left, x[0]);
-    if constexpr (kLate) seen = have_values(a, ctl);
+    if constexpr (kLate) seen = have_values(a, ctl, advance);
     for (;;) {
       step_group<WB, GB, MASTER, STOCHASTIC, false>(s, d, from, left, x[0]);
       from += kAdamGroup;

@@ -54,8 +54,8 @@
  *     batch) is copied into the workspace: muon_step and dimuon_step keep
  *     them per host thread, take one whose previous copy has completed or
  *     else allocate another (hipHostMalloc), up to 64 per thread, and free
- *     them when the thread exits; a plan holds one, freed by
- *     muon_plan_destroy.  The only host-side wait: a thread that already
+ *     them when the thread exits (adamw_step and muon_grad_norm take theirs
+ *     from the same pool); a plan holds one, freed by its destroy function.  The only host-side wait: a thread that already
  *     has 64 descriptor copies in flight waits for its oldest.
  *   - Every call is asynchronous on `stream` (a hipStream_t; NULL means the
  *     default stream).  Host-side validation runs before anything is
@@ -367,11 +367,12 @@ void adamw_config_default(adamw_config_t* cfg);
 
 /* Bytes of device workspace a call or a plan over this batch needs.
  * Errors: INVALID_ARG, DTYPE, UNSUPPORTED (n above 2^40, more than 2^20
- * tensors, more than 2^31 - 1 units of 2048 elements), MEMORY. */
+ * tensors, more than 2^24 - 1 units of 4096 elements), MEMORY. */
 muon_status_t adamw_workspace_bytes(const adamw_tensor_t* tensors, int64_t count,
                                     const adamw_config_t* cfg, size_t* bytes);
 
-/* One AdamW step over `count` tensors (host array); `step` is t, from 1 on.
+/* One AdamW step over `count` tensors (host array); `step` is t, from 1 on
+ * (at most 2^62).
  * Asynchronous on `stream`.  Uploads its descriptor table through a pinned
  * staging buffer, so it is refused while `stream` is being captured: capture
  * a plan's step instead.
@@ -395,7 +396,7 @@ muon_status_t adamw_plan_create(const adamw_tensor_t* tensors, int64_t count, co
 muon_status_t adamw_plan_step(adamw_plan_t* plan, void* stream);
 /* Learning rate of later steps (finite). */
 muon_status_t adamw_plan_set_lr(adamw_plan_t* plan, float lr, void* stream);
-/* Number of steps done, for resuming (>= 0). */
+/* Number of steps done, for resuming (>= 0, below 2^62). */
 muon_status_t adamw_plan_set_step(adamw_plan_t* plan, int64_t steps_done, void* stream);
 /* The moments as values, for checkpoints and for moving between 32- and 8-bit
  * moments.  `m` and `v` are device buffers of adamw_state_elems() elements of
@@ -422,7 +423,7 @@ void adamw_plan_destroy(adamw_plan_t* plan);
  * and dtypes, so no float32 gradient overflows the sum and results repeat bit
  * for bit.  NaN gives N = NaN and out[1] = NaN; Inf gives N = Inf and 0.
  * A tensor with n = 0 has norm 0.  max_norm > 0; +Inf measures only (out[1]
- * is 1, or NaN).  At most 2^20 tensors, and 2^31 - 1 pieces of 32 KB.
+ * is 1, or NaN).  At most 2^20 tensors, and 2^24 - 1 pieces of 32 KB.
  * The gradients may share memory; out and tensor_norms overlap no other
  * buffer.  Workspace, stream and capture rules are those of adamw_step and
  * of its plan.
