@@ -15,7 +15,7 @@ namespace {
 constexpr int64_t kMaxTensors = int64_t{1} << 20;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
 // Workgroups of one launch: its threads, 256 times as many, are below 2^32.
-constexpr int64_t kMaxUnits = (int64_t{1} << 24) - 1, kMaxLeaves = kMaxUnits;
+constexpr int64_t kMaxLeaves = (int64_t{1} << 24) - 1, kMaxUnits = kMaxLeaves / kAdamGroups;
 constexpr int64_t kMaxStep = int64_t{1} << 62;
 
 // Makes a plan's device current for one call.

@@ -611,32 +611,28 @@ __device__ __forceinline__ void set_group(const AdamDesc& d, int64_t at, int lef
   }
 }
 
-// Calls whole(desc, at) or part(desc, at, left) for each group of this
-// workgroup's unit.
+// Calls whole(desc, at) or part(desc, at, left) for this workgroup's group
+// (kAdamGroups workgroups to a unit).
 template <typename Whole, typename Part>
-__device__ __forceinline__ void each_group(const AdamArgs& a, Whole whole, Part part) {
-  const AdamUnit u = a.units[blockIdx.x];
+__device__ __forceinline__ void one_group(const AdamArgs& a, Whole whole, Part part) {
+  const uint32_t k = blockIdx.x / kAdamGroups;
+  const AdamUnit u = a.units[k];
   const AdamDesc& d = a.desc[u.tensor];
-  const int64_t at = static_cast<int64_t>(u.unit) * kAdamUnit;
-  if (blockIdx.x < a.nwhole) {
-#pragma unroll
-    for (int j = 0; j < kAdamGroups; ++j) whole(d, at + j * kAdamGroup);
-  } else {
-    for (int left = static_cast<int>(d.n - at), j = 0; left > 0; left -= kAdamGroup, ++j)
-      part(d, at + j * kAdamGroup, left);
-  }
+  const int64_t at = static_cast<int64_t>(u.unit) * kAdamUnit + blockIdx.x % kAdamGroups * kAdamGroup;
+  if (k < a.nwhole) whole(d, at);
+  else if (d.n > at) part(d, at, static_cast<int>(min(d.n - at, static_cast<int64_t>(kAdamGroup))));
 }
 
 template <bool BLOCK8, bool BF16>
 __global__ __launch_bounds__(kAdamThreads) void k_get(AdamArgs a, void* m, void* v) {
-  each_group(
+  one_group(
       a, [&](const AdamDesc& d, int64_t at) { get_group<BLOCK8, BF16, true>(d, at, kAdamGroup, m, v); },
       [&](const AdamDesc& d, int64_t at, int left) { get_group<BLOCK8, BF16, false>(d, at, left, m, v); });
 }
 
 template <bool BLOCK8, bool BF16>
 __global__ __launch_bounds__(kAdamThreads) void k_set(AdamArgs a, const void* m, const void* v) {
-  each_group(
+  one_group(
       a, [&](const AdamDesc& d, int64_t at) { set_group<BLOCK8, BF16, true>(d, at, kAdamGroup, m, v); },
       [&](const AdamDesc& d, int64_t at, int left) { set_group<BLOCK8, BF16, false>(d, at, left, m, v); });
 }
@@ -681,7 +677,7 @@ hipError_t launch_adamw_ctl(AdamCtl* ctl, const AdamCtl& value, bool set_step, h
 
 hipError_t launch_adamw_get(const AdamArgs& a, void* m, void* v, int32_t dt, hipStream_t s) {
   if (a.nunits == 0) return hipSuccess;
-  const dim3 grid(a.nunits), threads(kAdamThreads);
+  const dim3 grid(a.nunits * kAdamGroups), threads(kAdamThreads);
   const bool bf16 = dt == DT_BF16;
   if (a.block8) {
     if (bf16) hipLaunchKernelGGL((k_get<true, true>), grid, threads, 0, s, a, m, v);
@@ -695,7 +691,7 @@ hipError_t launch_adamw_get(const AdamArgs& a, void* m, void* v, int32_t dt, hip
 
 hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int32_t dt, hipStream_t s) {
   if (a.nunits == 0) return hipSuccess;
-  const dim3 grid(a.nunits), threads(kAdamThreads);
+  const dim3 grid(a.nunits * kAdamGroups), threads(kAdamThreads);
   const bool bf16 = dt == DT_BF16;
   if (a.block8) {
     if (bf16) hipLaunchKernelGGL((k_set<true, true>), grid, threads, 0, s, a, m, v);

@@ -367,7 +367,7 @@ void adamw_config_default(adamw_config_t* cfg);
 
 /* Bytes of device workspace a call or a plan over this batch needs.
  * Errors: INVALID_ARG, DTYPE, UNSUPPORTED (n above 2^40, more than 2^20
- * tensors, more than 2^24 - 1 units of 4096 elements), MEMORY. */
+ * tensors, more than 2^23 - 1 units of 4096 elements), MEMORY. */
 muon_status_t adamw_workspace_bytes(const adamw_tensor_t* tensors, int64_t count,
                                     const adamw_config_t* cfg, size_t* bytes);
 
