@@ -654,7 +654,9 @@ class AdamWPlan:
                   dtype: torch.dtype = torch.float32, stream=None):
         """The moments as values, (m, v): flat buffers of state_elems elements
         (new ones of `dtype`, zero in the gaps, if none are given)."""
-        if m is None and v is None:
+        if (m is None) != (v is None):
+            raise ValueError("give both m and v, or neither")
+        if m is None:
             with torch.cuda.stream(_torch_stream(stream, self.device)):
                 m, v = (torch.zeros(self.state_elems, dtype=dtype, device=self.device) for _ in range(2))
         _check(self._lib.adamw_plan_get_state(self._handle, *self._values(m, v),

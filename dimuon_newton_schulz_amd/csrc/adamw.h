@@ -158,7 +158,7 @@ struct alignas(32) NormLeaf {
 };
 
 struct alignas(32) NormNode {
-  uint32_t first, children;   // slots of the children's sums
+  uint32_t first, children;   // the children's sums are in slots first, first + 1, ...
   uint32_t slot, parent, tensor;
   uint32_t reserved0[3];
 };
@@ -172,6 +172,7 @@ struct NormArgs {
   float* tensor_norms;         // or NULL
   float max_norm;
   uint32_t nleaves;
+  int32_t stream;              // the gradients do not fit the Infinity Cache
 };
 
 hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s);

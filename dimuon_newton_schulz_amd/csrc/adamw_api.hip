@@ -244,6 +244,7 @@ struct NormTable {
   std::vector<NormLeaf> leaves;
   std::vector<NormNode> nodes;
   size_t nslots = 0;
+  int64_t grad_bytes = 0;
   size_t leaf_off = 0, node_off = 0, arrived_off = 0, sum_off = 0, table_bytes = 0, bytes = 0;
 };
 
@@ -293,6 +294,7 @@ muon_status_t norm_layout(const muon_grad_t* gs, int64_t count, NormTable& t) {
   std::vector<Owner> owner(count);
   for (int64_t i = 0; i < count; ++i) {
     const int64_t size = dtype_size(gs[i].dtype), most = kNormLeafBytes / size;
+    t.grad_bytes += gs[i].n * size;
     const uint32_t n = static_cast<uint32_t>(std::max<int64_t>(1, ceil_div(gs[i].n, most)));
     const uint32_t leaf0 = static_cast<uint32_t>(t.leaves.size()), slot0 = static_cast<uint32_t>(t.nslots);
     const uint32_t ti = static_cast<uint32_t>(i);
@@ -362,6 +364,7 @@ NormArgs norm_args(const NormTable& t, float max_norm, float* out, float* tensor
   a.tensor_norms = tensor_norms;
   a.max_norm = max_norm;
   a.nleaves = static_cast<uint32_t>(t.leaves.size());
+  a.stream = t.grad_bytes > (int64_t{256} << 20) ? 1 : 0;
   return a;
 }
 

@@ -6,10 +6,24 @@ namespace muon {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Eight consecutive elements per thread, raw as loaded: 16 bytes of bf16 or 32
-// of float32, eight code bytes.  p is the group's base (the same for the
-// whole workgroup) and `lane` the thread in it.  In a group that is not WHOLE, only
-// `cnt` of the eight exist; the others read as zero and are not written.
+// Eight elements per thread of a group, raw as loaded.  p is the group's base
+// (the same for the whole workgroup) and `lane` the thread in it.  In a group
+// that is not WHOLE, only `cnt` of the eight exist; the others read as zero
+// and are not written.
+//
+// The eight are consecutive: 16 bytes of bf16 or 32 of float32, eight code
+// bytes.  With SPLIT (whole groups only) a thread has four elements in each
+// half of the group, so that a float32 access takes 16 bytes from each lane
+// and neighbouring lanes touch neighbouring bytes.  Float32 stores of 32 bytes
+// a lane in two halves fill half a line each: writing 39M moments as float32
+// took 127 us that way with non-temporal stores and 103 us with plain ones,
+// and takes 57 us with SPLIT.  The 8-bit step keeps its eight together, which
+// makes its code accesses eight bytes long.
+//
+// Stores are non-temporal: nothing that a step writes is read again by it.
+// 39M elements with 8-bit moments and float32 master weights: 172 us with
+// plain stores, 153 us with these; loads past the caches were slower (215
+// against 238 us with 32-bit moments).
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -153,7 +167,7 @@ __device__ __forceinline__ const void* elem_at(const void* p, int64_t at, int si
 // ---------------------------------------------------------------------------
 // 8-bit moments.  A block of 256 elements is half a wave's: 32 lanes of eight
 // elements (16-byte bf16 and 8-byte code accesses; a block's maximum takes
-// four DPP steps and one exchange of 16-lane rows).
+// four DPP steps and one exchange of 16-lane rows, no LDS and no barrier).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kInfBits = 0x7F800000u;
 
@@ -479,9 +493,25 @@ __device__ __forceinline__ void step_group(const StepValues& s, const AdamDesc& 
   }
 }
 
+// The step reads and writes each element once and does 17 (32-bit moments) to
+// 48 (8-bit, stochastic) vector instructions on it: memory bounds it, and for
+// 8-bit moments the vector units are about three quarters busy beside it (the
+// square root, the reciprocal and the hash's two products run at a quarter of
+// the rate).
+//   369M elements, bf16 weights and gradients
+//     32-bit moments, 22 bytes an element    1511 us, 5.4 TB/s
+//      8-bit moments, 10 bytes an element     657 us, 5.6 TB/s
+//   39M elements, bf16 with float32 master weights
+//     32-bit moments, 28 bytes                207 us, 5.3 TB/s
+//      8-bit moments, 16 bytes                117 us, 5.4 TB/s
+// A kernel that only streams through four arrays and writes three of them back
+// reaches 5.3 to 5.4 TB/s here.
+//
 // One workgroup per unit, in the order of memory: measured against workgroups
-// that walk several units each (1024 to 16384 of them, interleaved), which
-// reach 4.6 to 5.1 TB/s with these streams where this reaches 5.3.
+// that walk several units each (1024 to 16384 of them, interleaved, the next
+// unit's operands loaded ahead), which reach 4.6 to 5.1 TB/s.  Two groups a
+// unit against one: 32-bit 1515 against 1540 us, 8-bit with its values 1076
+// against 1122 us.
 template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, typename Group>
 __device__ __forceinline__ void adamw_unit(const AdamArgs& a, bool advance) {
   const AdamCtl ctl = *a.ctl;
@@ -545,7 +575,11 @@ __global__ void k_ctl(AdamCtl* ctl, AdamCtl value, bool set_step) {
 }
 
 // ---------------------------------------------------------------------------
-// The moments as values
+// The moments as values.  Memory bounds both directions.
+//   8-bit codes of 39M elements to float32: 56 us, 7.0 TB/s (the Infinity Cache
+//     takes part of the writes)
+//   8-bit codes of 369M elements to bf16:  430 us, 5.1 TB/s
+//   float32 values of 369M elements to codes: 630 us, 5.9 TB/s
 // ---------------------------------------------------------------------------
 template <bool BLOCK8, bool BF16, bool WHOLE>
 __device__ __forceinline__ void get_group(const AdamDesc& d, int64_t at, int left, void* m_out, void* v_out) {

@@ -643,6 +643,8 @@ def test_state_value_buffers_are_checked():
     for bad in (torch.zeros(1000, device="cuda"), ok.double(), ok.cpu()):
         with pytest.raises(ValueError):
             plan.get_state(bad, ok)
+    with pytest.raises(ValueError):
+        plan.get_state(ok)
     with pytest.raises(D.MuonError) as e:
         plan.get_state(ok, ok)
     assert e.value.status == 4
