@@ -37,9 +37,9 @@ PEAK_TFLOPS = {"bf16": 2516.6, "f32": 157.3}
 # profiles/k_thin_lora_batch_64x8x4096.md.
 THIN_SOURCES = ("dimuon_newton_schulz_amd/csrc/thin_kernel.hip", "dimuon_newton_schulz_amd/csrc/common.h")
 MEASURED_TRAFFIC = {
-    "sources_sha256": "e35e3c4802044f21fb56a03786e5766071f0f5d903b32c8d9217c7ef0e710aeb",
-    "k_thin_a": {"fetch_kib": 17684.7, "write_kib": 19012.0},
-    "k_thin_b": {"fetch_kib": 18036.1, "write_kib": 18468.0},
+    "sources_sha256": "1935fcf05273d32f61e2ee157c5424836b783d2bab78dab4182c1a8f7c4b7a2c",
+    "k_thin_a": {"fetch_kib": 17703.5, "write_kib": 19012.0},
+    "k_thin_b": {"fetch_kib": 18039.1, "write_kib": 18468.0},
 }
 FETCH_SCALE, WRITE_SCALE = 2.0, 1.0
 
@@ -54,13 +54,13 @@ FETCH_SCALE, WRITE_SCALE = 2.0, 1.0
 GEMM_SOURCES = ("dimuon_newton_schulz_amd/csrc/gemm_kernels.hip", "dimuon_newton_schulz_amd/csrc/api.hip",
                 "dimuon_newton_schulz_amd/csrc/common.h")
 MEASURED_GEMM = {
-    "sources_sha256": "cf7e0845c718b4c011d8f77514d35717d007443866948b486c52999ccee92a78",
-    "gpt2_small_12x4_bf16": {"fetch_kib": [134273.6, 5270.3], "write_kib": [163840.1, 2048.0],
-                             "mfma_busy_frac": 0.363, "clock_ghz": 2.17},
-    "square_8x4096x4096_bf16": {"fetch_kib": [786652.0], "write_kib": [262231.2],
-                                "mfma_busy_frac": 0.573, "clock_ghz": 1.94},
-    "moe_64x(2048x1408+1408x2048)_bf16": {"fetch_kib": [968372.0], "write_kib": [786466.5],
-                                          "mfma_busy_frac": 0.475, "clock_ghz": 1.92},
+    "sources_sha256": "571eeb26874eb9228cd356fda852d9304cf5a583545c81150ad7052ca59dffb0",
+    "gpt2_small_12x4_bf16": {"fetch_kib": [134378.0, 5270.3], "write_kib": [163840.0, 2048.0],
+                             "mfma_busy_frac": 0.361, "clock_ghz": 2.19},
+    "square_8x4096x4096_bf16": {"fetch_kib": [786599.0], "write_kib": [262215.0],
+                                "mfma_busy_frac": 0.571, "clock_ghz": 2.00},
+    "moe_64x(2048x1408+1408x2048)_bf16": {"fetch_kib": [969355.0], "write_kib": [786463.0],
+                                          "mfma_busy_frac": 0.472, "clock_ghz": 1.93},
 }
 
 
