@@ -2,7 +2,9 @@
 // descriptor tables, launches, plans.
 #include <algorithm>
 #include <cmath>
+#include <memory>
 #include <new>
+#include <stdexcept>
 #include <vector>
 
 #include "adamw.h"
@@ -487,22 +489,17 @@ muon_status_t adamw_plan_create(const adamw_tensor_t* tensors, int64_t count, co
     muon_status_t st = adam_prepare(tensors, count, cfg, steps_done, workspace, workspace_bytes, t, ctl, table);
     if (st != MUON_OK) return st;
     if ((st = refuse_capture(static_cast<hipStream_t>(stream))) != MUON_OK) return st;
-    adamw_plan* pl = new adamw_plan();
+    std::unique_ptr<adamw_plan, void (*)(adamw_plan*)> pl(new adamw_plan(), adamw_plan_destroy);
     const hipError_t e = hipGetDevice(&pl->device);
-    if (e != hipSuccess) st = fail(MUON_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
-    if (st == MUON_OK) st = pl->staging.upload(table, workspace, static_cast<hipStream_t>(stream));
-    if (st != MUON_OK) {
-      pl->staging.release();
-      delete pl;
-      return st;
-    }
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
+    if ((st = pl->staging.upload(table, workspace, static_cast<hipStream_t>(stream))) != MUON_OK) return st;
     pl->cfg = *cfg;
     pl->args = adam_args(t, *cfg, workspace);
     pl->elems = t.elems;
     pl->buffers.swap(t.buffers);
     const uintptr_t lo = reinterpret_cast<uintptr_t>(workspace);
     pl->buffers.push_back({lo, lo + t.bytes, 0, "workspace", true});
-    *plan = pl;
+    *plan = pl.release();
     return MUON_OK;
   });
 }
@@ -623,17 +620,12 @@ muon_status_t muon_grad_norm_plan_create(const muon_grad_t* grads, int64_t count
     muon_status_t st = norm_prepare(grads, count, max_norm, out, tensor_norms, workspace, workspace_bytes, t, table);
     if (st != MUON_OK) return st;
     if ((st = refuse_capture(static_cast<hipStream_t>(stream))) != MUON_OK) return st;
-    muon_grad_norm_plan* pl = new muon_grad_norm_plan();
+    std::unique_ptr<muon_grad_norm_plan, void (*)(muon_grad_norm_plan*)> pl(new muon_grad_norm_plan(), muon_grad_norm_plan_destroy);
     const hipError_t e = hipGetDevice(&pl->device);
-    if (e != hipSuccess) st = fail(MUON_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
-    if (st == MUON_OK) st = pl->staging.upload(table, workspace, static_cast<hipStream_t>(stream));
-    if (st != MUON_OK) {
-      pl->staging.release();
-      delete pl;
-      return st;
-    }
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
+    if ((st = pl->staging.upload(table, workspace, static_cast<hipStream_t>(stream))) != MUON_OK) return st;
     pl->args = norm_args(t, max_norm, out, tensor_norms, workspace);
-    *plan = pl;
+    *plan = pl.release();
     return MUON_OK;
   });
 }

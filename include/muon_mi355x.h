@@ -271,8 +271,9 @@ void muon_plan_destroy(muon_plan_t* plan);
  * (decoupled weight decay, as in muon_step; the sitech.ge Muon blog and "From
  * PCG to Muon" leave the parameters that are not hidden matrices to AdamW).
  * All arithmetic is in binary32 (a v_t below 2^-126 counts as zero under the
- * root); the weight is rounded to its dtype once, at the end, to nearest even.  With `master`, w_{t-1} is read from the float32
- * master copy, which takes w_t unrounded, and w is only written.
+ * root); the weight is rounded to its dtype once, at the end, to nearest even.
+ * With `master`, w_{t-1} is read from the float32 master copy, which takes w_t
+ * unrounded, and w is only written.
  *
  * Moments in 32 bits (ADAMW_STATE_F32): m and v are float32, n elements each.
  *

@@ -750,6 +750,36 @@ def test_steps_repeat_on_another_stream_and_captured(state):
 
 
 @gpu
+def test_one_plan_in_two_graphs_and_eager_steps_between():
+    """Two captured graphs of one plan share its workspace: replays of either,
+    with eager steps between them, are the next steps."""
+    announce("adamw two graphs of one plan")
+    a, b = (tensors(SIZES + [300000], "bf16", "f32", "block8", False, seed=41) for _ in range(2))
+    plans = [D.AdamWPlan(x, D.adamw_config_for(x, seed=9)) for x in (a, b)]
+    norms = [D.GradNormPlan([p.g for p in x], 1e-3) for x in (a, b)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    torch.cuda.synchronize()
+    for g in graphs:
+        with torch.cuda.graph(g):
+            norms[1].run()
+            plans[1].step()
+    for how in (0, 1, 1, "eager", 0, "eager", 1, 0):
+        norms[0].run()
+        plans[0].step()
+        if how == "eager":
+            norms[1].run()
+            plans[1].step()
+        else:
+            graphs[how].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(norms[0].out, norms[1].out)
+        for p, q in zip(a, b):
+            for name in ("w", "m", "v", "m_scale", "v_scale"):
+                x, y = getattr(p, name), getattr(q, name)
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)) if x.numel() else True, (how, name)
+
+
+@gpu
 @pytest.mark.parametrize("variant", ["muon", "dimuon"])
 @pytest.mark.parametrize("nesterov", [False, True])
 def test_grad_scale_in_muon_equals_scaled_gradients(variant, nesterov):
