@@ -651,7 +651,7 @@ template <typename Whole, typename Part>
 __device__ __forceinline__ void one_group(const AdamArgs& a, Whole whole, Part part) {
   const uint32_t k = blockIdx.x / kAdamGroups;
   const AdamUnit u = a.units[k];
-  const AdamDesc& d = a.desc[u.tensor];
+  const AdamDesc d = a.desc[u.tensor];
   const int64_t at = static_cast<int64_t>(u.unit) * kAdamUnit + blockIdx.x % kAdamGroups * kAdamGroup;
   if (k < a.nwhole) whole(d, at);
   else if (d.n > at) part(d, at, static_cast<int>(min(d.n - at, static_cast<int64_t>(kAdamGroup))));
