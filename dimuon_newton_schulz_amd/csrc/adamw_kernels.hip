@@ -499,19 +499,20 @@ __device__ __forceinline__ void step_group(const StepValues& s, const AdamDesc& 
 // square root, the reciprocal and the hash's two products run at a quarter of
 // the rate).
 //   369M elements, bf16 weights and gradients
-//     32-bit moments, 22 bytes an element    1511 us, 5.4 TB/s
-//      8-bit moments, 10 bytes an element     657 us, 5.6 TB/s
+//     32-bit moments, 22 bytes an element   1337 us, 6.1 TB/s
+//      8-bit moments, 10 bytes an element    610 us, 6.1 TB/s
 //   39M elements, bf16 with float32 master weights
-//     32-bit moments, 28 bytes                207 us, 5.3 TB/s
-//      8-bit moments, 16 bytes                117 us, 5.4 TB/s
+//     32-bit moments, 28 bytes               192 us, 5.8 TB/s
+//      8-bit moments, 16 bytes               109 us, 5.8 TB/s
 // A kernel that only streams through four arrays and writes three of them back
-// reaches 5.3 to 5.4 TB/s here.
+// reaches 6.0 TB/s on the same card.  (Cards differ: on another one the large
+// 32-bit step took 1511 us and that kernel reached 5.4 TB/s.)
 //
 // One workgroup per unit, in the order of memory: measured against workgroups
 // that walk several units each (1024 to 16384 of them, interleaved, the next
-// unit's operands loaded ahead), which reach 4.6 to 5.1 TB/s.  Two groups a
-// unit against one: 32-bit 1515 against 1540 us, 8-bit with its values 1076
-// against 1122 us.
+// unit's operands loaded ahead), which reached 4.6 to 5.1 TB/s where this
+// reached 5.4.  Two groups a unit against one: 32-bit 1515 against 1540 us,
+// 8-bit with its values 1076 against 1122 us (the slower card).
 template <bool WB, bool GB, bool MASTER, bool STOCHASTIC, typename Group>
 __device__ __forceinline__ void adamw_unit(const AdamArgs& a, bool advance) {
   const AdamCtl ctl = *a.ctl;
@@ -578,8 +579,8 @@ __global__ void k_ctl(AdamCtl* ctl, AdamCtl value, bool set_step) {
 // The moments as values.  Memory bounds both directions.
 //   8-bit codes of 39M elements to float32: 56 us, 7.0 TB/s (the Infinity Cache
 //     takes part of the writes)
-//   8-bit codes of 369M elements to bf16:  430 us, 5.1 TB/s
-//   float32 values of 369M elements to codes: 630 us, 5.9 TB/s
+//   8-bit codes of 369M elements to bf16: 357 us, 6.2 TB/s
+//   float32 values of 369M elements to codes: 613 us, 6.0 TB/s
 // ---------------------------------------------------------------------------
 template <bool BLOCK8, bool BF16, bool WHOLE>
 __device__ __forceinline__ void get_group(const AdamDesc& d, int64_t at, int left, void* m_out, void* v_out) {
