@@ -139,12 +139,15 @@ hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int
 // Global gradient norm
 // ---------------------------------------------------------------------------
 // Every workgroup sums a stretch of one tensor (a leaf).  The sums meet in a
-// tree of nodes with at most 64 children: the last child to store its sum
-// adds up its siblings', one per lane, and goes on to the parent.  A tensor's
-// sum is the value of one leaf or node.
+// tree of nodes with at most 128 children: the last child to store its sum
+// adds up its siblings', two per lane, and goes on to the parent.  A tensor's
+// sum is the value of one leaf or node.  A level costs about 1 us, and a
+// node's counter 14 ns a child where all arrive at once: 128 tensors of 4
+// leaves take 7.0 us with 64 children a node (three levels), 6.2 with 128
+// (two) and 6.3 with 256; 128 tensors of 176 leaves 117, 116 and 118.5 us.
 constexpr int kNormThreads = 256;
 constexpr int kNormLeafBytes = 32768;
-constexpr int kNormChildren = 64;
+constexpr int kNormChildren = 128;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 struct alignas(32) NormLeaf {

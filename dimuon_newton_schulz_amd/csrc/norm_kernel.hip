@@ -66,15 +66,15 @@ __device__ __forceinline__ double leaf_sum(const void* g, int count) {
 // Reads every element once, and squares and adds it in binary64 (which no
 // float32 value overflows; a conversion and a product-sum an element, hidden
 // behind the reads).
-//   369M bf16: 117 us, 6.3 TB/s (a kernel that only reads reaches 7.4)
-//   4M float32 in 128 tensors: 7 to 8 us, of which 3 for the tree's three levels
+//   369M bf16: 116 us, 6.4 TB/s (a kernel that only reads reaches 7.4 to 7.7)
+//   4M float32 in 128 tensors: 6.2 us, of which 2 for the tree's two levels
 // Against 2048 workgroups with long stretches and one that adds up all sums:
-// 140 and 11.8 us.  Leaves of 16 KB took 7.3 and 126 us, of 64 KB 7.0 and 135
-// (both before STREAM), against 7.0 and 130.
+// 140 and 11.8 us.  Leaves of 16 KB took 126 and 7.3 us, of 64 KB 135 and 7.0
+// (both before STREAM and with 64 children a node), against 130 and 7.0.
 //
 // STREAM: the gradients do not fit the 256 MB Infinity Cache, and are read
 // past it (non-temporal).  369M bf16: 130 us without, 118 us with; 4M float32,
-// which fit: 7.0 us without, 7.2 to 8 with.
+// which fit: 7.0 us without, 7.2 to 8 with (64 children a node).
 template <bool STREAM>
 __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
   __shared__ double red[4];
@@ -103,8 +103,16 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
     if (before != node.children - 1) return;
     asm volatile("" ::: "memory");
     if (lane == 0) __hip_atomic_store(&a.arrived[parent].count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const double own = lane < static_cast<int>(node.children) ? load_partial(&a.sums[node.first + lane]) : 0.0;
-    sum = wave_sum_f64(own);
+    double own[kNormChildren / 64];
+#pragma unroll
+    for (int k = 0; k < kNormChildren / 64; ++k) {
+      const int c = lane + 64 * k;
+      own[k] = c < static_cast<int>(node.children) ? load_partial(&a.sums[node.first + c]) : 0.0;
+    }
+    sum = own[0];
+#pragma unroll
+    for (int k = 1; k < kNormChildren / 64; ++k) sum += own[k];
+    sum = wave_sum_f64(sum);
     slot = node.slot;
     parent = node.parent;
     tensor = node.tensor;
