@@ -35,6 +35,7 @@ namespace muon {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
@@ -147,6 +148,23 @@ __device__ __forceinline__ void issue_stage(const MUON_GLOBAL uint16_t* P, int64
     uint16_t* dst = buf + (is_a ? 0 : BM * LBK) + blk * 512;
     __builtin_amdgcn_global_load_lds((const MUON_GLOBAL void*)(src), (__attribute__((address_space(3))) void*)(dst),
                                      16, 0, 0);
+  }
+}
+
+// Fragments read from LDS have arrived in registers at this point of the
+// program, and what uses them later uses those registers.  The products' last
+// k-step of a stage is multiplied after the barrier that lets the other waves
+// refill the stage's buffer; without this the compiler may move its reads
+// there too (an LDS read is not ordered with s_barrier once the machine code
+// is formed: it moved the transposing reads of X into the block of the
+// products, past loads into another part of the same buffer).
+template <int N>
+__device__ __forceinline__ void in_registers(bf16x8_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    i32x4_t v = __builtin_bit_cast(i32x4_t, r[i]);
+    asm volatile("" : "+v"(v));
+    r[i] = __builtin_bit_cast(bf16x8_t, v);
   }
 }
 
@@ -280,6 +298,8 @@ __device__ __forceinline__ void mma_bf16(const uint16_t* Pg, int64_t ldp, const 
   auto sync = [&]() {
     // (The scheduling barriers keep the MFMAs on their side of the wait.)
     __builtin_amdgcn_sched_barrier(0);
+    in_registers(fa[(NQ - 1) & 1]);
+    in_registers(fb[(NQ - 1) & 1]);
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     wait_vm<0>();
     __builtin_amdgcn_s_barrier();
@@ -316,6 +336,8 @@ __device__ __forceinline__ void mma_bf16(const uint16_t* Pg, int64_t ldp, const 
     // has landed (the two stages issued after it may still be in flight).
     auto sync_deep = [&]() {
       __builtin_amdgcn_sched_barrier(0);
+      in_registers(fa[(NQ - 1) & 1]);
+      in_registers(fb[(NQ - 1) & 1]);
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
       wait_vm<2 * LPS>();
       __builtin_amdgcn_s_barrier();
