@@ -27,6 +27,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmuon_mi3
 MUON_F32, MUON_BF16 = 0, 1
 _DT_CODE = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
 _DT_NAME = {"f32": MUON_F32, "bf16": MUON_BF16}
+MUON_CONFIG_FIELDS = 0x4D43F702   # muon_config_t.fields: grad_scale counts
 
 STATUS_NAMES = {0: "MUON_OK", 1: "MUON_ERR_INVALID_ARG", 2: "MUON_ERR_DTYPE",
                 3: "MUON_ERR_WORKSPACE", 4: "MUON_ERR_ALIAS", 5: "MUON_ERR_HIP",
@@ -61,7 +62,7 @@ class MuonConfig(ctypes.Structure):
                 ("w_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32),
                 ("mom_dtype", ctypes.c_int32), ("ns_dtype", ctypes.c_int32),
                 ("dimuon_eps", ctypes.c_float), ("nesterov", ctypes.c_int32),
-                ("weight_decay", ctypes.c_float), ("reserved0", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float), ("fields", ctypes.c_uint32),
                 ("grad_scale", ctypes.c_void_p), ("reserved", ctypes.c_int32 * 1)]
 
 
@@ -217,6 +218,7 @@ class StepConfig:
         cfg.dimuon_eps = self.dimuon_eps
         cfg.nesterov = 1 if self.nesterov else 0
         cfg.weight_decay = self.weight_decay
+        cfg.fields = MUON_CONFIG_FIELDS
         cfg.grad_scale = _scalar_ptr(self.grad_scale)
         return cfg, keep
 

@@ -57,6 +57,11 @@ struct Plan {
 // 256 * max(16, KP) / KP positions (thin_slice_len).
 bool is_thin(int64_t m, int64_t n) { return std::min(m, n) <= kThinMaxK; }
 
+// The config's gradient scale, if the caller's config has that field.
+const float* grad_scale_of(const muon_config_t& cfg) {
+  return cfg.fields == MUON_CONFIG_FIELDS ? cfg.grad_scale : nullptr;
+}
+
 muon_status_t validate_config(const muon_config_t* cfg) {
   if (!cfg) return fail(MUON_ERR_INVALID_ARG, "cfg is NULL");
   const int32_t dts[4] = {cfg->w_dtype, cfg->g_dtype, cfg->mom_dtype, cfg->ns_dtype};
@@ -68,7 +73,7 @@ muon_status_t validate_config(const muon_config_t* cfg) {
     return fail(MUON_ERR_INVALID_ARG, "lr, momentum and weight_decay must be finite");
   if (!finite(cfg->dimuon_eps) || cfg->dimuon_eps < 0.0f)
     return fail(MUON_ERR_INVALID_ARG, "dimuon_eps must be finite and >= 0");
-  if (reinterpret_cast<uintptr_t>(cfg->grad_scale) % 4 != 0)
+  if (reinterpret_cast<uintptr_t>(grad_scale_of(*cfg)) % 4 != 0)
     return fail(MUON_ERR_INVALID_ARG, "grad_scale is not 4-byte aligned");
   if (cfg->coeff_schedule) {
     for (int i = 0; i < 3 * cfg->ns_steps; ++i)
@@ -118,8 +123,8 @@ muon_status_t validate_buffers(const muon_matrix_t* mats, int64_t count, const m
       rs.push_back({lo, lo + b.bytes, i, b.what, b.wr});
     }
   }
-  if (cfg->grad_scale) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(cfg->grad_scale);
+  if (const float* scale = grad_scale_of(*cfg)) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(scale);
     rs.push_back({lo, lo + 4, 0, "grad_scale", false});
   }
   return check_overlaps(rs, "matrix");
@@ -474,7 +479,7 @@ muon_status_t prepare(const muon_matrix_t* mats, int64_t count, const muon_confi
     return fail(MUON_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, p.total_bytes);
   // The workspace must not overlap any caller buffer.
   const uintptr_t lo = reinterpret_cast<uintptr_t>(ws), hi = lo + p.total_bytes;
-  const uintptr_t gs = reinterpret_cast<uintptr_t>(cfg->grad_scale);
+  const uintptr_t gs = reinterpret_cast<uintptr_t>(grad_scale_of(*cfg));
   if (gs && gs < hi && lo < gs + 4) return fail(MUON_ERR_ALIAS, "grad_scale lies in the workspace");
   for (int64_t i = 0; i < count; ++i) {
     const muon_matrix_t& x = mats[i];
@@ -507,7 +512,7 @@ StepArgs make_args(const Plan& p, const muon_config_t& cfg, void* ws, bool dimuo
   a.w_dt = cfg.w_dtype;
   a.ns_dt = cfg.ns_dtype;
   a.nesterov = cfg.nesterov ? 1 : 0;
-  a.grad_scale = cfg.grad_scale;
+  a.grad_scale = grad_scale_of(cfg);
   a.dimuon = dimuon ? 1 : 0;
   return a;
 }
@@ -729,6 +734,7 @@ void muon_config_default(muon_config_t* cfg) {
   cfg->dimuon_eps = 1e-4f;
   cfg->nesterov = 0;
   cfg->weight_decay = 0.0f;
+  cfg->fields = MUON_CONFIG_FIELDS;
 }
 
 muon_status_t muon_workspace_bytes(const muon_matrix_t* mats, int64_t count, const muon_config_t* cfg,

@@ -114,6 +114,8 @@ typedef struct muon_matrix {
   float reserved0;
 } muon_matrix_t;
 
+#define MUON_CONFIG_FIELDS 0x4D43F702u   /* value of muon_config_t.fields */
+
 typedef struct muon_config {
   float lr;                     /* learning rate eta */
   float momentum;               /* mu */
@@ -129,7 +131,10 @@ typedef struct muon_config {
   float dimuon_eps;             /* floor added to the relative energy (1e-4) */
   int32_t nesterov;             /* nonzero: orthogonalise G + mu*M_t instead of M_t */
   float weight_decay;           /* W_t = W_{t-1} - lr*(scale*O_t + weight_decay*W_{t-1}) */
-  int32_t reserved0;
+  uint32_t fields;              /* MUON_CONFIG_FIELDS (muon_config_default writes it): the caller knows
+                                   grad_scale.  With any other value grad_scale is not looked at:
+                                   it lies where earlier versions had reserved words, which a caller
+                                   that fills the struct by hand may never have set. */
   const float* grad_scale;      /* device or NULL: one float32 s, read by the step; the step then
                                    uses s*G (rounded to float32) wherever G stands.  The clip
                                    coefficient of muon_grad_norm (out + 1) goes here.  Must stay
@@ -139,7 +144,8 @@ typedef struct muon_config {
 } muon_config_t;
 
 /* Fill `cfg` with the defaults: lr 0.02, mu 0.95, NS5 (3.4445, -4.7750,
- * 2.0315), bf16 everywhere, eps 1e-4, no Nesterov, no weight decay. */
+ * 2.0315), bf16 everywhere, eps 1e-4, no Nesterov, no weight decay, no
+ * gradient scale (and `fields`, so that grad_scale counts once it is set). */
 void muon_config_default(muon_config_t* cfg);
 
 /* Bytes of device workspace a call over this batch needs.  The value covers
