@@ -299,6 +299,20 @@ def workspace_for(params: Sequence[Param], cfg: StepConfig, device=None) -> torc
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
 
 
+def _check_workspace(workspace, device, any_dtype=False):
+    """A caller's workspace (None: there is none): one stretch of memory on
+    the batch's device, of bytes.  Muon's calls take any dtype, and of its
+    size the element count."""
+    if workspace is None:
+        return
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the batch on {device}")
+    if not any_dtype and workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be uint8, got {workspace.dtype}")
+
+
 def _torch_stream(stream, device):
     """The launch stream as a torch stream object (None: the current stream)."""
     if stream is None:
@@ -315,6 +329,7 @@ def _step(fn_name: str, params: Sequence[Param], cfg: StepConfig, workspace: Opt
     arr = _marshal(params)
     c, _keep = cfg.to_c()
     device = params[0].w.device
+    _check_workspace(workspace, device, any_dtype=True)
     ts = _torch_stream(stream, device)
     if workspace is None:
         workspace = workspace_for(params, cfg)
@@ -419,6 +434,7 @@ class Plan:
         self.params = list(params)
         self.cfg = cfg
         self.device = params[0].w.device
+        _check_workspace(workspace, self.device, any_dtype=True)
         self.workspace = workspace if workspace is not None else workspace_for(params, cfg)
         arr = _marshal(params)
         c, keep = cfg.to_c()
@@ -593,6 +609,7 @@ def adamw_step(params: Sequence[AdamWParam], cfg: AdamWConfig, step: int,
     arr, c = _marshal_adamw(params, cfg), cfg.to_c()
     nbytes = ctypes.c_size_t(0)
     _check(lib.adamw_workspace_bytes(arr, len(params), ctypes.byref(c), ctypes.byref(nbytes)))
+    _check_workspace(workspace, params[0].w.device)
     device = _gpu_device(params[0].w.device)
     ts = _torch_stream(stream, device)
     if workspace is None:
@@ -618,6 +635,7 @@ class AdamWPlan:
         _check(lib.adamw_workspace_bytes(arr, len(params), ctypes.byref(c), ctypes.byref(nbytes)))
         _check(lib.adamw_state_elems(arr, len(params), ctypes.byref(elems)))
         self.params, self.cfg = list(params), cfg
+        _check_workspace(workspace, params[0].w.device)
         self.device = _gpu_device(params[0].w.device)
         self.state_elems = elems.value
         ts = _torch_stream(stream, self.device)
@@ -707,6 +725,7 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = float("inf"), out
     grad_scale to the steps.  Refused under stream capture."""
     if not grads:
         raise ValueError("no gradients")
+    _check_workspace(workspace, grads[0].device)
     device = _gpu_device(grads[0].device)
     ts = _torch_stream(stream, device)
     if out is None:
@@ -735,6 +754,7 @@ class GradNormPlan:
             raise ValueError("no gradients")
         self._handle = ctypes.c_void_p(0)
         self._lib = lib = load_library()
+        _check_workspace(workspace, grads[0].device)
         self.device = _gpu_device(grads[0].device)
         self.grads, self.tensor_norms = list(grads), tensor_norms
         self.out = out if out is not None else torch.zeros(2, device=self.device)
