@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass, field
+from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
 import torch  # loads the HIP runtime the library then shares
@@ -410,6 +410,15 @@ class LaunchTimer:
         return n
 
 
+def _own(obj):
+    """Copy of a Param, AdamWParam or config for a plan: the same memory, in
+    tensors that the caller's later assignments (to the object's fields, or
+    to a tensor's .data) do not reach."""
+    own = object.__new__(type(obj))
+    own.__dict__.update((k, v.detach() if isinstance(v, torch.Tensor) else v) for k, v in obj.__dict__.items())
+    return own
+
+
 # The current stream's handle without a Stream object around it (0.1 instead
 # of 2 us, of the 6 that a small step took), where torch has it.
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -425,14 +434,18 @@ def _stream_handle(stream, device):
 
 class Plan:
     """A prepared batch (muon_plan_t): validated and uploaded once, then
-    stepped repeatedly.  Keeps the tensors and the workspace alive."""
+    stepped repeatedly.  Keeps the tensors and the workspace alive, and goes on
+    reading the memory it was created with: gradients must stay where they are
+    (``zero_grad(set_to_none=False)``, or flat gradient buffers), since a new
+    ``p.grad`` is memory that the plan does not know.  A graph that holds a
+    captured step needs the plan as long as it is replayed."""
 
     def __init__(self, params: Sequence[Param], cfg: StepConfig, dimuon: bool,
                  workspace: Optional[torch.Tensor] = None, stream=None):
         lib = load_library()
         _check_dtypes(params, cfg)
-        self.params = list(params)
-        self.cfg = cfg
+        self.params = [_own(p) for p in params]
+        self.cfg = _own(cfg)
         self.device = params[0].w.device
         _check_workspace(workspace, self.device, any_dtype=True)
         self.workspace = workspace if workspace is not None else workspace_for(params, cfg)
@@ -622,8 +635,10 @@ def adamw_step(params: Sequence[AdamWParam], cfg: AdamWConfig, step: int,
 
 class AdamWPlan:
     """A prepared AdamW batch (adamw_plan_t): validated and uploaded once,
-    then stepped repeatedly.  Keeps the tensors and the workspace alive.
-    ``step()`` can be captured into a graph: every replay is the next step."""
+    then stepped repeatedly.  Keeps the tensors and the workspace alive, and
+    goes on reading the memory it was created with (gradients must stay where
+    they are, as for ``Plan``).  ``step()`` can be captured into a graph: every
+    replay is the next step, and needs the plan."""
 
     def __init__(self, params: Sequence[AdamWParam], cfg: AdamWConfig, step: int = 0,
                  workspace: Optional[torch.Tensor] = None, stream=None):
@@ -634,7 +649,7 @@ class AdamWPlan:
         nbytes, elems = ctypes.c_size_t(0), ctypes.c_int64(0)
         _check(lib.adamw_workspace_bytes(arr, len(params), ctypes.byref(c), ctypes.byref(nbytes)))
         _check(lib.adamw_state_elems(arr, len(params), ctypes.byref(elems)))
-        self.params, self.cfg = list(params), cfg
+        self.params, self.cfg = [_own(p) for p in params], _own(cfg)
         _check_workspace(workspace, params[0].w.device)
         self.device = _gpu_device(params[0].w.device)
         self.state_elems = elems.value
@@ -744,8 +759,9 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = float("inf"), out
 
 class GradNormPlan:
     """A prepared global gradient norm (muon_grad_norm_plan_t): ``run()``
-    launches one kernel and returns ``out``.  Keeps the tensors alive; can be
-    captured into a graph."""
+    launches one kernel and returns ``out``.  Keeps the tensors alive, and goes
+    on reading the memory it was created with (gradients must stay where they
+    are, as for ``Plan``); can be captured into a graph, which needs the plan."""
 
     def __init__(self, grads: Sequence[torch.Tensor], max_norm: float = float("inf"),
                  out: Optional[torch.Tensor] = None, tensor_norms: Optional[torch.Tensor] = None,
@@ -756,8 +772,9 @@ class GradNormPlan:
         self._lib = lib = load_library()
         _check_workspace(workspace, grads[0].device)
         self.device = _gpu_device(grads[0].device)
-        self.grads, self.tensor_norms = list(grads), tensor_norms
+        self.grads, self.tensor_norms = [g.detach() for g in grads], tensor_norms
         self.out = out if out is not None else torch.zeros(2, device=self.device)
+        self._written = [t.detach() for t in (self.out, tensor_norms) if t is not None]
         arr, nbytes = _marshal_grads(grads, self.out, tensor_norms), ctypes.c_size_t(0)
         _check(lib.muon_grad_norm_workspace_bytes(arr, len(grads), ctypes.byref(nbytes)))
         ts = _torch_stream(stream, self.device)
