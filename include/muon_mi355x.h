@@ -295,7 +295,9 @@ void muon_plan_destroy(muon_plan_t* plan);
  *        u(255) = NaN, and u(c) is the binary32 with the bits
  *        (c + 768) << 20 otherwise, so u(248) = 1.  A v above zero never takes
  *        code 0: it is stored as at least u(1) = 1.125 * 2^-31, so that no
- *        element's denominator falls to eps.
+ *        element's denominator falls to eps.  (With a v_scale below 2^-94, or
+ *        a beta2 below 1/2, beta2 times the smallest values may fall below
+ *        2^-126, and then counts as zero under the root all the same.)
  * A non-finite m or v, and a negative v, has the code of NaN, and the block's
  * scale is that of its other elements.  m^ and v^ of a step come from the
  * new moments before they are rounded to codes.  Rounding to a code:
@@ -410,8 +412,10 @@ muon_status_t adamw_plan_set_step(adamw_plan_t* plan, int64_t steps_done, void* 
  * `dtype` (F32 or BF16), 16-byte aligned, overlapping no buffer of the plan;
  * tensor i's n values start at the sum over j < i of n_j rounded up to
  * ADAMW_BLOCK.  The gaps are left as they were.  set_state rounds to 8-bit
- * codes to nearest.  The codes of a block whose scales are normal float32
- * numbers survive get_state in F32 followed by set_state. */
+ * codes to nearest.  get_state in F32 followed by set_state keeps m's codes
+ * where m_scale is a normal float32 number, and v's where v_scale is 2^-114
+ * or more; with smaller scales the smallest values lose bits to float32's
+ * own range, down to zero. */
 muon_status_t adamw_plan_get_state(adamw_plan_t* plan, void* m, void* v, muon_dtype_t dtype, void* stream);
 muon_status_t adamw_plan_set_state(adamw_plan_t* plan, const void* m, const void* v, muon_dtype_t dtype,
                                    void* stream);
