@@ -87,6 +87,7 @@ struct Staging {
   void* host = nullptr;
   size_t cap = 0;
   hipEvent_t ev = nullptr;
+  int device = -1;   // of the event, which can be recorded on that device's streams only
   bool pending = false;
 
   // True when the buffer may be written: no copy from it is in flight.
@@ -113,10 +114,18 @@ struct Staging {
       }
       cap = table.size();
     }
+    int current = -1;
+    if ((err = hipGetDevice(&current)) != hipSuccess)
+      return fail(MUON_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(err));
+    if (ev && device != current) {   // a thread that steps on several devices
+      (void)hipEventDestroy(ev);
+      ev = nullptr;
+    }
     if (!ev && (err = hipEventCreateWithFlags(&ev, hipEventDisableTiming)) != hipSuccess) {
       ev = nullptr;
       return fail(MUON_ERR_HIP, "hipEventCreate: %s", hipGetErrorString(err));
     }
+    device = current;
     std::memcpy(host, table.data(), table.size());
     if ((err = hipMemcpyAsync(dst, host, table.size(), hipMemcpyHostToDevice, s)) != hipSuccess)
       return fail(MUON_ERR_HIP, "hipMemcpyAsync: %s", hipGetErrorString(err));
