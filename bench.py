@@ -54,13 +54,13 @@ FETCH_SCALE, WRITE_SCALE = 2.0, 1.0
 GEMM_SOURCES = ("dimuon_newton_schulz_amd/csrc/gemm_kernels.hip", "dimuon_newton_schulz_amd/csrc/api.hip",
                 "dimuon_newton_schulz_amd/csrc/common.h")
 MEASURED_GEMM = {
-    "sources_sha256": "571eeb26874eb9228cd356fda852d9304cf5a583545c81150ad7052ca59dffb0",
-    "gpt2_small_12x4_bf16": {"fetch_kib": [134378.0, 5270.3], "write_kib": [163840.0, 2048.0],
-                             "mfma_busy_frac": 0.361, "clock_ghz": 2.19},
-    "square_8x4096x4096_bf16": {"fetch_kib": [786599.0], "write_kib": [262215.0],
-                                "mfma_busy_frac": 0.571, "clock_ghz": 2.00},
-    "moe_64x(2048x1408+1408x2048)_bf16": {"fetch_kib": [969355.0], "write_kib": [786463.0],
-                                          "mfma_busy_frac": 0.472, "clock_ghz": 1.93},
+    "sources_sha256": "2136081f1c0c61873773c530d4777a1bdf35faf17a67d3ba91c6604d9792db3e",
+    "gpt2_small_12x4_bf16": {"fetch_kib": [134275.0, 5260.3], "write_kib": [163840.0, 2048.0],
+                             "mfma_busy_frac": 0.369, "clock_ghz": 2.18},
+    "square_8x4096x4096_bf16": {"fetch_kib": [786589.0], "write_kib": [262147.0],
+                                "mfma_busy_frac": 0.589, "clock_ghz": 1.93},
+    "moe_64x(2048x1408+1408x2048)_bf16": {"fetch_kib": [965603.0], "write_kib": [786443.0],
+                                          "mfma_busy_frac": 0.478, "clock_ghz": 1.96},
 }
 
 

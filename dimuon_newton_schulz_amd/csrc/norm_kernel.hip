@@ -67,7 +67,9 @@ __device__ __forceinline__ double leaf_sum(const void* g, int count) {
 // float32 value overflows; a conversion and a product-sum an element, hidden
 // behind the reads).
 //   369M bf16: 116 us, 6.4 TB/s (a kernel that only reads reaches 7.4 to 7.7)
-//   4M float32 in 128 tensors: 6.2 us, of which 2 for the tree's two levels
+//   4M float32 in 128 tensors: 7.5 us, of which 2 for the tree's two levels
+//     (three sets of gradients in turn; 6.2 where two sets stay in the caches,
+//     as in the comparisons below)
 // Against 2048 workgroups with long stretches and one that adds up all sums:
 // 140 and 11.8 us.  Leaves of 16 KB took 126 and 7.3 us, of 64 KB 135 and 7.0
 // (both before STREAM and with 64 children a node), against 130 and 7.0.
