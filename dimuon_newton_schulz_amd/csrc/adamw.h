@@ -145,7 +145,7 @@ hipError_t launch_adamw_set(const AdamArgs& a, const void* m, const void* v, int
 // node's counter 14 ns a child where all arrive at once.  With 64, 128 and 256
 // children a node (three sets of gradients in turn): 128 tensors of 4 leaves
 // take 8.3 us (three levels), 7.5 (two) and 7.6; 129 of them 8.5, 8.7 and 7.6;
-// 256 of them 10.7, 11.3 and 11.1; one tensor of 128 leaves 7.2, 7.9 and 9.4;
+// 256 of them 10.7, 11.3 and 11.1; one tensor of 512 leaves 7.2, 7.9 and 9.4;
 // 128 tensors of 176 leaves 117, 116 and 118.
 constexpr int kNormThreads = 256;
 constexpr int kNormLeafBytes = 32768;
