@@ -1,4 +1,4 @@
-"""Python binding of libmuon_mi355x.so (the MI355X Muon / Dimuon step, AdamW and the gradient norm).
+"""Python binding of libmuon_mi355x.so (the MI355X Muon / Dimuon step, AdamW, the gradient norm and the experts' layers).
 
 Argument marshalling only: tensors are turned into device pointers and
 shapes, and every step of the method runs in the library's HIP kernels.  The
@@ -10,7 +10,9 @@ Entry points mirror the C ABI in ``include/muon_mi355x.h``:
 ``muon_status_string``; ``adamw_step``, ``AdamWPlan`` (AdamW for the
 parameters Muon does not take, moments in 32 or 8 bits); ``grad_norm``,
 ``GradNormPlan`` (global gradient norm and clip coefficient, which the steps
-take as ``grad_scale``).
+take as ``grad_scale``); in ``experts``: ``expert_sort``, ``expert_gather``,
+``expert_combine`` and its gradient, ``linear`` and ``linear_grad`` (the
+experts' layers, whose weight gradients the steps read).
 """
 
 from __future__ import annotations
@@ -40,12 +42,16 @@ EXPORTED_SYMBOLS = ("muon_config_default", "muon_workspace_bytes", "muon_step", 
                     "adamw_plan_create", "adamw_plan_step", "adamw_plan_set_lr", "adamw_plan_set_step",
                     "adamw_plan_get_state", "adamw_plan_set_state", "adamw_plan_destroy",
                     "muon_grad_norm_workspace_bytes", "muon_grad_norm", "muon_grad_norm_plan_create",
-                    "muon_grad_norm_plan_run", "muon_grad_norm_plan_destroy")
+                    "muon_grad_norm_plan_run", "muon_grad_norm_plan_destroy",
+                    "expert_sort_workspace_bytes", "expert_sort", "expert_gather", "expert_combine",
+                    "expert_combine_grad", "linear_forward", "linear_grad_workspace_bytes", "linear_grad")
 
 LAUNCH_KINDS = {-1: "start", 0: "thin_b", 1: "momentum", 2: "condition", 3: "prescale", 4: "norm",
                 5: "gram", 6: "poly", 7: "combine", 8: "postnorm", 9: "update", 10: "thin_energy",
                 11: "thin_a", 12: "momentum_prescale", 13: "energy", 14: "adamw", 15: "state_get", 16: "state_set",
-                17: "grad_norm"}
+                17: "grad_norm", 18: "expert_sort", 19: "expert_gather", 20: "expert_combine",
+                21: "expert_combine_grad", 22: "linear", 23: "linear_slope", 24: "linear_input", 25: "linear_weight",
+                26: "linear_bias"}
 
 
 class MuonMatrix(ctypes.Structure):
@@ -154,6 +160,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.argtypes, fn.restype = args, ctypes.c_int
     for name in ("adamw_plan_destroy", "muon_grad_norm_plan_destroy"):
         getattr(lib, name).argtypes, getattr(lib, name).restype = [vp], None
+    experts.bind(lib)
     lib.muon_status_string.argtypes = [ctypes.c_int]
     lib.muon_status_string.restype = ctypes.c_char_p
     lib.muon_last_error.argtypes = []
@@ -801,8 +808,14 @@ class GradNormPlan:
             pass
 
 
+from . import experts  # noqa: E402 (uses what is defined above)
+from .experts import (ACTIVATIONS, ExpertRoutes, expert_combine, expert_combine_grad, expert_gather,  # noqa: E402
+                      expert_sort, linear, linear_grad, linear_grad_workspace)
+
 __all__ = ["MuonMatrix", "MuonConfig", "MuonError", "StepConfig", "Param", "load_library",
            "muon_step", "dimuon_step", "muon_step_noalloc", "muon_workspace_bytes", "muon_status_string",
            "Plan", "workspace_for", "config_for", "EXPORTED_SYMBOLS", "LaunchTimer",
            "LAUNCH_KINDS", "AdamWConfig", "AdamWParam", "AdamWPlan", "adamw_param", "adamw_config_for",
-           "adamw_step", "adamw_workspace_bytes", "ADAMW_BLOCK", "grad_norm", "GradNormPlan"]
+           "adamw_step", "adamw_workspace_bytes", "ADAMW_BLOCK", "grad_norm", "GradNormPlan",
+           "ACTIVATIONS", "ExpertRoutes", "expert_sort", "expert_gather", "expert_combine", "expert_combine_grad",
+           "linear", "linear_grad", "linear_grad_workspace"]

@@ -14,7 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon_mi355x.so")
 SOURCES = ["api.hip", "stream_kernels.hip", "gemm_kernels.hip", "thin_kernel.hip",
-           "adamw_api.hip", "adamw_kernels.hip", "norm_kernel.hip"]
+           "adamw_api.hip", "adamw_kernels.hip", "norm_kernel.hip",
+           "expert_api.hip", "expert_kernels.hip", "linear_kernels.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -37,18 +37,6 @@ struct DeviceGuard {
   }
 };
 
-// No C++ exception leaves a C entry point.
-template <typename F>
-muon_status_t guarded(F&& f) {
-  try {
-    g_last_error.clear();
-    return f();
-  } catch (const std::bad_alloc&) {
-  } catch (const std::length_error&) {
-  }
-  return fail(MUON_ERR_MEMORY, "host memory exhausted");
-}
-
 // A copy from a staging buffer that is used again cannot be part of a
 // captured graph: calls that upload a table are refused under capture, before
 // they touch a staging buffer.

@@ -9,6 +9,8 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <new>
+#include <stdexcept>
 #include <string>
 #include <vector>
 
@@ -45,6 +47,18 @@ inline muon_status_t fail(muon_status_t st, const char* fmt, ...) {
   va_end(ap);
   g_last_error = buf;
   return st;
+}
+
+// No C++ exception leaves a C entry point.
+template <typename F>
+muon_status_t guarded(F&& f) {
+  try {
+    g_last_error.clear();
+    return f();
+  } catch (const std::bad_alloc&) {
+  } catch (const std::length_error&) {
+  }
+  return fail(MUON_ERR_MEMORY, "host memory exhausted");
 }
 
 constexpr size_t kAlign = 256;

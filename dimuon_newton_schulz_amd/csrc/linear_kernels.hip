@@ -1,0 +1,795 @@
+// Products over groups of rows, with bias, activation and residual, and their
+// gradients.  Group g holds the rows offsets[g] .. offsets[g+1]-1 and has a
+// weight W_g (out x in) of its own; a plain layer is one group.
+//
+//   forward        C(m, n) = sum_k x[m][k] W[n][k]     k-contiguous operands
+//   input gradient C(m, n) = sum_k dz[m][k] W[k][n]    W k-major
+//   weight gradient C(m, n) = sum_k dz[k][m] x[k][n]   both k-major, k the group's rows
+//
+// A BM x BN tile per workgroup; both operands go from global memory straight
+// into a ring of two LDS stages of 128 bytes of k per row (64 bf16 or 32
+// float32 values).  Buffer loads carry the bounds: their descriptor ends
+// with the operand, so that rows behind a group's last one, columns behind
+// the matrix and the ragged end of k arrive as zeros and no operand is
+// padded.  The products run with W's (or x's) fragment first, so that a lane
+// holds runs of four output columns of one row.
+#include <algorithm>
+#include <type_traits>
+
+#include "expert.h"
+#include "muon_mi355x.h"
+
+namespace muon {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+#define MUON_LDS __attribute__((address_space(3)))
+
+constexpr int NQ = 4;                    // k-steps of a stage: 16 (bf16) or 8 (f32) values of k each
+constexpr uint32_t kNowhere = 0x80000000u;   // an offset behind every descriptor's end
+
+// ---------------------------------------------------------------------------
+// Activations.  All in float32; expf is the accurate one.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// z Phi(z), with Phi from the complementary error function: no cancellation for negative z.
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
+// (1 + tanh(u)) / 2 = sigmoid(2u)
+constexpr float kTanhScale = 2.0f * 0.79788456080286536f, kTanhCubic = 0.044715f;
+
+__device__ __forceinline__ float activate(int act, float z) {
+  switch (act) {
+    case LINEAR_RELU: return z < 0.0f ? 0.0f : z;
+    case LINEAR_SILU: return z / (1.0f + expf(-z));
+    case LINEAR_GELU: return z * normal_cdf(z);
+    case LINEAR_GELU_TANH: return z / (1.0f + expf(-kTanhScale * (z + kTanhCubic * z * z * z)));
+    default: return z;
+  }
+}
+
+// The slope.  Beyond 100 it is 0 or 1 in float32 for all of them, and the
+// formulas would multiply 0 by infinity further out; NaN stays.
+__device__ __forceinline__ float slope(int act, float z) {
+  z = z > 100.0f ? 100.0f : (z < -100.0f ? -100.0f : z);
+  switch (act) {
+    case LINEAR_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    case LINEAR_SILU: {
+      const float s = sigmoid(z);
+      return s * (1.0f + z * (1.0f - s));
+    }
+    case LINEAR_GELU: return normal_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    case LINEAR_GELU_TANH: {
+      const float s = sigmoid(kTanhScale * (z + kTanhCubic * z * z * z));
+      return s + z * s * (1.0f - s) * kTanhScale * (1.0f + 3.0f * kTanhCubic * z * z);
+    }
+    default: return 1.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Work of a workgroup
+// ---------------------------------------------------------------------------
+struct Group {
+  int index, lo, hi;   // rows lo .. hi-1
+};
+
+__device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// Workgroups are dealt to the 8 XCDs in turn; runs of `run` neighbouring
+// tiles, which share operand panels, go to one XCD and so one L2.
+__device__ __forceinline__ int tile_of(int bid, int run) {
+  const int xcd = bid & 7, i = bid >> 3;
+  return ((i / run) * 8 + xcd) * run + i % run;
+}
+
+// Tile idx of the list that has every group's tiles of bm rows x nt columns
+// after another: its group and number within the group.  False behind the
+// last tile.  The groups' tiles are added up 64 groups at a time over the
+// lanes of a wave.
+__device__ __forceinline__ bool find_rows(const LinArgs& a, int idx, int bm, int nt, Group& g, int& local) {
+  if (!a.offsets) {
+    g = {0, 0, a.rows};
+    local = idx;
+    return idx < (a.rows + bm - 1) / bm * nt;
+  }
+  const int lane = threadIdx.x & 63;
+  const MUON_GLOBAL int32_t* off = gmem(a.offsets);
+  int before = 0;
+  for (int g0 = 0; g0 < a.groups; g0 += 64) {
+    const int i = g0 + lane;
+    int lo = 0, hi = 0;
+    if (i < a.groups) {
+      lo = clamped(off[i], 0, a.rows);
+      hi = clamped(off[i + 1], lo, a.rows);
+    }
+    const int tiles = (hi - lo + bm - 1) / bm * nt;
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    const uint64_t past = __ballot(before + sum > idx);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      g.index = g0 + l;
+      g.lo = __builtin_amdgcn_readlane(lo, l);
+      g.hi = __builtin_amdgcn_readlane(hi, l);
+      local = idx - (before + __builtin_amdgcn_readlane(sum - tiles, l));
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
+// Tile `local` of mt x nt: blocks of up to eight row tiles by all columns,
+// rows first, so that neighbours share panels of both operands.
+__device__ __forceinline__ void block_order(int local, int mt, int nt, int& rt, int& ct) {
+  const int per = 8 * nt, b = local / per, r = local - b * per, rows = min(8, mt - 8 * b);
+  rt = 8 * b + r % rows;
+  ct = r / rows;
+}
+
+// ---------------------------------------------------------------------------
+// Tiles
+// ---------------------------------------------------------------------------
+// WR x WC waves, each with (BM / WR) x (BN / WC) of the tile in 32 x 32 blocks.
+template <int BM_, int BN_, int WR_, int WC_>
+struct Geo {
+  static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_;
+  static constexpr int NW = WR * WC, NT = 64 * NW, WM = BM / WR, WN = BN / WC, MS = WM / 32, NS = WN / 32;
+  static constexpr int LA = BM * 8 / NT, LB = BN * 8 / NT;   // 16-byte loads per thread and stage
+  static constexpr int STAGE = (BM + BN) * 128;              // bytes
+  // Each wave stages 32 output rows at a time in a strip of its own, the
+  // strips of even and odd waves in different halves of the ring.
+  static constexpr int SP = WN + 4, STRIP = 32 * SP * 4;
+  static_assert(STRIP * ((NW + 1) / 2) <= STAGE, "strips fit the ring");
+};
+
+// Rows of 128 bytes (k-contiguous operand): 16-byte chunk c of row r sits in
+// slot c ^ ((r >> 1) & 7), so that the 16 rows of a fragment read's phase
+// fall on distinct banks.
+__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+// k-major operand, rows of B values: bf16, chunk c of k-row r in slot
+// c ^ (4 (r & 3)) (the four k-rows of a transposing read on distinct banks);
+// float32, c ^ (8 ((r >> 2) & 1)) (the k-rows of a wave's two halves).
+template <bool F32>
+__device__ __forceinline__ int kswz(int row) { return F32 ? 8 * ((row >> 2) & 1) : 4 * (row & 3); }
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
+// One operand of a tile: B rows (or columns, k-major) of which `valid` exist.
+template <bool F32, bool KM, int B, int NT>
+struct Operand {
+  static constexpr int ES = F32 ? 4 : 2, LBK = 128 / ES, L = B * 8 / NT, CPR = B * ES / 16;
+  const char* base;
+  uint32_t ld;         // bytes
+  int valid, k;
+  uint32_t off[L];     // of this thread's chunks within a stage
+
+  __device__ __forceinline__ Operand(const void* p, int64_t ld_elems, int valid_, int k_)
+      : base(static_cast<const char*>(p)), ld(static_cast<uint32_t>(ld_elems * ES)), valid(valid_), k(k_) {
+#pragma unroll
+    for (int q = 0; q < L; ++q) {
+      const int i = q * NT + threadIdx.x;
+      if constexpr (KM) {
+        const int r = i / CPR, c = (i % CPR) ^ kswz<F32>(r);
+        off[q] = c * 16 < valid * ES ? r * ld + c * 16 : kNowhere;
+      } else {
+        const int r = i >> 3, c = (i & 7) ^ swz(r);
+        off[q] = r * ld + c * 16;
+      }
+    }
+  }
+
+  // Loads of stage st into `buf` (this operand's part of a ring buffer).
+  __device__ __forceinline__ void issue(int st, char* buf) const {
+    const int left = k - st * LBK, here = left < LBK ? left : LBK;
+    const char* p = base + (KM ? static_cast<uint64_t>(st) * LBK * ld : static_cast<uint64_t>(st) * 128);
+    const uint32_t end = KM ? (here - 1) * ld + valid * ES : (valid - 1) * ld + here * ES;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, end, 0x00020000);
+    const int wave = threadIdx.x >> 6;
+    // The ragged end of k: chunks behind it would read the next row.
+    const bool cut = !KM && here < LBK;
+    const int c = (threadIdx.x & 7) ^ swz(threadIdx.x >> 3);   // the same chunk in each of the thread's rows
+    const bool out = cut && c * 16 >= here * ES;
+#pragma unroll
+    for (int q = 0; q < L; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (MUON_LDS void*)(buf + (q * NT + wave * 64) * 16), 16,
+                                               out ? kNowhere : off[q], 0, 0, 0);
+  }
+
+  // Operands whose rows do not lie on 16-byte borders, or whose sizes are not
+  // whole chunks: element by element, through registers.
+  __device__ __forceinline__ void fetch(int st, u32x4_t (&r)[L]) const {
+    const int k0 = st * LBK;
+#pragma unroll
+    for (int q = 0; q < L; ++q) {
+      const int i = q * NT + threadIdx.x;
+      int row, col, rows, cols;   // of the chunk's first element, and the operand's end
+      if constexpr (KM) {
+        row = i / CPR;
+        col = ((i % CPR) ^ kswz<F32>(row)) * (16 / ES);
+        rows = k - k0;
+        cols = valid;
+      } else {
+        row = i >> 3;
+        col = ((i & 7) ^ swz(row)) * (16 / ES);
+        rows = valid;
+        cols = k - k0;
+      }
+      const char* p = base + (KM ? static_cast<uint64_t>(k0) * ld : static_cast<uint64_t>(k0) * ES) +
+                      static_cast<uint64_t>(row) * ld + static_cast<uint64_t>(col) * ES;
+      uint32_t v[16 / ES];
+#pragma unroll
+      for (int e = 0; e < 16 / ES; ++e) {
+        v[e] = 0;
+        if (row < rows && col + e < cols) {
+          if constexpr (F32) v[e] = gmem(reinterpret_cast<const uint32_t*>(p))[e];
+          else v[e] = gmem(reinterpret_cast<const uint16_t*>(p))[e];
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if constexpr (F32) r[q][w] = v[w];
+        else r[q][w] = v[2 * w] | (v[2 * w + 1] << 16);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const u32x4_t (&r)[L], char* buf) const {
+#pragma unroll
+    for (int q = 0; q < L; ++q) *reinterpret_cast<u32x4_t*>(buf + (q * NT + threadIdx.x) * 16) = r[q];
+  }
+};
+
+// Fragments of k-step q of N blocks of 32 rows from row0 on.  bf16: lane l
+// holds k = 16q + 8 (l / 32) + 0..7 of row l mod 32; float32: k = 8q +
+// 4 (l / 32) + 0..3 (element e of both operands is the lane's k-slot of the
+// e-th of four products).
+template <bool F32, bool KM, int B, int N>
+__device__ __forceinline__ void read_frags(const char* buf, int row0, int q, u32x4_t (&f)[N]) {
+  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+  if constexpr (!KM) {
+    const char* p = buf + (row0 + fr) * 128 + (((2 * q + half) ^ swz(fr)) * 16);
+#pragma unroll
+    for (int t = 0; t < N; ++t) f[t] = *reinterpret_cast<const u32x4_t*>(p + t * 32 * 128);
+  } else if constexpr (F32) {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 8 * q + 4 * half + e, col = row0 + t * 32 + fr;
+        f[t][e] = *reinterpret_cast<const uint32_t*>(buf + r * B * 4 + ((((col >> 2) ^ kswz<true>(r)) << 2) + (col & 3)) * 4);
+      }
+  } else {
+    // Two transposing reads a block: in each group of 16 lanes, lane m
+    // receives column m's values of four k-rows, of which lane i reads the
+    // four columns 4 (i mod 4) of k-row i / 4.
+    const int m16 = lane & 15, g16 = lane >> 4;
+    const int r = 16 * q + 8 * half + (m16 >> 2), sw = 4 * (m16 >> 2);
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      const int col = row0 + t * 32 + 16 * (g16 & 1) + 4 * (m16 & 3);
+      const char* p = buf + r * B * 2 + ((((col >> 3) ^ sw) << 3) + (col & 7)) * 2;
+      const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUON_LDS i16x4_t*)(p));
+      const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUON_LDS i16x4_t*)(p + 4 * B * 2));
+      f[t] = __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+}
+
+// Fragments read from LDS are in registers at this point of the program (an
+// LDS read is otherwise free to move behind the barrier that lets the other
+// waves refill its buffer).
+template <int N>
+__device__ __forceinline__ void in_registers(u32x4_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i]));
+}
+
+template <bool F32, int MS, int NS>
+__device__ __forceinline__ void multiply(const u32x4_t (&fp)[MS], const u32x4_t (&fq)[NS], f32x16_t (&acc)[MS][NS]) {
+#pragma unroll
+  for (int s = 0; s < MS; ++s)
+#pragma unroll
+    for (int t = 0; t < NS; ++t) {
+      if constexpr (F32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(fq[t][e]), __uint_as_float(fp[s][e]),
+                                                           acc[s][t], 0, 0, 0);
+      } else {
+        acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fq[t]),
+                                                            __builtin_bit_cast(bf16x8_t, fp[s]), acc[s][t], 0, 0, 0);
+      }
+    }
+}
+
+// acc += P Q over k.  The two ring buffers are separate arrays, so that the
+// compiler can tell a read of one from a load into the other.
+template <bool F32, bool PKM, bool QKM, typename G, bool VEC>
+__device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT>& P,
+                                        const Operand<F32, QKM, G::BN, G::NT>& Q, int k, char* b0, char* b1,
+                                        f32x16_t (&acc)[G::MS][G::NS]) {
+  constexpr int LBK = F32 ? 32 : 64, QOFF = G::BM * 128;
+  const int wave = threadIdx.x >> 6, row_p = (wave / G::WC) * G::WM, row_q = (wave % G::WC) * G::WN;
+  const int nk = (k + LBK - 1) / LBK;
+  if (nk == 0) return;
+  u32x4_t fp[2][G::MS], fq[2][G::NS];
+  auto read = [&](const char* buf, int q) {
+    read_frags<F32, PKM, G::BM, G::MS>(buf, row_p, q, fp[q & 1]);
+    read_frags<F32, QKM, G::BN, G::NS>(buf + QOFF, row_q, q, fq[q & 1]);
+  };
+  auto mul = [&](int q) { multiply<F32, G::MS, G::NS>(fp[q & 1], fq[q & 1], acc); };
+  if constexpr (!VEC) {
+    u32x4_t rp[G::LA], rq[G::LB];
+    P.fetch(0, rp);
+    Q.fetch(0, rq);
+    for (int st = 0; st < nk; ++st) {
+      __syncthreads();
+      P.put(rp, b0);
+      Q.put(rq, b0 + QOFF);
+      __syncthreads();
+      if (st + 1 < nk) {
+        P.fetch(st + 1, rp);
+        Q.fetch(st + 1, rq);
+      }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        read(b0, q);
+        mul(q);
+      }
+    }
+  } else {
+    auto issue = [&](int st, char* buf) {
+      P.issue(st, buf);
+      Q.issue(st, buf + QOFF);
+    };
+    // This wave's reads of the stage are complete and the next stage has
+    // landed: behind it the stage's buffer may be refilled.
+    auto sync = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      in_registers(fp[(NQ - 1) & 1]);
+      in_registers(fq[(NQ - 1) & 1]);
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+      wait_vm<0>();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    issue(0, b0);
+    if (nk > 1) {
+      __builtin_amdgcn_s_barrier();   // every wave's stage-0 loads go out before any of stage 1
+      issue(1, b1);
+      wait_vm<G::LA + G::LB>();
+    } else {
+      wait_vm<0>();
+    }
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    read(b0, 0);
+#pragma unroll
+    for (int q = 1; q < NQ; ++q) {
+      read(b0, q);
+      mul(q - 1);
+    }
+    sync();
+    // From one sync to the next: load stage kt+2 into cur, multiply stage
+    // kt's last step, then stage kt+1's others.
+    auto step = [&](char* cur, const char* nxt, int kt) {
+      if (kt + 2 < nk) P.issue(kt + 2, cur);
+      read(nxt, 0);
+      mul(NQ - 1);
+      if (kt + 2 < nk) Q.issue(kt + 2, cur + QOFF);
+#pragma unroll
+      for (int q = 1; q < NQ; ++q) {
+        read(nxt, q);
+        mul(q - 1);
+      }
+      sync();
+    };
+    for (int kt = 0; kt < nk - 1; kt += 2) {
+      step(b0, b1, kt);
+      if (kt + 1 >= nk - 1) break;
+      step(b1, b0, kt + 1);
+    }
+    mul(NQ - 1);
+  }
+}
+
+// Eight values at p (16-byte aligned).
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
+  const MUON_GLOBAL u32x4_t* q = reinterpret_cast<const MUON_GLOBAL u32x4_t*>(gmem(static_cast<const char*>(p)));
+  if constexpr (F32) {
+    const u32x4_t a = q[0], b = q[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __uint_as_float(a[e]);
+      v[4 + e] = __uint_as_float(b[e]);
+    }
+  } else {
+    const u32x4_t a = q[0];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(a[e] << 16);
+      v[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
+    }
+  }
+}
+__device__ __forceinline__ void store8(void* p, const float (&v)[8], bool f32) {
+  MUON_GLOBAL u32x4_t* q = reinterpret_cast<MUON_GLOBAL u32x4_t*>(gmem(static_cast<char*>(p)));
+  if (f32) {
+    u32x4_t a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = __float_as_uint(v[e]);
+      b[e] = __float_as_uint(v[4 + e]);
+    }
+    q[0] = a;
+    q[1] = b;
+  } else {
+    u32x4_t a;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+    q[0] = a;
+  }
+}
+
+// Run of eight values (VEC), or as many as exist.
+template <bool VEC>
+__device__ __forceinline__ void load_run(const void* p, int64_t at, int n, bool f32, float (&v)[8]) {
+  if constexpr (VEC) {
+    const char* q = static_cast<const char*>(p) + at * (f32 ? 4 : 2);
+    if (f32) load8<true>(q, v);
+    else load8<false>(q, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? load_elem(p, at + e, f32 ? DT_F32 : DT_BF16) : 0.0f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_run(void* p, int64_t at, int n, bool f32, const float (&v)[8]) {
+  if constexpr (VEC) {
+    store8(static_cast<char*>(p) + at * (f32 ? 4 : 2), v, f32);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) store_elem(p, at + e, f32 ? DT_F32 : DT_BF16, v[e]);
+  }
+}
+
+// What becomes of eight sums of row m (of the operands' rows; of the weight
+// gradient: an output feature) from column n on, in group g.
+template <bool F32, int MODE, bool VEC>
+__device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_t m, int n, float (&v)[8]) {
+  const int left = a.n - n;
+  if constexpr (MODE == LIN_FORWARD) {
+    if (a.bias) {
+      float b[8];
+      load_run<VEC>(a.bias, static_cast<int64_t>(g) * a.n + n, left, F32, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += b[e];
+    }
+    if (a.pre) store_run<VEC>(a.pre, m * a.ldpre + n, left, F32, v);
+    if (a.act != LINEAR_NONE) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = activate(a.act, v[e]);
+    }
+    if (a.aux) {
+      float r[8];
+      load_run<VEC>(a.aux, m * a.ldaux + n, left, F32, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += r[e];
+    }
+    store_run<VEC>(a.c, m * a.ldc + n, left, F32, v);
+  } else if constexpr (MODE == LIN_INPUT) {
+    if (a.aux) {
+      float z[8];
+      load_run<VEC>(a.aux, m * a.ldaux + n, left, F32, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= slope(a.act, z[e]);
+    }
+    store_run<VEC>(a.c, m * a.ldc + n, left, F32, v);
+  } else if (a.parts > 1) {
+    const int64_t at = (static_cast<int64_t>(part) * a.groups + g) * a.m + m;
+    store_run<VEC>(a.part, at * a.n + n, left, true, v);
+  } else {
+    const int64_t at = g * a.gc + m * a.ldc + n;
+    if (a.accumulate) {
+      float o[8];
+      load_run<VEC>(a.c, at, left, a.c_dt == DT_F32, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += o[e];
+    }
+    store_run<VEC>(a.c, at, left, a.c_dt == DT_F32, v);
+  }
+}
+
+template <bool F32, int MODE, typename G, bool VEC>
+__global__ __launch_bounds__(G::NT, 1) void k_linear(LinArgs a, int run) {
+  constexpr int ES = F32 ? 4 : 2, LBK = 128 / ES;
+  constexpr bool PKM = MODE == LIN_WEIGHT, QKM = MODE != LIN_FORWARD;
+  __shared__ __attribute__((aligned(16))) char ring0[G::STAGE];
+  __shared__ __attribute__((aligned(16))) char ring1[G::STAGE];
+  const int idx = tile_of(blockIdx.x, run), nt = (a.n + G::BN - 1) / G::BN;
+  Group g;
+  int rt, ct, part = 0, k, m_valid;
+  int64_t row0;   // first row of the tile (weight gradient: of the group's part)
+  const char *p, *q;
+  if constexpr (MODE == LIN_WEIGHT) {
+    const int mt = (a.m + G::BM - 1) / G::BM;
+    if (idx >= mt * nt * a.groups * a.parts) return;
+    const int gi = idx / (mt * nt);
+    part = gi / a.groups;
+    g.index = gi % a.groups;
+    g.lo = a.offsets ? clamped(gmem(a.offsets)[g.index], 0, a.rows) : 0;
+    g.hi = a.offsets ? clamped(gmem(a.offsets)[g.index + 1], g.lo, a.rows) : a.rows;
+    block_order(idx % (mt * nt), mt, nt, rt, ct);
+    const int rows = g.hi - g.lo;
+    const int per = a.parts > 1 ? ((rows + a.parts - 1) / a.parts + LBK - 1) / LBK * LBK : rows;
+    const int first = static_cast<int>(min(static_cast<int64_t>(rows), static_cast<int64_t>(part) * per));
+    k = min(per, rows - first);
+    row0 = g.lo + first;
+    m_valid = min(G::BM, a.m - rt * G::BM);
+    p = static_cast<const char*>(a.p) + (row0 * a.ldp + rt * G::BM) * ES;
+    q = static_cast<const char*>(a.q) + (row0 * a.ldq + ct * G::BN) * ES;
+  } else {
+    int local;
+    if (!find_rows(a, idx, G::BM, nt, g, local)) return;
+    block_order(local, (g.hi - g.lo + G::BM - 1) / G::BM, nt, rt, ct);
+    k = a.k;
+    row0 = g.lo + rt * G::BM;
+    m_valid = min(G::BM, g.hi - static_cast<int>(row0));
+    p = static_cast<const char*>(a.p) + row0 * a.ldp * ES;
+    const int64_t at = static_cast<int64_t>(ct) * G::BN;
+    q = static_cast<const char*>(a.q) + (g.index * a.gq + (MODE == LIN_FORWARD ? at * a.ldq : at)) * ES;
+  }
+  const int n0 = ct * G::BN, n_valid = min(G::BN, a.n - n0);
+  f32x16_t acc[G::MS][G::NS];
+#pragma unroll
+  for (int s = 0; s < G::MS; ++s)
+#pragma unroll
+    for (int t = 0; t < G::NS; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[s][t][e] = 0.0f;
+  const Operand<F32, PKM, G::BM, G::NT> P(p, a.ldp, m_valid, k);
+  const Operand<F32, QKM, G::BN, G::NT> Q(q, a.ldq, n_valid, k);
+  product<F32, PKM, QKM, G, VEC>(P, Q, k, ring0, ring1, acc);
+
+  // Through the wave's strip: a lane puts four columns of one row at a time
+  // and takes eight, so that global accesses are whole 16-byte runs.
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float* strip = reinterpret_cast<float*>((wave & 1 ? ring1 : ring0) + (wave >> 1) * G::STRIP);
+  constexpr int CPR = G::WN / 8;
+  const int m_out = MODE == LIN_WEIGHT ? rt * G::BM : 0;
+  // (One copy of what follows the sums, for all blocks of rows.)
+#pragma unroll 1
+  for (int s = 0; s < G::MS; ++s) {
+    const int ms = (wave / G::WC) * G::WM + s * 32;
+    if (ms >= m_valid) break;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int b = 0; b < G::MS; ++b)
+      if (b == s) {
+#pragma unroll
+        for (int t = 0; t < G::NS; ++t)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<f32x4_t*>(strip + (lane & 31) * G::SP + t * 32 + 8 * u + 4 * (lane >> 5)) =
+                f32x4_t{acc[b][t][4 * u], acc[b][t][4 * u + 1], acc[b][t][4 * u + 2], acc[b][t][4 * u + 3]};
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int i = lane; i < 32 * CPR; i += 64) {
+      const int r = i / CPR, c = (i % CPR) * 8;
+      const int n = n0 + (wave % G::WC) * G::WN + c;
+      if (ms + r >= m_valid || n >= a.n) continue;
+      float v[8];
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(strip + r * G::SP + c);
+      const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(strip + r * G::SP + c + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = lo[e];
+        v[4 + e] = hi[e];
+      }
+      finish<F32, MODE, VEC>(a, g.index, part, (MODE == LIN_WEIGHT ? m_out : row0) + ms + r, n, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Elementwise and column passes
+// ---------------------------------------------------------------------------
+constexpr int kPassThreads = 256;
+
+// Rows that belong to a group (all without offsets).
+__device__ __forceinline__ int rows_used(const int32_t* offsets, int groups, int rows) {
+  return offsets ? clamped(gmem(offsets)[groups], 0, rows) : rows;
+}
+
+template <bool F32, bool VEC>
+__global__ __launch_bounds__(kPassThreads) void k_linear_slope(const void* dy, int64_t ld_dy, const void* pre,
+                                                              int64_t ld_pre, void* dz, int64_t ld_dz,
+                                                              const int32_t* offsets, int groups, int rows, int out,
+                                                              int act) {
+  const int runs = (out + 7) / 8;
+  const int64_t n = static_cast<int64_t>(rows_used(offsets, groups, rows)) * runs;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPassThreads + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kPassThreads) {
+    const int64_t r = i / runs;
+    const int c = static_cast<int>(i % runs) * 8;
+    float g[8], z[8];
+    load_run<VEC>(dy, r * ld_dy + c, out - c, F32, g);
+    load_run<VEC>(pre, r * ld_pre + c, out - c, F32, z);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] *= slope(act, z[e]);
+    store_run<VEC>(dz, r * ld_dz + c, out - c, F32, g);
+  }
+}
+
+// Column sums of a group's rows (or of one part of them): four waves take
+// every fourth row, 64 columns each, and are added in wave order.
+template <bool F32>
+__global__ __launch_bounds__(kPassThreads) void k_linear_bias(const void* dz, int64_t ld, const int32_t* offsets,
+                                                             int rows, int out, void* db, int grad_dt, int accumulate,
+                                                             float* part, int parts) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int blocks = (out + 63) / 64, g = blockIdx.x / blocks, c = (blockIdx.x % blocks) * 64 + lane;
+  const int lo = offsets ? clamped(gmem(offsets)[g], 0, rows) : 0;
+  const int hi = offsets ? clamped(gmem(offsets)[g + 1], lo, rows) : rows;
+  const int per = (hi - lo + parts - 1) / parts;
+  const int first = static_cast<int>(min(static_cast<int64_t>(hi), lo + static_cast<int64_t>(blockIdx.y) * per));
+  const int last = min(hi, first + per);
+  float s = 0.0f;
+  if (c < out)
+    for (int r = first + wave; r < last; r += 4) s += load_elem(dz, r * ld + c, F32 ? DT_F32 : DT_BF16);
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < out) {
+    s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    const int64_t at = static_cast<int64_t>(g) * out + c;
+    if (parts > 1) {
+      part[static_cast<int64_t>(blockIdx.y) * (gridDim.x / blocks) * out + at] = s;
+    } else {
+      if (accumulate) s += load_elem(db, at, grad_dt);
+      store_elem(db, at, grad_dt, s);
+    }
+  }
+}
+
+// c (+)= sum of `parts` arrays of `groups` x m x n, in order.
+__global__ __launch_bounds__(kPassThreads) void k_linear_join(const float* part, int parts, int groups, int m, int n,
+                                                             void* c, int64_t ldc, int64_t gc, int c_dt,
+                                                             int accumulate) {
+  const int64_t total = static_cast<int64_t>(groups) * m * n;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPassThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kPassThreads) {
+    float s = 0.0f;
+    for (int p = 0; p < parts; ++p) s += gmem(part)[p * total + i];
+    const int64_t row = i / n, at = row / m * gc + row % m * ldc + i % n;
+    if (accumulate) s += load_elem(c, at, c_dt);
+    store_elem(c, at, c_dt, s);
+  }
+}
+
+using Large = Geo<256, 256, 2, 4>;
+using Medium = Geo<128, 128, 2, 2>;
+using Small = Geo<64, 128, 1, 4>;
+
+int64_t ceil_of(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kMaxBlocks = (int64_t{1} << 23) - 1;
+
+// Tiles of a launch at most (the groups' last tiles may be partial).
+template <typename G>
+int64_t tiles_at_most(const LinArgs& a, int mode) {
+  const int64_t nt = ceil_of(a.n, G::BN);
+  if (mode == LIN_WEIGHT) return ceil_of(a.m, G::BM) * nt * a.groups * a.parts;
+  const int64_t mt = a.offsets ? std::min<int64_t>(a.rows, a.rows / G::BM + a.groups) : ceil_of(a.rows, G::BM);
+  return mt * nt;
+}
+
+template <bool F32, int MODE, typename G, bool VEC>
+hipError_t go(const LinArgs& a, bool dry, hipStream_t s) {
+  const int64_t tiles = tiles_at_most<G>(a, MODE);
+  const int64_t run = std::max<int64_t>(1, std::min<int64_t>(32, tiles / 16));
+  const int64_t blocks = ceil_of(tiles, 8 * run) * 8 * run;
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
+  if (blocks == 0 || dry) return hipSuccess;
+  hipLaunchKernelGGL((k_linear<F32, MODE, G, VEC>), dim3(static_cast<uint32_t>(blocks)), dim3(G::NT), 0, s, a,
+                     static_cast<int>(run));
+  return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t pick(const LinArgs& a, int dt, bool vec, bool dry, hipStream_t s) {
+  if (dt == DT_F32) return vec ? go<true, MODE, Medium, true>(a, dry, s) : go<true, MODE, Medium, false>(a, dry, s);
+  if (!vec) return go<false, MODE, Medium, false>(a, dry, s);
+  if constexpr (MODE != LIN_WEIGHT) {
+    if (a.rows / a.groups <= 96) return go<false, MODE, Small, true>(a, dry, s);
+  }
+  if (tiles_at_most<Large>(a, MODE) >= 512) return go<false, MODE, Large, true>(a, dry, s);
+  return go<false, MODE, Medium, true>(a, dry, s);
+}
+
+uint32_t pass_blocks(int64_t n) {
+  return static_cast<uint32_t>(std::max<int64_t>(1, std::min<int64_t>(1 << 20, ceil_of(n, kPassThreads))));
+}
+
+}  // namespace
+
+static hipError_t linear(const LinArgs& a, int mode, int dt, bool vec, bool dry, hipStream_t s) {
+  if (mode == LIN_FORWARD) return pick<LIN_FORWARD>(a, dt, vec, dry, s);
+  if (mode == LIN_INPUT) return pick<LIN_INPUT>(a, dt, vec, dry, s);
+  return pick<LIN_WEIGHT>(a, dt, vec, dry, s);
+}
+hipError_t launch_linear(const LinArgs& a, int mode, int dt, bool vec, hipStream_t s) {
+  return linear(a, mode, dt, vec, false, s);
+}
+bool linear_fits(const LinArgs& a, int mode, int dt, bool vec) {
+  return linear(a, mode, dt, vec, true, nullptr) == hipSuccess;
+}
+
+int linear_weight_parts(int64_t rows, int64_t out, int64_t in, int64_t groups) {
+  const int64_t tiles = ceil_of(out, 128) * ceil_of(in, 128) * groups;
+  const int64_t most = std::max<int64_t>(1, rows / groups / 512);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most, 512 / tiles, 64})));
+}
+
+hipError_t launch_linear_join(const LinArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(k_linear_join, dim3(pass_blocks(static_cast<int64_t>(a.groups) * a.m * a.n)), dim3(kPassThreads), 0,
+                     s, a.part, a.parts, a.groups, a.m, a.n, a.c, a.ldc, a.gc, a.c_dt, a.accumulate);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_slope(const void* dy, int64_t ld_dy, const void* pre, int64_t ld_pre, void* dz, int64_t ld_dz,
+                               const int32_t* offsets, int groups, int64_t rows, int64_t out, int act, int dt, bool vec,
+                               hipStream_t s) {
+  const dim3 grid(pass_blocks(rows * ceil_of(out, 8))), threads(kPassThreads);
+#define MUON_SLOPE(F32, VEC)                                                                                         \
+  hipLaunchKernelGGL((k_linear_slope<F32, VEC>), grid, threads, 0, s, dy, ld_dy, pre, ld_pre, dz, ld_dz, offsets,    \
+                     groups, (int)rows, (int)out, act)
+  if (dt == DT_F32) {
+    if (vec) MUON_SLOPE(true, true); else MUON_SLOPE(true, false);
+  } else {
+    if (vec) MUON_SLOPE(false, true); else MUON_SLOPE(false, false);
+  }
+#undef MUON_SLOPE
+  return hipGetLastError();
+}
+
+int linear_bias_parts(int64_t rows, int64_t groups) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows / groups / 256, 64)));
+}
+
+hipError_t launch_linear_bias(const void* dz, int64_t ld, const int32_t* offsets, int groups, int64_t rows, int64_t out,
+                              void* db, int dt, int grad_dt, int accumulate, float* part, int parts, hipStream_t s) {
+  const dim3 grid(static_cast<uint32_t>(ceil_of(out, 64) * groups), static_cast<uint32_t>(parts)), threads(kPassThreads);
+  if (dt == DT_F32)
+    hipLaunchKernelGGL(k_linear_bias<true>, grid, threads, 0, s, dz, ld, offsets, (int)rows, (int)out, db, grad_dt,
+                       accumulate, part, parts);
+  else
+    hipLaunchKernelGGL(k_linear_bias<false>, grid, threads, 0, s, dz, ld, offsets, (int)rows, (int)out, db, grad_dt,
+                       accumulate, part, parts);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || parts == 1) return e;
+  hipLaunchKernelGGL(k_linear_join, dim3(pass_blocks(out * groups)), threads, 0, s, part, parts, groups, 1, (int)out, db,
+                     out, out, grad_dt, accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace muon

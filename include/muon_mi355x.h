@@ -1,7 +1,8 @@
 /*
  * muon_mi355x.h: C ABI of the MI355X (gfx950) Muon / Dimuon optimizer step,
- * of AdamW for the parameters Muon does not take, and of the global gradient
- * norm that clips both.
+ * of AdamW for the parameters Muon does not take, of the global gradient
+ * norm that clips both, and of the experts' layers whose weight gradients the
+ * steps read: tokens sorted by expert and back, products over groups of rows.
  *
  * One Muon call updates a batch of independent 2-D weight matrices of mixed
  * shapes:
@@ -218,7 +219,16 @@ typedef enum muon_launch_kind {
   MUON_LAUNCH_ADAMW = 14,     /* AdamW step */
   MUON_LAUNCH_STATE_GET = 15, /* AdamW moments to values */
   MUON_LAUNCH_STATE_SET = 16, /* values to AdamW moments */
-  MUON_LAUNCH_GRAD_NORM = 17  /* global gradient norm */
+  MUON_LAUNCH_GRAD_NORM = 17, /* global gradient norm */
+  MUON_LAUNCH_EXPERT_SORT = 18,    /* expert_sort (one or two kernels) */
+  MUON_LAUNCH_EXPERT_GATHER = 19,
+  MUON_LAUNCH_EXPERT_COMBINE = 20,
+  MUON_LAUNCH_EXPERT_COMBINE_GRAD = 21,
+  MUON_LAUNCH_LINEAR = 22,         /* linear_forward */
+  MUON_LAUNCH_LINEAR_SLOPE = 23,   /* linear_grad: dz */
+  MUON_LAUNCH_LINEAR_INPUT = 24,   /* linear_grad: dx */
+  MUON_LAUNCH_LINEAR_WEIGHT = 25,  /* linear_grad: dW (and the sum of its parts) */
+  MUON_LAUNCH_LINEAR_BIAS = 26     /* linear_grad: db (and the sum of its parts) */
 } muon_launch_kind_t;
 
 /* Timing hook, per host thread; not part of the method.  When `events` is
@@ -455,6 +465,166 @@ muon_status_t muon_grad_norm_plan_create(const muon_grad_t* grads, int64_t count
                                          void* stream, muon_grad_norm_plan_t** plan);
 muon_status_t muon_grad_norm_plan_run(muon_grad_norm_plan_t* plan, void* stream);
 void muon_grad_norm_plan_destroy(muon_grad_norm_plan_t* plan);
+
+/* ------------------------------------------------------------------------
+ * Experts: tokens sorted by expert and back, with weights, and the gradient.
+ *
+ * A batch of `tokens` tokens, each with `top` choices of an expert; choice j
+ * of token t is slot s = t * top + j, and slots = tokens * top.  expert_sort
+ * turns the experts' numbers ids[s] into
+ *   offsets[e]   number of slots with an expert below e, e = 0 .. experts:
+ *                expert e has the sorted rows offsets[e] .. offsets[e+1]-1
+ *   place[s]     sorted row of slot s; -1 if ids[s] is outside 0..experts-1
+ *                (a slot that is not routed)
+ *   order[r]     slot of sorted row r; -1 behind offsets[experts]
+ * An expert's rows are in the order of their slots.
+ *
+ *   expert_gather         xs[place[s]] = x[t]
+ *   expert_combine        y[t] = residual[t] + sum over j of weights[s] * ys[place[s]]
+ *                         (residual 0 if NULL, weights 1 if NULL; unrouted slots
+ *                         add nothing)
+ *   expert_combine_grad   dys[place[s]] = weights[s] * dy[t]
+ *                         dweights[s] = sum over the columns of dy[t] * ys[place[s]]
+ *                         (0 for an unrouted slot)
+ * The gradient of expert_gather is expert_combine without weights; that of
+ * the residual is dy.  Sorted rows without a slot are left as they were.
+ * Sums are float32 (the residual, then j ascending), rounded once.  Results
+ * repeat bit for bit.
+ *
+ * Rows have `width` consecutive elements of `dtype` and a stride in elements
+ * (at least width, at most 2^20); rows of whole 16-byte runs on 16-byte
+ * borders are the fast case.  weights and dweights are of weights_dtype, one
+ * a slot.  Sorted buffers have `slots` rows.  Limits: 1 <= top, 1 <= experts
+ * <= 1024, slots <= 2^30, width <= 65536; tokens = 0 is allowed (the sort
+ * then writes offsets only).  A written buffer overlaps no other buffer,
+ * except that y may be the residual itself (same pointer and stride).
+ * Entries of place outside 0 .. slots-1 count as -1, whatever wrote them.
+ *
+ * These calls allocate nothing and upload nothing: they may be captured.
+ * The buffers are those of the stream's device, which is current.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, ALIAS, UNSUPPORTED, HIP.
+ * ------------------------------------------------------------------------ */
+typedef struct expert_routes {
+  int32_t* offsets;     /* device, experts + 1 */
+  int32_t* order;       /* device, tokens * top */
+  int32_t* place;       /* device, tokens * top */
+  int64_t tokens;
+  int32_t top;
+  int32_t experts;
+} expert_routes_t;
+
+/* Workspace of expert_sort (256-byte aligned device memory; 0 bytes for up
+ * to 8192 slots, then NULL will do).  Calls that share one must be ordered. */
+muon_status_t expert_sort_workspace_bytes(int64_t tokens, int32_t top, int32_t experts, size_t* bytes);
+/* `ids`: device, tokens * top integers of id_bytes (4 or 8) each. */
+muon_status_t expert_sort(const void* ids, int32_t id_bytes, const expert_routes_t* routes, void* workspace,
+                          size_t workspace_bytes, void* stream);
+muon_status_t expert_gather(const void* x, int64_t x_stride, int64_t width, muon_dtype_t dtype,
+                            const expert_routes_t* routes, void* xs, int64_t xs_stride, void* stream);
+muon_status_t expert_combine(const void* ys, int64_t ys_stride, int64_t width, muon_dtype_t dtype,
+                             const expert_routes_t* routes, const void* weights, muon_dtype_t weights_dtype,
+                             const void* residual, int64_t residual_stride, void* y, int64_t y_stride, void* stream);
+muon_status_t expert_combine_grad(const void* dy, int64_t dy_stride, const void* ys, int64_t ys_stride, int64_t width,
+                                  muon_dtype_t dtype, const expert_routes_t* routes, const void* weights,
+                                  muon_dtype_t weights_dtype, void* dys, int64_t dys_stride, void* dweights,
+                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products over groups of rows, with bias, activation and residual, and
+ * their gradients.  Group g holds the rows offsets[g] .. offsets[g+1]-1 and
+ * has a weight W_g (out x in) and a bias b_g; offsets = NULL (groups = 1)
+ * means all rows, a plain layer.
+ *
+ *   linear_forward   z = x W_g^T + b_g;   pre = z;   y = act(z) + residual
+ *   linear_grad      dz = dy * act'(pre)
+ *                    dx = (dz W_g) * x_act'(x_pre)
+ *                    dW_g (+)= dz^T x,  db_g (+)= column sums of dz, over the group's rows
+ *
+ * act: none, relu (slope 0 at 0), gelu (z times the normal distribution
+ * function), gelu_tanh (its tanh form), silu (z times the sigmoid).
+ * x_act and x_pre, if given, carry dx on through the activation that made x:
+ * then dx is the gradient of x_pre.  The gradient of the residual is dy.
+ * With `accumulate`, dW and db are added to what the buffers hold; without,
+ * groups without rows get zeros.  Rows of no group (before offsets[0], behind
+ * offsets[groups]) are left as they were in y, pre and dx.  offsets are
+ * nondecreasing and within 0 .. rows; others are cut to that.
+ *
+ * Products of bf16 values with float32 sums (MFMA), or of float32 values
+ * (dtype F32).  y and pre are rounded once from float32, y from the unrounded
+ * z.  dz is rounded to dtype before its products (it is an operand of the
+ * matrix units).  Results repeat bit for bit.
+ *
+ * Strides are in elements, rows' elements consecutive, strides at most 2^20.
+ * The fast case: in and out multiples of 8, rows and group strides on 16-byte
+ * borders.  bias, db: groups x out, consecutive.  Limits: rows < 2^30; in and
+ * out 1 .. 65536 (as for muon_step); groups 1 .. 4096.  rows = 0 is allowed
+ * (dW and db are then zero, or unchanged).  A written buffer overlaps no other
+ * buffer, except that y may be the residual itself (same pointer and stride).
+ * offsets live on the device: no call waits for the host.
+ *
+ * Allocation, capture and errors as for the experts' calls above.  dW_g and
+ * W_g are what muon_matrix_t takes as g and w (rows consecutive).
+ * ------------------------------------------------------------------------ */
+typedef enum linear_activation {
+  LINEAR_NONE = 0,
+  LINEAR_RELU = 1,
+  LINEAR_GELU = 2,
+  LINEAR_GELU_TANH = 3,
+  LINEAR_SILU = 4
+} linear_activation_t;
+
+typedef struct linear_args {
+  int64_t rows, in, out;
+  int64_t groups;
+  const int32_t* offsets;   /* device, groups + 1, or NULL (groups = 1) */
+  int32_t dtype;            /* muon_dtype_t of x, w, bias, residual, y and pre */
+  int32_t activation;       /* linear_activation_t */
+  const void* x;            /* device, rows x in */
+  int64_t x_stride;
+  const void* w;            /* device, groups x out x in */
+  int64_t w_stride, w_group_stride;
+  const void* bias;         /* device, groups x out, or NULL */
+  const void* residual;     /* device, rows x out, or NULL */
+  int64_t residual_stride;
+  void* y;                  /* device, rows x out */
+  int64_t y_stride;
+  void* pre;                /* device, rows x out, or NULL: receives z */
+  int64_t pre_stride;
+} linear_args_t;
+
+muon_status_t linear_forward(const linear_args_t* args, void* stream);
+
+typedef struct linear_grad_args {
+  int64_t rows, in, out;
+  int64_t groups;
+  const int32_t* offsets;
+  int32_t dtype;            /* of dy, pre, x, w, x_pre and dx */
+  int32_t grad_dtype;       /* of dw and db */
+  int32_t activation;
+  int32_t x_activation;
+  int32_t accumulate;
+  int32_t reserved0;
+  const void* dy;           /* device, rows x out */
+  int64_t dy_stride;
+  const void* pre;          /* device, rows x out: z (not read without activation) */
+  int64_t pre_stride;
+  const void* x;            /* device, rows x in (for dw) */
+  int64_t x_stride;
+  const void* w;            /* device, groups x out x in (for dx) */
+  int64_t w_stride, w_group_stride;
+  const void* x_pre;        /* device, rows x in (with x_activation) */
+  int64_t x_pre_stride;
+  void* dx;                 /* device, rows x in, or NULL */
+  int64_t dx_stride;
+  void* dw;                 /* device, groups x out x in, or NULL */
+  int64_t dw_stride, dw_group_stride;
+  void* db;                 /* device, groups x out, or NULL */
+} linear_grad_args_t;
+
+/* Workspace of linear_grad: dz (with an activation), and sums in parts where
+ * a gradient's rows are split.  Checks sizes, not pointers. */
+muon_status_t linear_grad_workspace_bytes(const linear_grad_args_t* args, size_t* bytes);
+muon_status_t linear_grad(const linear_grad_args_t* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* muon_status_string(muon_status_t status);
