@@ -24,51 +24,87 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 #define MUON_LDS __attribute__((address_space(3)))
 
-constexpr int NQ = 4;                    // k-steps of a stage: 16 (bf16) or 8 (f32) values of k each
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset behind every descriptor's end
 
 // ---------------------------------------------------------------------------
-// Activations.  All in float32; expf is the accurate one.
+// Activations, in float32.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
 // z Phi(z), with Phi from the complementary error function: no cancellation for negative z.
 __device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
 // (1 + tanh(u)) / 2 = sigmoid(2u)
 constexpr float kTanhScale = 2.0f * 0.79788456080286536f, kTanhCubic = 0.044715f;
 
-__device__ __forceinline__ float activate(int act, float z) {
-  switch (act) {
-    case LINEAR_RELU: return z < 0.0f ? 0.0f : z;
-    case LINEAR_SILU: return z / (1.0f + expf(-z));
-    case LINEAR_GELU: return z * normal_cdf(z);
-    case LINEAR_GELU_TANH: return z / (1.0f + expf(-kTanhScale * (z + kTanhCubic * z * z * z)));
-    default: return z;
-  }
+// EXACT (float32 outputs): expf and a true quotient; otherwise the hardware's
+// exponential and reciprocal, 1 ulp each (z log2 e rounds to 2^-24 z, so the
+// exponential is off by at most 2^-24 |z| + 2 ulps, far below a bf16 step).
+template <bool EXACT>
+__device__ __forceinline__ float over_one_plus_exp(float z, float u) {   // z / (1 + exp(-u))
+  if constexpr (EXACT) return z / (1.0f + expf(-u));
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * u));
 }
 
-// The slope.  Beyond 100 it is 0 or 1 in float32 for all of them, and the
+// The slope's argument: beyond 100 every slope is 0 or 1 in float32, and the
 // formulas would multiply 0 by infinity further out; NaN stays.
-__device__ __forceinline__ float slope(int act, float z) {
-  z = z > 100.0f ? 100.0f : (z < -100.0f ? -100.0f : z);
-  switch (act) {
-    case LINEAR_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    case LINEAR_SILU: {
-      const float s = sigmoid(z);
-      return s * (1.0f + z * (1.0f - s));
-    }
-    case LINEAR_GELU: return normal_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-    case LINEAR_GELU_TANH: {
-      const float s = sigmoid(kTanhScale * (z + kTanhCubic * z * z * z));
-      return s + z * s * (1.0f - s) * kTanhScale * (1.0f + 3.0f * kTanhCubic * z * z);
-    }
-    default: return 1.0f;
+__device__ __forceinline__ float within_100(float z) { return z > 100.0f ? 100.0f : (z < -100.0f ? -100.0f : z); }
+
+template <int ACT, bool EXACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == LINEAR_RELU) return z < 0.0f ? 0.0f : z;
+  if constexpr (ACT == LINEAR_SILU) return over_one_plus_exp<EXACT>(z, z);
+  if constexpr (ACT == LINEAR_GELU) return z * normal_cdf(z);
+  return over_one_plus_exp<EXACT>(z, kTanhScale * (z + kTanhCubic * z * z * z));
+}
+
+template <int ACT, bool EXACT>
+__device__ __forceinline__ float slope(float z) {
+  z = within_100(z);
+  if constexpr (ACT == LINEAR_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+  if constexpr (ACT == LINEAR_SILU) {
+    const float s = over_one_plus_exp<EXACT>(1.0f, z);
+    return s * (1.0f + z * (1.0f - s));
   }
+  if constexpr (ACT == LINEAR_GELU) return normal_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+  const float s = over_one_plus_exp<EXACT>(1.0f, kTanhScale * (z + kTanhCubic * z * z * z));
+  return s + z * s * (1.0f - s) * kTanhScale * (1.0f + 3.0f * kTanhCubic * z * z);
+}
+
+// v = act(v), and v *= act'(z): one branch for eight values.
+template <bool EXACT>
+__device__ __forceinline__ void activate8(int act, float (&v)[8]) {
+#define MUON_EACH(ACT)            \
+  case ACT:                       \
+    _Pragma("unroll")             \
+    for (int e = 0; e < 8; ++e) v[e] = activate<ACT, EXACT>(v[e]); \
+    break
+  switch (act) {
+    MUON_EACH(LINEAR_RELU);
+    MUON_EACH(LINEAR_SILU);
+    MUON_EACH(LINEAR_GELU);
+    MUON_EACH(LINEAR_GELU_TANH);
+    default: break;
+  }
+#undef MUON_EACH
+}
+template <bool EXACT>
+__device__ __forceinline__ void times_slope8(int act, const float (&z)[8], float (&v)[8]) {
+#define MUON_EACH(ACT)            \
+  case ACT:                       \
+    _Pragma("unroll")             \
+    for (int e = 0; e < 8; ++e) v[e] *= slope<ACT, EXACT>(z[e]); \
+    break
+  switch (act) {
+    MUON_EACH(LINEAR_RELU);
+    MUON_EACH(LINEAR_SILU);
+    MUON_EACH(LINEAR_GELU);
+    MUON_EACH(LINEAR_GELU_TANH);
+    default: break;
+  }
+#undef MUON_EACH
 }
 
 // ---------------------------------------------------------------------------
@@ -139,28 +175,29 @@ __device__ __forceinline__ void block_order(int local, int mt, int nt, int& rt, 
 // ---------------------------------------------------------------------------
 // Tiles
 // ---------------------------------------------------------------------------
-// WR x WC waves, each with (BM / WR) x (BN / WC) of the tile in 32 x 32 blocks.
-template <int BM_, int BN_, int WR_, int WC_>
+// WR x WC waves, each with (BM / WR) x (BN / WC) of the tile in 16 x 16
+// blocks.  Stages have KB = 128 bytes of k of every row; a ring of U units
+// holds the stages' operands in turn, P_0 Q_0 P_1 Q_1 ..., so that with five
+// units one operand's loads have two stages' time to arrive.
+template <int BM_, int BN_, int WR_, int WC_, int U_, int UNIT_ = (BM_ > BN_ ? BM_ : BN_) * 128>
 struct Geo {
-  static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_;
-  static constexpr int NW = WR * WC, NT = 64 * NW, WM = BM / WR, WN = BN / WC, MS = WM / 32, NS = WN / 32;
-  static constexpr int LA = BM * 8 / NT, LB = BN * 8 / NT;   // 16-byte loads per thread and stage
-  static constexpr int STAGE = (BM + BN) * 128;              // bytes
-  // Each wave stages 32 output rows at a time in a strip of its own, the
-  // strips of even and odd waves in different halves of the ring.
+  static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, U = U_, UNIT = UNIT_;   // UNIT: bytes
+  static constexpr int NW = WR * WC, NT = 64 * NW, WM = BM / WR, WN = BN / WC, MS = WM / 16, NS = WN / 16;
+  static constexpr int LP = BM * 8 / NT, LQ = BN * 8 / NT;      // 16-byte loads per thread and unit
+  // Each wave stages 32 output rows at a time in a strip of its own.
   static constexpr int SP = WN + 4, STRIP = 32 * SP * 4;
-  static_assert(STRIP * ((NW + 1) / 2) <= STAGE, "strips fit the ring");
 };
+constexpr int KB = 128, NQ = 2;   // a stage's k: bytes, and steps of 32 (bf16) or 16 (f32) values
 
-// Rows of 128 bytes (k-contiguous operand): 16-byte chunk c of row r sits in
-// slot c ^ ((r >> 1) & 7), so that the 16 rows of a fragment read's phase
-// fall on distinct banks.
+// k-contiguous operand, rows of KB bytes: 16-byte chunk c of row r sits in
+// slot c ^ swz(r), so that the 16 rows of a fragment read's phase fall on
+// distinct banks.
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 // k-major operand, rows of B values: bf16, chunk c of k-row r in slot
 // c ^ (4 (r & 3)) (the four k-rows of a transposing read on distinct banks);
-// float32, c ^ (8 ((r >> 2) & 1)) (the k-rows of a wave's two halves).
+// float32, c ^ (4 ((r >> 2) & 3)) (the k-rows of a wave's four quarters).
 template <bool F32>
-__device__ __forceinline__ int kswz(int row) { return F32 ? 8 * ((row >> 2) & 1) : 4 * (row & 3); }
+__device__ __forceinline__ int kswz(int row) { return F32 ? 4 * ((row >> 2) & 3) : 4 * (row & 3); }
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -170,7 +207,8 @@ __device__ __forceinline__ void wait_vm() {
 // One operand of a tile: B rows (or columns, k-major) of which `valid` exist.
 template <bool F32, bool KM, int B, int NT>
 struct Operand {
-  static constexpr int ES = F32 ? 4 : 2, LBK = 128 / ES, L = B * 8 / NT, CPR = B * ES / 16;
+  static constexpr int ES = F32 ? 4 : 2, LBK = KB / ES, CR = KB / 16, L = B * CR / NT, CPR = B * ES / 16;
+  static_assert(L * NT == B * CR && NT / CR % 16 == 0, "whole loads; a thread's rows have one swizzle");
   const char* base;
   uint32_t ld;         // bytes
   int valid, k;
@@ -185,7 +223,7 @@ struct Operand {
         const int r = i / CPR, c = (i % CPR) ^ kswz<F32>(r);
         off[q] = c * 16 < valid * ES ? r * ld + c * 16 : kNowhere;
       } else {
-        const int r = i >> 3, c = (i & 7) ^ swz(r);
+        const int r = i / CR, c = (i % CR) ^ swz(r);
         off[q] = r * ld + c * 16;
       }
     }
@@ -194,13 +232,14 @@ struct Operand {
   // Loads of stage st into `buf` (this operand's part of a ring buffer).
   __device__ __forceinline__ void issue(int st, char* buf) const {
     const int left = k - st * LBK, here = left < LBK ? left : LBK;
-    const char* p = base + (KM ? static_cast<uint64_t>(st) * LBK * ld : static_cast<uint64_t>(st) * 128);
-    const uint32_t end = KM ? (here - 1) * ld + valid * ES : (valid - 1) * ld + here * ES;
+    const char* p = base + (KM ? static_cast<uint64_t>(st) * LBK * ld : static_cast<uint64_t>(st) * KB);
+    // (Behind the last slot nothing is read: the descriptor is empty.)
+    const uint32_t end = here <= 0 ? 0 : KM ? (here - 1) * ld + valid * ES : (valid - 1) * ld + here * ES;
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, end, 0x00020000);
     const int wave = threadIdx.x >> 6;
     // The ragged end of k: chunks behind it would read the next row.
     const bool cut = !KM && here < LBK;
-    const int c = (threadIdx.x & 7) ^ swz(threadIdx.x >> 3);   // the same chunk in each of the thread's rows
+    const int c = (threadIdx.x % CR) ^ swz(threadIdx.x / CR);   // the same chunk in each of the thread's rows
     const bool out = cut && c * 16 >= here * ES;
 #pragma unroll
     for (int q = 0; q < L; ++q)
@@ -222,8 +261,8 @@ struct Operand {
         rows = k - k0;
         cols = valid;
       } else {
-        row = i >> 3;
-        col = ((i & 7) ^ swz(row)) * (16 / ES);
+        row = i / CR;
+        col = ((i % CR) ^ swz(row)) * (16 / ES);
         rows = valid;
         cols = k - k0;
       }
@@ -251,34 +290,33 @@ struct Operand {
   }
 };
 
-// Fragments of k-step q of N blocks of 32 rows from row0 on.  bf16: lane l
-// holds k = 16q + 8 (l / 32) + 0..7 of row l mod 32; float32: k = 8q +
-// 4 (l / 32) + 0..3 (element e of both operands is the lane's k-slot of the
+// Fragments of k-step q of N blocks of 16 rows from row0 on.  bf16: lane l
+// holds k = 32q + 8 (l / 16) + 0..7 of row l mod 16; float32: k = 16q +
+// 4 (l / 16) + 0..3 (element e of both operands is the lane's k-slot of the
 // e-th of four products).
 template <bool F32, bool KM, int B, int N>
 __device__ __forceinline__ void read_frags(const char* buf, int row0, int q, u32x4_t (&f)[N]) {
-  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+  const int lane = threadIdx.x & 63, m16 = lane & 15, g16 = lane >> 4;
   if constexpr (!KM) {
-    const char* p = buf + (row0 + fr) * 128 + (((2 * q + half) ^ swz(fr)) * 16);
+    const char* p = buf + (row0 + m16) * KB + (((4 * q + g16) ^ swz(m16)) * 16);
 #pragma unroll
-    for (int t = 0; t < N; ++t) f[t] = *reinterpret_cast<const u32x4_t*>(p + t * 32 * 128);
+    for (int t = 0; t < N; ++t) f[t] = *reinterpret_cast<const u32x4_t*>(p + t * 16 * KB);
   } else if constexpr (F32) {
 #pragma unroll
     for (int t = 0; t < N; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = 8 * q + 4 * half + e, col = row0 + t * 32 + fr;
+        const int r = 16 * q + 4 * g16 + e, col = row0 + t * 16 + m16;
         f[t][e] = *reinterpret_cast<const uint32_t*>(buf + r * B * 4 + ((((col >> 2) ^ kswz<true>(r)) << 2) + (col & 3)) * 4);
       }
   } else {
     // Two transposing reads a block: in each group of 16 lanes, lane m
     // receives column m's values of four k-rows, of which lane i reads the
     // four columns 4 (i mod 4) of k-row i / 4.
-    const int m16 = lane & 15, g16 = lane >> 4;
-    const int r = 16 * q + 8 * half + (m16 >> 2), sw = 4 * (m16 >> 2);
+    const int r = 32 * q + 8 * g16 + (m16 >> 2), sw = 4 * (m16 >> 2);
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-      const int col = row0 + t * 32 + 16 * (g16 & 1) + 4 * (m16 & 3);
+      const int col = row0 + t * 16 + 4 * (m16 & 3);
       const char* p = buf + r * B * 2 + ((((col >> 3) ^ sw) << 3) + (col & 7)) * 2;
       const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUON_LDS i16x4_t*)(p));
       const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUON_LDS i16x4_t*)(p + 4 * B * 2));
@@ -297,7 +335,7 @@ __device__ __forceinline__ void in_registers(u32x4_t (&r)[N]) {
 }
 
 template <bool F32, int MS, int NS>
-__device__ __forceinline__ void multiply(const u32x4_t (&fp)[MS], const u32x4_t (&fq)[NS], f32x16_t (&acc)[MS][NS]) {
+__device__ __forceinline__ void multiply(const u32x4_t (&fp)[MS], const u32x4_t (&fq)[NS], f32x4_t (&acc)[MS][NS]) {
 #pragma unroll
   for (int s = 0; s < MS; ++s)
 #pragma unroll
@@ -305,39 +343,59 @@ __device__ __forceinline__ void multiply(const u32x4_t (&fp)[MS], const u32x4_t 
       if constexpr (F32) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(fq[t][e]), __uint_as_float(fp[s][e]),
+          acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fq[t][e]), __uint_as_float(fp[s][e]),
                                                            acc[s][t], 0, 0, 0);
       } else {
-        acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fq[t]),
+        acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fq[t]),
                                                             __builtin_bit_cast(bf16x8_t, fp[s]), acc[s][t], 0, 0, 0);
       }
     }
 }
 
-// acc += P Q over k.  The two ring buffers are separate arrays, so that the
-// compiler can tell a read of one from a load into the other.
+// Order of a k-step's instructions: the next step's fragments are read between
+// its first products, so that they are there when it ends, and the loads go
+// out between the later ones.
+template <bool F32, bool PKM, bool QKM, typename G, int LOADS>
+__device__ __forceinline__ void pace() {
+  constexpr int M = G::MS * G::NS * (F32 ? 4 : 1), H = M / 2;   // products
+  constexpr int R = G::MS * (PKM ? (F32 ? 4 : 2) : 1) + G::NS * (QKM ? (F32 ? 4 : 2) : 1);   // reads
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+#pragma unroll
+    for (int j = i * R / H; j < (i + 1) * R / H; ++j) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < M - H; ++i) {
+#pragma unroll
+    for (int j = i * LOADS / (M - H); j < (i + 1) * LOADS / (M - H); ++j)
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  }
+}
+
+// acc += P Q over k.
 template <bool F32, bool PKM, bool QKM, typename G, bool VEC>
 __device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT>& P,
-                                        const Operand<F32, QKM, G::BN, G::NT>& Q, int k, char* b0, char* b1,
-                                        f32x16_t (&acc)[G::MS][G::NS]) {
-  constexpr int LBK = F32 ? 32 : 64, QOFF = G::BM * 128;
-  const int wave = threadIdx.x >> 6, row_p = (wave / G::WC) * G::WM, row_q = (wave % G::WC) * G::WN;
+                                        const Operand<F32, QKM, G::BN, G::NT>& Q, int k, char* const (&ring)[G::U],
+                                        int row_p, int row_q, f32x4_t (&acc)[G::MS][G::NS]) {
+  constexpr int LBK = KB / (F32 ? 4 : 2), U = G::U;
   const int nk = (k + LBK - 1) / LBK;
   if (nk == 0) return;
   u32x4_t fp[2][G::MS], fq[2][G::NS];
-  auto read = [&](const char* buf, int q) {
-    read_frags<F32, PKM, G::BM, G::MS>(buf, row_p, q, fp[q & 1]);
-    read_frags<F32, QKM, G::BN, G::NS>(buf + QOFF, row_q, q, fq[q & 1]);
+  auto read = [&](const char* bp, const char* bq, int q) {
+    read_frags<F32, PKM, G::BM, G::MS>(bp, row_p, q, fp[q & 1]);
+    read_frags<F32, QKM, G::BN, G::NS>(bq, row_q, q, fq[q & 1]);
   };
   auto mul = [&](int q) { multiply<F32, G::MS, G::NS>(fp[q & 1], fq[q & 1], acc); };
   if constexpr (!VEC) {
-    u32x4_t rp[G::LA], rq[G::LB];
+    u32x4_t rp[G::LP], rq[G::LQ];
     P.fetch(0, rp);
     Q.fetch(0, rq);
     for (int st = 0; st < nk; ++st) {
       __syncthreads();
-      P.put(rp, b0);
-      Q.put(rq, b0 + QOFF);
+      P.put(rp, ring[0]);
+      Q.put(rq, ring[1]);
       __syncthreads();
       if (st + 1 < nk) {
         P.fetch(st + 1, rp);
@@ -345,64 +403,82 @@ __device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT>& P
       }
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        read(b0, q);
+        read(ring[0], ring[1], q);
         mul(q);
       }
     }
   } else {
-    auto issue = [&](int st, char* buf) {
-      P.issue(st, buf);
-      Q.issue(st, buf + QOFF);
+    static_assert(NQ % 2 == 0, "fragment sets alternate");
+    // Loads of this wave in units first .. U-1 of the order P Q P Q ...
+    constexpr auto loads_from = [](int first) {
+      int n = 0;
+      for (int u = first; u < U; ++u) n += u % 2 ? G::LQ : G::LP;
+      return n;
     };
-    // This wave's reads of the stage are complete and the next stage has
-    // landed: behind it the stage's buffer may be refilled.
+    auto issue = [&](int st, int operand, char* buf) {
+      if (operand == 0) P.issue(st, buf);
+      else Q.issue(st, buf);
+    };
+    // The stage's reads are complete and the next stage has landed, the loads
+    // behind it still in flight: behind this point the stage's units may be
+    // refilled.
     auto sync = [&]() {
       __builtin_amdgcn_sched_barrier(0);
       in_registers(fp[(NQ - 1) & 1]);
       in_registers(fq[(NQ - 1) & 1]);
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-      wait_vm<0>();
+      wait_vm<loads_from(4)>();
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
       __builtin_amdgcn_sched_barrier(0);
     };
-    issue(0, b0);
-    if (nk > 1) {
-      __builtin_amdgcn_s_barrier();   // every wave's stage-0 loads go out before any of stage 1
-      issue(1, b1);
-      wait_vm<G::LA + G::LB>();
-    } else {
-      wait_vm<0>();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      issue(u / 2, u % 2, ring[u]);
+      if (u % 2) __builtin_amdgcn_s_barrier();   // every wave's loads of a stage go out before any of the next
     }
+    wait_vm<loads_from(2)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    read(b0, 0);
+    read(ring[0], ring[1], 0);
 #pragma unroll
     for (int q = 1; q < NQ; ++q) {
-      read(b0, q);
+      read(ring[0], ring[1], q);
       mul(q - 1);
     }
     sync();
-    // From one sync to the next: load stage kt+2 into cur, multiply stage
-    // kt's last step, then stage kt+1's others.
-    auto step = [&](char* cur, const char* nxt, int kt) {
-      if (kt + 2 < nk) P.issue(kt + 2, cur);
-      read(nxt, 0);
+    // From the sync after stage st to the next one: its units (c0, c1) take
+    // the U-th and U+1-st units behind them (U odd: Q first), while its last
+    // step and the next stage's (units n0, n1) others are multiplied.
+    constexpr bool ODD = U % 2;
+    auto step = [&](char* c0, char* c1, const char* n0, const char* n1, int st) {
+      read(n0, n1, 0);
+      issue(st + U / 2, ODD, c0);
       mul(NQ - 1);
-      if (kt + 2 < nk) Q.issue(kt + 2, cur + QOFF);
+      pace<F32, PKM, QKM, G, ODD ? G::LQ : G::LP>();
+      read(n0, n1, 1);
+      issue(st + U / 2 + ODD, !ODD, c1);
+      mul(0);
+      pace<F32, PKM, QKM, G, ODD ? G::LP : G::LQ>();
 #pragma unroll
-      for (int q = 1; q < NQ; ++q) {
-        read(nxt, q);
+      for (int q = 2; q < NQ; ++q) {
+        read(n0, n1, q);
         mul(q - 1);
+        pace<F32, PKM, QKM, G, 0>();
       }
       sync();
     };
-    for (int kt = 0; kt < nk - 1; kt += 2) {
-      step(b0, b1, kt);
-      if (kt + 1 >= nk - 1) break;
-      step(b1, b0, kt + 1);
+    constexpr int PERIOD = ODD ? U : U / 2;   // stages until the units' order repeats
+    for (int st = 0; st < nk - 1; st += PERIOD) {
+#pragma unroll
+      for (int b = 0; b < PERIOD; ++b) {
+        if (st + b >= nk - 1) break;
+        step(ring[2 * b % U], ring[(2 * b + 1) % U], ring[(2 * b + 2) % U], ring[(2 * b + 3) % U], st + b);
+      }
     }
     mul(NQ - 1);
+    // No load may still be writing the ring when the epilogue uses it.
+    wait_vm<0>();
   }
 }
 
@@ -481,10 +557,7 @@ __device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_
       for (int e = 0; e < 8; ++e) v[e] += b[e];
     }
     if (a.pre) store_run<VEC>(a.pre, m * a.ldpre + n, left, F32, v);
-    if (a.act != LINEAR_NONE) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = activate(a.act, v[e]);
-    }
+    activate8<F32>(a.act, v);
     if (a.aux) {
       float r[8];
       load_run<VEC>(a.aux, m * a.ldaux + n, left, F32, r);
@@ -496,8 +569,7 @@ __device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_
     if (a.aux) {
       float z[8];
       load_run<VEC>(a.aux, m * a.ldaux + n, left, F32, z);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= slope(a.act, z[e]);
+      times_slope8<F32>(a.act, z, v);
     }
     store_run<VEC>(a.c, m * a.ldc + n, left, F32, v);
   } else if (a.parts > 1) {
@@ -515,98 +587,140 @@ __device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_
   }
 }
 
+// What a workgroup's part of a product reads and writes.
+struct Tile {
+  const char *p, *q;
+  int group, part, k;
+  int m_valid, n_valid, n0;
+  int64_t row0;   // of c: a row (forward, input gradient) or an output feature
+};
+
+// One tile of at most G::BM x G::BN.
+template <bool F32, int MODE, typename G, bool VEC>
+__device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* const (&ring)[G::U]) {
+  constexpr bool PKM = MODE == LIN_WEIGHT, QKM = MODE != LIN_FORWARD;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int row_p = (wave / G::WC) * G::WM, row_q = (wave % G::WC) * G::WN;
+  f32x4_t acc[G::MS][G::NS];
+#pragma unroll
+  for (int s = 0; s < G::MS; ++s)
+#pragma unroll
+    for (int t = 0; t < G::NS; ++t) acc[s][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const Operand<F32, PKM, G::BM, G::NT> P(w.p, a.ldp, w.m_valid, w.k);
+  const Operand<F32, QKM, G::BN, G::NT> Q(w.q, a.ldq, w.n_valid, w.k);
+  product<F32, PKM, QKM, G, VEC>(P, Q, w.k, ring, row_p, row_q, acc);
+
+  // Through the wave's strip: a lane puts four columns of one row at a time
+  // and takes eight, so that global accesses are whole 16-byte runs.
+  __syncthreads();
+  constexpr int PER = G::UNIT / G::STRIP, CPR = G::WN / 8;   // strips of a unit
+  static_assert(PER * G::U >= G::NW, "strips fit the ring");
+  uint32_t base = 0;
+#pragma unroll
+  for (int b = 0; b < G::U; ++b)
+    base = wave / PER == b ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MUON_LDS char*)ring[b])) : base;
+  MUON_LDS float* strip = (MUON_LDS float*)(static_cast<uintptr_t>(base + (wave % PER) * G::STRIP));
+  // (One copy of what follows the sums, for all blocks of rows.)
+#pragma unroll 1
+  for (int s = 0; s < G::MS / 2; ++s) {
+    const int ms = row_p + s * 32;
+    if (ms >= w.m_valid) break;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int b = 0; b < G::MS; ++b)
+      if (b / 2 == s) {
+#pragma unroll
+        for (int t = 0; t < G::NS; ++t)
+          *(MUON_LDS f32x4_t*)(strip + (b % 2 * 16 + (lane & 15)) * G::SP + t * 16 + 4 * (lane >> 4)) = acc[b][t];
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+    for (int i = lane; i < 32 * CPR; i += 64) {
+      const int r = i / CPR, c = (i % CPR) * 8;
+      const int n = w.n0 + row_q + c;
+      if (ms + r >= w.m_valid || n >= a.n) continue;
+      float v[8];
+      const f32x4_t lo = *(const MUON_LDS f32x4_t*)(strip + r * G::SP + c);
+      const f32x4_t hi = *(const MUON_LDS f32x4_t*)(strip + r * G::SP + c + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = lo[e];
+        v[4 + e] = hi[e];
+      }
+      finish<F32, MODE, VEC>(a, w.group, w.part, w.row0 + ms + r, n, v);
+    }
+  }
+}
+
 template <bool F32, int MODE, typename G, bool VEC>
 __global__ __launch_bounds__(G::NT, 1) void k_linear(LinArgs a, int run) {
-  constexpr int ES = F32 ? 4 : 2, LBK = 128 / ES;
-  constexpr bool PKM = MODE == LIN_WEIGHT, QKM = MODE != LIN_FORWARD;
-  __shared__ __attribute__((aligned(16))) char ring0[G::STAGE];
-  __shared__ __attribute__((aligned(16))) char ring1[G::STAGE];
+  constexpr int ES = F32 ? 4 : 2, LBK = KB / ES;
+  // (Arrays of their own, so that the compiler can tell a read of one unit
+  // from a load into another.)
+  __shared__ __attribute__((aligned(16))) char unit0[G::UNIT];
+  __shared__ __attribute__((aligned(16))) char unit1[G::UNIT];
+  __shared__ __attribute__((aligned(16))) char unit2[G::U > 2 ? G::UNIT : 16];
+  __shared__ __attribute__((aligned(16))) char unit3[G::U > 3 ? G::UNIT : 16];
+  __shared__ __attribute__((aligned(16))) char unit4[G::U > 4 ? G::UNIT : 16];
   const int idx = tile_of(blockIdx.x, run), nt = (a.n + G::BN - 1) / G::BN;
   Group g;
-  int rt, ct, part = 0, k, m_valid;
-  int64_t row0;   // first row of the tile (weight gradient: of the group's part)
-  const char *p, *q;
+  Tile w;
+  int rt, ct;
+  w.part = 0;
   if constexpr (MODE == LIN_WEIGHT) {
     const int mt = (a.m + G::BM - 1) / G::BM;
     if (idx >= mt * nt * a.groups * a.parts) return;
     const int gi = idx / (mt * nt);
-    part = gi / a.groups;
+    w.part = gi / a.groups;
     g.index = gi % a.groups;
     g.lo = a.offsets ? clamped(gmem(a.offsets)[g.index], 0, a.rows) : 0;
     g.hi = a.offsets ? clamped(gmem(a.offsets)[g.index + 1], g.lo, a.rows) : a.rows;
     block_order(idx % (mt * nt), mt, nt, rt, ct);
     const int rows = g.hi - g.lo;
     const int per = a.parts > 1 ? ((rows + a.parts - 1) / a.parts + LBK - 1) / LBK * LBK : rows;
-    const int first = static_cast<int>(min(static_cast<int64_t>(rows), static_cast<int64_t>(part) * per));
-    k = min(per, rows - first);
-    row0 = g.lo + first;
-    m_valid = min(G::BM, a.m - rt * G::BM);
-    p = static_cast<const char*>(a.p) + (row0 * a.ldp + rt * G::BM) * ES;
-    q = static_cast<const char*>(a.q) + (row0 * a.ldq + ct * G::BN) * ES;
+    const int first = static_cast<int>(min(static_cast<int64_t>(rows), static_cast<int64_t>(w.part) * per));
+    w.k = min(per, rows - first);
+    const int64_t from = g.lo + first;
+    w.row0 = rt * G::BM;
+    w.m_valid = min(G::BM, a.m - rt * G::BM);
+    w.p = static_cast<const char*>(a.p) + (from * a.ldp + rt * G::BM) * ES;
+    w.q = static_cast<const char*>(a.q) + (from * a.ldq + ct * G::BN) * ES;
   } else {
     int local;
     if (!find_rows(a, idx, G::BM, nt, g, local)) return;
     block_order(local, (g.hi - g.lo + G::BM - 1) / G::BM, nt, rt, ct);
-    k = a.k;
-    row0 = g.lo + rt * G::BM;
-    m_valid = min(G::BM, g.hi - static_cast<int>(row0));
-    p = static_cast<const char*>(a.p) + row0 * a.ldp * ES;
+    w.k = a.k;
+    w.row0 = g.lo + rt * G::BM;
+    w.m_valid = min(G::BM, g.hi - static_cast<int>(w.row0));
+    w.p = static_cast<const char*>(a.p) + w.row0 * a.ldp * ES;
     const int64_t at = static_cast<int64_t>(ct) * G::BN;
-    q = static_cast<const char*>(a.q) + (g.index * a.gq + (MODE == LIN_FORWARD ? at * a.ldq : at)) * ES;
+    w.q = static_cast<const char*>(a.q) + (g.index * a.gq + (MODE == LIN_FORWARD ? at * a.ldq : at)) * ES;
   }
-  const int n0 = ct * G::BN, n_valid = min(G::BN, a.n - n0);
-  f32x16_t acc[G::MS][G::NS];
-#pragma unroll
-  for (int s = 0; s < G::MS; ++s)
-#pragma unroll
-    for (int t = 0; t < G::NS; ++t)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[s][t][e] = 0.0f;
-  const Operand<F32, PKM, G::BM, G::NT> P(p, a.ldp, m_valid, k);
-  const Operand<F32, QKM, G::BN, G::NT> Q(q, a.ldq, n_valid, k);
-  product<F32, PKM, QKM, G, VEC>(P, Q, k, ring0, ring1, acc);
-
-  // Through the wave's strip: a lane puts four columns of one row at a time
-  // and takes eight, so that global accesses are whole 16-byte runs.
-  __syncthreads();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* strip = reinterpret_cast<float*>((wave & 1 ? ring1 : ring0) + (wave >> 1) * G::STRIP);
-  constexpr int CPR = G::WN / 8;
-  const int m_out = MODE == LIN_WEIGHT ? rt * G::BM : 0;
-  // (One copy of what follows the sums, for all blocks of rows.)
-#pragma unroll 1
-  for (int s = 0; s < G::MS; ++s) {
-    const int ms = (wave / G::WC) * G::WM + s * 32;
-    if (ms >= m_valid) break;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int b = 0; b < G::MS; ++b)
-      if (b == s) {
-#pragma unroll
-        for (int t = 0; t < G::NS; ++t)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<f32x4_t*>(strip + (lane & 31) * G::SP + t * 32 + 8 * u + 4 * (lane >> 5)) =
-                f32x4_t{acc[b][t][4 * u], acc[b][t][4 * u + 1], acc[b][t][4 * u + 2], acc[b][t][4 * u + 3]};
+  w.group = g.index;
+  w.n0 = ct * G::BN;
+  w.n_valid = min(G::BN, a.n - w.n0);
+  if constexpr (G::U == 5) {
+    char* const ring[5] = {unit0, unit1, unit2, unit3, unit4};
+    // A tile that is less than half full in one direction takes half the time.
+    if constexpr (G::BM == 256 && G::BN == 256) {
+      if (w.n_valid <= 128) {
+        tile<F32, MODE, Geo<256, 128, 4, 1, 5, G::UNIT>, VEC>(a, w, ring);
+        return;
       }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-    for (int i = lane; i < 32 * CPR; i += 64) {
-      const int r = i / CPR, c = (i % CPR) * 8;
-      const int n = n0 + (wave % G::WC) * G::WN + c;
-      if (ms + r >= m_valid || n >= a.n) continue;
-      float v[8];
-      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(strip + r * G::SP + c);
-      const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(strip + r * G::SP + c + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = lo[e];
-        v[4 + e] = hi[e];
+      if (w.m_valid <= 128) {
+        tile<F32, MODE, Geo<128, 256, 1, 4, 5, G::UNIT>, VEC>(a, w, ring);
+        return;
       }
-      finish<F32, MODE, VEC>(a, g.index, part, (MODE == LIN_WEIGHT ? m_out : row0) + ms + r, n, v);
     }
+    tile<F32, MODE, G, VEC>(a, w, ring);
+  } else if constexpr (G::U == 4) {
+    char* const ring[4] = {unit0, unit1, unit2, unit3};
+    tile<F32, MODE, G, VEC>(a, w, ring);
+  } else {
+    char* const ring[2] = {unit0, unit1};
+    tile<F32, MODE, G, VEC>(a, w, ring);
   }
 }
 
@@ -634,8 +748,7 @@ __global__ __launch_bounds__(kPassThreads) void k_linear_slope(const void* dy, i
     float g[8], z[8];
     load_run<VEC>(dy, r * ld_dy + c, out - c, F32, g);
     load_run<VEC>(pre, r * ld_pre + c, out - c, F32, z);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] *= slope(act, z[e]);
+    times_slope8<F32>(act, z, g);
     store_run<VEC>(dz, r * ld_dz + c, out - c, F32, g);
   }
 }
@@ -686,9 +799,10 @@ __global__ __launch_bounds__(kPassThreads) void k_linear_join(const float* part,
   }
 }
 
-using Large = Geo<256, 256, 2, 4>;
-using Medium = Geo<128, 128, 2, 2>;
-using Small = Geo<64, 128, 1, 4>;
+using Large = Geo<256, 256, 2, 2, 5>;
+using Medium = Geo<128, 128, 2, 2, 5>;
+using Plain = Geo<128, 128, 2, 2, 2, 2 * Medium::STRIP>;   // operands through registers
+using Small = Geo<64, 128, 1, 4, 4>;
 
 int64_t ceil_of(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -717,12 +831,12 @@ hipError_t go(const LinArgs& a, bool dry, hipStream_t s) {
 
 template <int MODE>
 hipError_t pick(const LinArgs& a, int dt, bool vec, bool dry, hipStream_t s) {
-  if (dt == DT_F32) return vec ? go<true, MODE, Medium, true>(a, dry, s) : go<true, MODE, Medium, false>(a, dry, s);
-  if (!vec) return go<false, MODE, Medium, false>(a, dry, s);
+  if (dt == DT_F32) return vec ? go<true, MODE, Medium, true>(a, dry, s) : go<true, MODE, Plain, false>(a, dry, s);
+  if (!vec) return go<false, MODE, Plain, false>(a, dry, s);
   if constexpr (MODE != LIN_WEIGHT) {
     if (a.rows / a.groups <= 96) return go<false, MODE, Small, true>(a, dry, s);
   }
-  if (tiles_at_most<Large>(a, MODE) >= 512) return go<false, MODE, Large, true>(a, dry, s);
+  if (tiles_at_most<Large>(a, MODE) >= 256) return go<false, MODE, Large, true>(a, dry, s);
   return go<false, MODE, Medium, true>(a, dry, s);
 }
 
