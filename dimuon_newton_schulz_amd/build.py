@@ -1,10 +1,12 @@
-"""Builds libmuon_mi355x.so for gfx950 with hipcc (in-tree, no JIT cache)."""
+"""Builds libmuon_mi355x.so for gfx950 with hipcc, and the package's extension
+module with the host compiler (in-tree, no JIT cache)."""
 
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +18,8 @@ LIB = os.path.join(PKG, "libmuon_mi355x.so")
 SOURCES = ["api.hip", "stream_kernels.hip", "gemm_kernels.hip", "thin_kernel.hip",
            "adamw_api.hip", "adamw_kernels.hip", "norm_kernel.hip",
            "expert_api.hip", "expert_kernels.hip", "linear_kernels.hip"]
+
+BINDING = os.path.join(PKG, "_binding.so")   # csrc/binding.cpp
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -35,6 +39,21 @@ def _run(cmd):
     return out
 
 
+def build_binding():
+    """The extension module that marshals short calls: host code against torch's C++ headers."""
+    import torch
+
+    home, rocm = os.path.dirname(torch.__file__), os.path.dirname(os.path.dirname(HIPCC))
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(rocm, "include"), INCLUDE, sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__=1",
+          "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include),
+          os.path.join(CSRC, "binding.cpp"), f"-L{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_hip", "-o", tmp])
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, jobs: int = 4) -> str:
     """Compile every source and link the shared library; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -47,7 +66,9 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, LIB)

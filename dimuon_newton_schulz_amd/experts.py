@@ -15,7 +15,8 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import (_DT_CODE, _check, _check_workspace, _gpu_device, _ptr, _torch_stream, _workspace_on, load_library)
+from . import (_DT_CODE, _check, _check_workspace, _current_raw_stream, _ptr, _stream_handle, _torch_stream,
+               _workspace_on, load_library)
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -64,28 +65,71 @@ def bind(lib):
                        ("linear_grad", [ctypes.POINTER(LinearGradArgs), vp, size, vp])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
+    global _fast
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError(f"{__package__}._binding is missing: build it with `python -m {__package__}.build`") from e
+    _binding.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in
+                    ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "linear_forward")))
+    _fast = _binding
+
+
+# The ordinary case of a call (current GPU and stream, tensors as expected) is
+# marshalled natively: csrc/binding.cpp.  None from it: not that case, and the
+# Python code goes on.
+_fast = None
+
+
+def _native():
+    if _fast is None:
+        load_library()
+    return _fast
+
+
+def _done(result):
+    """What a native call made, or its failing status."""
+    if result.__class__ is int:
+        _check(result)
+    return result
 
 
 # ---------------------------------------------------------------------------
-# Checks
+# Checks.  A short call's host time is these, so the common case of each takes
+# a few attribute reads; the function behind it says what is wrong.
 # ---------------------------------------------------------------------------
-def _tensor(t, name, device, shape, dtype):
-    """A tensor argument: on the call's device, of this shape and one of these
-    dtypes, its rows' elements consecutive."""
+_MAX_STRIDE = 1 << 20
+_FLOATS = tuple(_DT_CODE)
+_INTS = (torch.int32, torch.int64)
+
+
+def _tensor(t, name, index, shape, dtype):
+    """A tensor argument: on GPU `index` (None: anywhere), of this shape and
+    one of these dtypes."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's tensors on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors on {_device_name(index)}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} is {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name} is {t.dtype}, expected one of {dtype}")
 
 
-def _rows(t, name, device, shape, dtype) -> int:
-    """Row stride of a 2-D argument."""
-    _tensor(t, name, device, shape, dtype)
+def _device_name(index):
+    return "the CPU" if index < 0 else f"GPU {index}"
+
+
+def _rows(t, name, index, shape, dtype) -> int:
+    """Row stride of a 2-D argument whose rows' elements are consecutive."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+            a, b = t.stride()
+            if b == 1 and shape[1] <= a <= _MAX_STRIDE:
+                return a
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _tensor(t, name, index, shape, dtype)
     if t.dim() != 2:
         raise ValueError(f"{name} must have rows and columns, got shape {tuple(t.shape)}")
     if t.shape[1] > 1 and t.stride(1) != 1:
@@ -95,22 +139,63 @@ def _rows(t, name, device, shape, dtype) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
 
 
-def _dense(t, name, device, shape, dtype):
-    _tensor(t, name, device, shape, dtype)
+def _dense(t, name, index, shape, dtype):
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _tensor(t, name, index, shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _output(t, name, device, shape, dtype, ts) -> torch.Tensor:
-    """The caller's output, or a new one on the launch stream."""
-    if t is None:
-        with torch.cuda.stream(ts):
-            t = torch.empty(shape, dtype=dtype, device=device)
-    return t
+def _matrix(t, name):
+    """Shape and dtype of a call's leading 2-D argument."""
+    _tensor(t, name, None, None, _FLOATS)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have rows and columns, got shape {tuple(t.shape)}")
+    return t.shape, t.dtype
 
 
-_FLOATS = tuple(_DT_CODE)
-_INTS = (torch.int32, torch.int64)
+class _Launch:
+    """Where a call runs: the GPU of its tensors and the launch stream."""
+    __slots__ = ("index", "stream", "given")
+
+    def __init__(self, index, stream):
+        if index < 0:
+            raise ValueError("the tensors are on the CPU: they must be on the GPU")
+        self.index, self.given = index, stream
+        if stream is None and _current_raw_stream is not None:
+            self.stream = _current_raw_stream(index)
+        else:
+            self.stream = _stream_handle(stream, torch.device("cuda", index))
+
+    def empty(self, shape, dtype):
+        """A new tensor that belongs to the launch stream."""
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
+        with torch.cuda.stream(_torch_stream(self.given, torch.device("cuda", self.index))):
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
+
+    def workspace(self, given, nbytes):
+        """The caller's workspace, or one that the allocator keeps until the
+        launch stream is done with it: (pointer, bytes, tensor)."""
+        if given is None:
+            if not nbytes:
+                return None, 0, None
+            device = torch.device("cuda", self.index)
+            given = _workspace_on(None, nbytes, device, _torch_stream(self.given, device))
+        return given.data_ptr(), given.numel(), given
+
+    def call(self, fn, *args):
+        if torch.cuda.current_device() == self.index:
+            status = fn(*args, self.stream)
+        else:
+            with torch.cuda.device(self.index):
+                status = fn(*args, self.stream)
+        if status:
+            _check(status)
 
 
 # ---------------------------------------------------------------------------
@@ -138,22 +223,25 @@ class ExpertRoutes:
         return self.place.shape[1]
 
     def to_c(self) -> ExpertRoutesC:
-        device = self.place.device if isinstance(self.place, torch.Tensor) else None
-        _dense(self.place, "routes.place", device, None, torch.int32)
-        if self.place.dim() != 2:
-            raise ValueError(f"routes.place must be (tokens, top), got {tuple(self.place.shape)}")
-        _dense(self.offsets, "routes.offsets", device, None, torch.int32)
-        if self.offsets.dim() != 1 or self.offsets.numel() < 2:
-            raise ValueError(f"routes.offsets must hold experts + 1 numbers, got shape {tuple(self.offsets.shape)}")
-        _dense(self.order, "routes.order", device, (self.place.numel(),), torch.int32)
-        return ExpertRoutesC(self.offsets.data_ptr(), self.order.data_ptr(), self.place.data_ptr(), self.tokens,
-                             self.top, self.experts)
+        place, offsets, order = self.place, self.offsets, self.order
+        try:
+            index, (tokens, top), n = place.get_device(), place.shape, offsets.numel()
+        except (AttributeError, ValueError):
+            raise ValueError("routes.place must be (tokens, top), routes.offsets a tensor") from None
+        _dense(place, "routes.place", index, place.shape, torch.int32)
+        _dense(offsets, "routes.offsets", index, (n,), torch.int32)
+        _dense(order, "routes.order", index, (tokens * top,), torch.int32)
+        if n < 2:
+            raise ValueError(f"routes.offsets must hold experts + 1 numbers, got {n}")
+        return ExpertRoutesC(offsets.data_ptr(), order.data_ptr(), place.data_ptr(), tokens, top, n - 1)
 
 
-def _routes(routes) -> ExpertRoutesC:
+def _routes(routes):
+    """(expert_routes_t, its address for a call, GPU)."""
     if not isinstance(routes, ExpertRoutes):
         raise ValueError(f"routes must be ExpertRoutes, got {type(routes).__name__}")
-    return routes.to_c()
+    c = routes.to_c()
+    return c, ctypes.byref(c), routes.place.get_device()
 
 
 def expert_sort(ids: torch.Tensor, experts: int, routes: Optional[ExpertRoutes] = None,
@@ -161,29 +249,39 @@ def expert_sort(ids: torch.Tensor, experts: int, routes: Optional[ExpertRoutes] 
     """Sorts the choices of a batch by expert: ``ids`` (tokens, top), int32 or
     int64, each 0..experts-1, or another number for a choice that is not
     routed.  Returns (fills, if given) ``routes``.  The sort is stable."""
-    _dense(ids, "ids", None, None, _INTS)
+    if routes is None and workspace is None and stream is None:
+        done = _native().sort(ids, experts)
+        if done is not None:
+            return ExpertRoutes(*_done(done))
+    _tensor(ids, "ids", None, None, _INTS)
     if ids.dim() != 2 or ids.shape[1] < 1:
         raise ValueError(f"ids must be (tokens, top), got {tuple(ids.shape)}")
-    lib, nbytes = load_library(), ctypes.c_size_t(0)
-    tokens, top = ids.shape
-    _check(lib.expert_sort_workspace_bytes(tokens, top, experts, ctypes.byref(nbytes)))
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    lib, (tokens, top) = load_library(), ids.shape
+    nbytes = 0
+    if tokens * top > _SORT_ALONE or not 0 < experts <= _MAX_EXPERTS:   # otherwise none is needed
+        size = ctypes.c_size_t(0)
+        _check(lib.expert_sort_workspace_bytes(tokens, top, experts, ctypes.byref(size)))
+        nbytes = size.value
     _check_workspace(workspace, ids.device)
-    device = _gpu_device(ids.device)
-    ts = _torch_stream(stream, device)
+    on = _Launch(ids.get_device(), stream)
     if routes is None:
-        flat = _output(None, "routes", device, (experts + 1 + 2 * tokens * top,), torch.int32, ts)
         n = tokens * top
-        routes = ExpertRoutes(flat[2 * n:], flat[:n], flat[n:2 * n].view(tokens, top))
-    c = _routes(routes)
-    _tensor(routes.place, "routes.place", device, (tokens, top), torch.int32)
-    if c.experts != experts:
-        raise ValueError(f"routes are of {c.experts} experts, the call of {experts}")
-    if workspace is None and nbytes.value:
-        workspace = _workspace_on(None, nbytes.value, device, ts)
-    with torch.cuda.device(device):
-        _check(lib.expert_sort(ids.data_ptr(), ids.element_size(), ctypes.byref(c), _ptr(workspace),
-                               0 if workspace is None else workspace.numel(), ts.cuda_stream))
+        offsets, order, place = on.empty(experts + 1 + 2 * n, torch.int32).split((experts + 1, n, n))
+        c = ExpertRoutesC(offsets.data_ptr(), order.data_ptr(), place.data_ptr(), tokens, top, experts)
+        routes = ExpertRoutes(offsets, order, place.view(tokens, top))
+    else:
+        c, _, _ = _routes(routes)
+        _dense(routes.place, "routes.place", on.index, (tokens, top), torch.int32)
+        if c.experts != experts:
+            raise ValueError(f"routes are of {c.experts} experts, the call of {experts}")
+    ws, ws_bytes, _keep = on.workspace(workspace, nbytes)
+    on.call(lib.expert_sort, ids.data_ptr(), ids.element_size(), ctypes.byref(c), ws, ws_bytes)
     return routes
+
+
+_SORT_ALONE, _MAX_EXPERTS = 8192, 1024   # a sort of that many slots needs no workspace
 
 
 def expert_gather(x: torch.Tensor, routes: ExpertRoutes, out: Optional[torch.Tensor] = None,
@@ -191,22 +289,25 @@ def expert_gather(x: torch.Tensor, routes: ExpertRoutes, out: Optional[torch.Ten
     """Every token's row to its sorted rows: (tokens, width) to (tokens * top,
     width).  Rows behind the last routed one are left as they were (undefined
     in a new ``out``).  The gradient is ``expert_combine`` without weights."""
-    c = _routes(routes)
-    device = _gpu_device(routes.place.device)
-    ld = _rows(x, "x", device, None, _FLOATS)
-    _tensor(x, "x", device, (c.tokens, x.shape[1]), _FLOATS)
-    ts = _torch_stream(stream, device)
-    shape = (c.tokens * c.top, x.shape[1])
-    out = _output(out, "out", device, shape, x.dtype, ts)
-    ld_out = _rows(out, "out", device, shape, x.dtype)
-    with torch.cuda.device(device):
-        _check(load_library().expert_gather(x.data_ptr(), ld, x.shape[1], _DT_CODE[x.dtype], ctypes.byref(c),
-                                            out.data_ptr(), ld_out, ts.cuda_stream))
+    if stream is None and routes.__class__ is ExpertRoutes:
+        done = _native().gather(x, routes.offsets, routes.order, routes.place, out)
+        if done is not None:
+            return _done(done)
+    c, ref, index = _routes(routes)
+    (_, width), dt = _matrix(x, "x")
+    ld = _rows(x, "x", index, (c.tokens, width), dt)
+    on, shape = _Launch(index, stream), (c.tokens * c.top, width)
+    if out is None:
+        out = on.empty(shape, dt)
+    ld_out = _rows(out, "out", index, shape, dt)
+    on.call(load_library().expert_gather, x.data_ptr(), ld, width, _DT_CODE[dt], ref, out.data_ptr(), ld_out)
     return out
 
 
-def _weights(weights, device, c):
-    _dense(weights, "weights", device, (c.tokens, c.top), _FLOATS)
+def _weights(weights, index, c):
+    _tensor(weights, "weights", index, (c.tokens, c.top), _FLOATS)
+    if not weights.is_contiguous():
+        raise ValueError("weights must be contiguous")
     return weights.data_ptr(), _DT_CODE[weights.dtype]
 
 
@@ -216,19 +317,22 @@ def expert_combine(ys: torch.Tensor, routes: ExpertRoutes, weights: Optional[tor
     """Sorted rows back to their tokens: ``residual`` + the sum over a token's
     choices of ``weights`` * row (``weights`` (tokens, top), float32 or
     bfloat16).  ``out`` may be the residual itself."""
-    c = _routes(routes)
-    device = _gpu_device(routes.place.device)
-    ld = _rows(ys, "ys", device, None, _FLOATS)
-    _tensor(ys, "ys", device, (c.tokens * c.top, ys.shape[1]), _FLOATS)
-    shape = (c.tokens, ys.shape[1])
-    w, w_dt = (None, 0) if weights is None else _weights(weights, device, c)
-    ld_res = 0 if residual is None else _rows(residual, "residual", device, shape, ys.dtype)
-    ts = _torch_stream(stream, device)
-    out = _output(out, "out", device, shape, ys.dtype, ts)
-    ld_out = _rows(out, "out", device, shape, ys.dtype)
-    with torch.cuda.device(device):
-        _check(load_library().expert_combine(ys.data_ptr(), ld, ys.shape[1], _DT_CODE[ys.dtype], ctypes.byref(c), w,
-                                             w_dt, _ptr(residual), ld_res, out.data_ptr(), ld_out, ts.cuda_stream))
+    if stream is None and routes.__class__ is ExpertRoutes:
+        done = _native().combine(ys, routes.offsets, routes.order, routes.place, weights, residual, out)
+        if done is not None:
+            return _done(done)
+    c, ref, index = _routes(routes)
+    (_, width), dt = _matrix(ys, "ys")
+    ld = _rows(ys, "ys", index, (c.tokens * c.top, width), dt)
+    shape = (c.tokens, width)
+    w, w_dt = (None, 0) if weights is None else _weights(weights, index, c)
+    res, ld_res = (None, 0) if residual is None else (residual.data_ptr(), _rows(residual, "residual", index, shape, dt))
+    on = _Launch(index, stream)
+    if out is None:
+        out = on.empty(shape, dt)
+    ld_out = _rows(out, "out", index, shape, dt)
+    on.call(load_library().expert_combine, ys.data_ptr(), ld, width, _DT_CODE[dt], ref, w, w_dt, res, ld_res,
+            out.data_ptr(), ld_out)
     return out
 
 
@@ -237,22 +341,25 @@ def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tenso
                         stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Gradient of ``expert_combine`` with weights: (dys, dweights).  The
     residual's is dy itself."""
-    c = _routes(routes)
-    device = _gpu_device(routes.place.device)
-    ld = _rows(ys, "ys", device, None, _FLOATS)
-    shape = (c.tokens * c.top, ys.shape[1])
-    _tensor(ys, "ys", device, shape, _FLOATS)
-    ld_dy = _rows(dy, "dy", device, (c.tokens, ys.shape[1]), ys.dtype)
-    w, w_dt = _weights(weights, device, c)
-    ts = _torch_stream(stream, device)
-    dys = _output(dys, "dys", device, shape, ys.dtype, ts)
-    ld_dys = _rows(dys, "dys", device, shape, ys.dtype)
-    dweights = _output(dweights, "dweights", device, weights.shape, weights.dtype, ts)
-    _dense(dweights, "dweights", device, weights.shape, weights.dtype)
-    with torch.cuda.device(device):
-        _check(load_library().expert_combine_grad(dy.data_ptr(), ld_dy, ys.data_ptr(), ld, ys.shape[1],
-                                                  _DT_CODE[ys.dtype], ctypes.byref(c), w, w_dt, dys.data_ptr(),
-                                                  ld_dys, dweights.data_ptr(), ts.cuda_stream))
+    if stream is None and routes.__class__ is ExpertRoutes:
+        done = _native().combine_grad(dy, ys, weights, routes.offsets, routes.order, routes.place, dys, dweights)
+        if done is not None:
+            return _done(done)
+    c, ref, index = _routes(routes)
+    (_, width), dt = _matrix(ys, "ys")
+    shape = (c.tokens * c.top, width)
+    ld = _rows(ys, "ys", index, shape, dt)
+    ld_dy = _rows(dy, "dy", index, (c.tokens, width), dt)
+    w, w_dt = _weights(weights, index, c)
+    on = _Launch(index, stream)
+    if dys is None:
+        dys = on.empty(shape, dt)
+    ld_dys = _rows(dys, "dys", index, shape, dt)
+    if dweights is None:
+        dweights = on.empty(weights.shape, weights.dtype)
+    _dense(dweights, "dweights", index, weights.shape, weights.dtype)
+    on.call(load_library().expert_combine_grad, dy.data_ptr(), ld_dy, ys.data_ptr(), ld, width, _DT_CODE[dt], ref, w,
+            w_dt, dys.data_ptr(), ld_dys, dweights.data_ptr())
     return dys, dweights
 
 
@@ -265,25 +372,31 @@ def _activation(name) -> int:
     return ACTIVATIONS[name]
 
 
-def _weight(w, name, device, shape, dtype):
+def _weight(w, name, index, dtype):
     """(groups, out, in, row stride, group stride) of a weight: (out, in), or
     (groups, out, in)."""
-    _tensor(w, name, device, shape, dtype)
-    if w.dim() not in (2, 3):
-        raise ValueError(f"{name} must be (out, in) or (groups, out, in), got {tuple(w.shape)}")
-    groups, (out, inn) = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2:]
-    if inn > 1 and w.stride(-1) != 1:
+    _tensor(w, name, index, None, dtype)
+    shape, strides = w.shape, w.stride()
+    if len(shape) == 3:
+        groups, out, inn = shape
+        if strides[2] == 1 and strides[1] >= inn and (strides[0] >= out * strides[1] or groups == 1) and out > 1:
+            return groups, out, inn, strides[1], strides[0] if groups > 1 else out * strides[1]
+    elif len(shape) == 2:
+        groups, (out, inn) = 1, shape
+    else:
+        raise ValueError(f"{name} must be (out, in) or (groups, out, in), got {tuple(shape)}")
+    if inn > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: a row's elements must be consecutive")
-    ld = w.stride(-2) if out > 1 else max(1, inn)
-    return groups, out, inn, ld, (w.stride(0) if groups > 1 else out * ld)
+    ld = strides[-2] if out > 1 else max(1, inn)
+    return groups, out, inn, ld, (strides[0] if groups > 1 else out * ld)
 
 
-def _groups(offsets, w, groups, device):
+def _groups(offsets, groups, index):
     if offsets is None:
         if groups != 1:
             raise ValueError(f"{groups} groups need offsets")
         return None
-    _dense(offsets, "offsets", device, (groups + 1,), torch.int32)
+    _dense(offsets, "offsets", index, (groups + 1,), torch.int32)
     return offsets.data_ptr()
 
 
@@ -298,26 +411,30 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     receives x w^T + bias, which ``linear_grad`` wants where there is an
     activation.  ``out`` may be the residual itself."""
     act = _activation(activation)
-    ld = _rows(x, "x", None, None, _FLOATS)
-    groups, n, k, ld_w, group_w = _weight(w, "w", x.device, None, x.dtype)
-    rows = x.shape[0]
-    _tensor(x, "x", None, (rows, k), x.dtype)
-    device, shape = x.device, (rows, n)
+    if stream is None:
+        done = _native().linear(x, w, bias, act, residual, offsets, pre, out)
+        if done is not None:
+            return _done(done)
+    (rows, k), dt = _matrix(x, "x")
+    index = x.get_device()
+    groups, n, k_w, ld_w, group_w = _weight(w, "w", index, dt)
+    if k_w != k:
+        raise ValueError(f"x has {k} columns, the weight {k_w}")
+    shape = (rows, n)
+    ld = _rows(x, "x", index, (rows, k), dt)
     if bias is not None:
-        _dense(bias, "bias", device, w.shape[:-1], x.dtype)
-    off = _groups(offsets, w, groups, device)
-    ld_res = 0 if residual is None else _rows(residual, "residual", device, shape, x.dtype)
-    ld_pre = 0 if pre is None else _rows(pre, "pre", device, shape, x.dtype)
-    if out is not None:
-        _rows(out, "out", device, shape, x.dtype)
-    device = _gpu_device(device)
-    ts = _torch_stream(stream, device)
-    out = _output(out, "out", device, shape, x.dtype, ts)
-    a = LinearArgs(rows, k, n, groups, off, _DT_CODE[x.dtype], act, x.data_ptr(), ld, w.data_ptr(), ld_w, group_w,
-                   _ptr(bias), _ptr(residual), ld_res, out.data_ptr(), _rows(out, "out", device, shape, x.dtype),
-                   _ptr(pre), ld_pre)
-    with torch.cuda.device(device):
-        _check(load_library().linear_forward(ctypes.byref(a), ts.cuda_stream))
+        _dense(bias, "bias", index, w.shape[:-1], dt)
+    off = _groups(offsets, groups, index)
+    ld_res = 0 if residual is None else _rows(residual, "residual", index, shape, dt)
+    ld_pre = 0 if pre is None else _rows(pre, "pre", index, shape, dt)
+    ld_out = 0 if out is None else _rows(out, "out", index, shape, dt)
+    on = _Launch(index, stream)
+    if out is None:
+        out = on.empty(shape, dt)
+        ld_out = max(1, n)
+    a = LinearArgs(rows, k, n, groups, off, _DT_CODE[dt], act, x.data_ptr(), ld, w.data_ptr(), ld_w, group_w,
+                   _ptr(bias), _ptr(residual), ld_res, out.data_ptr(), ld_out, _ptr(pre), ld_pre)
+    on.call(load_library().linear_forward, ctypes.byref(a))
     return out
 
 
@@ -337,59 +454,60 @@ def linear_grad(dy: torch.Tensor, x: Optional[torch.Tensor] = None, w: Optional[
     act, x_act = _activation(activation), _activation(x_activation)
     if dx is None and dw is None and db is None:
         raise ValueError("give at least one of dx, dw and db")
-    ld_dy = _rows(dy, "dy", None, None, _FLOATS)
-    rows, n = dy.shape
-    device, dt = dy.device, dy.dtype
+    (rows, n), dt = _matrix(dy, "dy")
+    index = dy.get_device()
+    ld_dy = _rows(dy, "dy", index, (rows, n), dt)
     weight = w if w is not None else dw
     if weight is not None:
-        groups, out, k, _, _ = _weight(weight, "w" if w is not None else "dw", device, None, _FLOATS)
+        groups, out, k, ld_w, group_w = _weight(weight, "w" if w is not None else "dw", index, _FLOATS)
+        grouped = weight.dim() == 3
         if out != n:
             raise ValueError(f"the weight has {out} rows, dy {n} columns")
     else:
-        groups, k = (db.shape[0] if db.dim() == 2 else 1), 1
-    a = LinearGradArgs(rows=rows, in_=k, out=n, groups=groups, dtype=_DT_CODE[dt], activation=act,
-                       x_activation=x_act, accumulate=1 if accumulate else 0, dy=dy.data_ptr(), dy_stride=ld_dy)
-    grouped = weight.dim() == 3 if weight is not None else db.dim() == 2
-    a.offsets = _groups(offsets, weight, groups, device)
+        grouped = db.dim() == 2
+        groups, k = (db.shape[0] if grouped else 1), 1
+    a = LinearGradArgs(rows, k, n, groups, _groups(offsets, groups, index), _DT_CODE[dt], 0, act, x_act,
+                       1 if accumulate else 0, 0, dy.data_ptr(), ld_dy)
     if act:
         if pre is None:
             raise ValueError(f"the gradient through {activation} needs pre")
-        a.pre_stride = _rows(pre, "pre", device, (rows, n), dt)
+        a.pre_stride = _rows(pre, "pre", index, (rows, n), dt)
         a.pre = pre.data_ptr()
     if dx is not None:
         if w is None:
             raise ValueError("dx needs w")
-        _, _, _, a.w_stride, a.w_group_stride = _weight(w, "w", device, None, dt)
-        a.w = w.data_ptr()
-        a.dx_stride = _rows(dx, "dx", device, (rows, k), dt)
+        if w.dtype is not dt:
+            raise ValueError(f"w is {w.dtype}, dy {dt}")
+        a.w, a.w_stride, a.w_group_stride = w.data_ptr(), ld_w, group_w
+        a.dx_stride = _rows(dx, "dx", index, (rows, k), dt)
         a.dx = dx.data_ptr()
         if x_act:
             if x_pre is None:
                 raise ValueError(f"dx through {x_activation} needs x_pre")
-            a.x_pre_stride = _rows(x_pre, "x_pre", device, (rows, k), dt)
+            a.x_pre_stride = _rows(x_pre, "x_pre", index, (rows, k), dt)
             a.x_pre = x_pre.data_ptr()
     grad_dt = None
     if dw is not None:
         if x is None:
             raise ValueError("dw needs x")
-        a.x_stride = _rows(x, "x", device, (rows, k), dt)
+        a.x_stride = _rows(x, "x", index, (rows, k), dt)
         a.x = x.data_ptr()
-        _, _, _, a.dw_stride, a.dw_group_stride = _weight(dw, "dw", device, weight.shape, _FLOATS)
+        _, _, _, a.dw_stride, a.dw_group_stride = _weight(dw, "dw", index, _FLOATS)
+        if dw.shape != weight.shape:
+            raise ValueError(f"dw has shape {tuple(dw.shape)}, expected {tuple(weight.shape)}")
         a.dw, grad_dt = dw.data_ptr(), dw.dtype
     if db is not None:
-        _dense(db, "db", device, (groups, n) if grouped else (n,), _FLOATS if grad_dt is None else grad_dt)
+        shape = (groups, n) if grouped else (n,)
+        _tensor(db, "db", index, shape, _FLOATS if grad_dt is None else grad_dt)
+        _dense(db, "db", index, shape, db.dtype)
         a.db, grad_dt = db.data_ptr(), db.dtype
-    a.grad_dtype = _DT_CODE[grad_dt] if grad_dt is not None else a.dtype
-    lib, nbytes = load_library(), ctypes.c_size_t(0)
-    _check(lib.linear_grad_workspace_bytes(ctypes.byref(a), ctypes.byref(nbytes)))
-    _check_workspace(workspace, device)
-    device = _gpu_device(device)
-    ts = _torch_stream(stream, device)
-    if workspace is None and nbytes.value:
-        workspace = _workspace_on(None, nbytes.value, device, ts)
-    with torch.cuda.device(device):
-        _check(lib.linear_grad(ctypes.byref(a), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                               ts.cuda_stream))
+    a.grad_dtype = _DT_CODE[dt if grad_dt is None else grad_dt]
+    lib, ref, size = load_library(), ctypes.byref(a), ctypes.c_size_t(0)
+    _check_workspace(workspace, dy.device)
+    on = _Launch(index, stream)
+    _check(lib.linear_grad_workspace_bytes(ref, ctypes.byref(size)))
+    ws, ws_bytes, _keep = on.workspace(workspace, size.value)
+    on.call(lib.linear_grad, ref, ws, ws_bytes)
     return dx, dw, db
 
 
@@ -397,7 +515,7 @@ def linear_grad_workspace(rows: int, w: torch.Tensor, activation: str = "none", 
                           dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """A workspace for ``linear_grad`` over up to ``rows`` rows, to be used
     again and again (calls that share one must be ordered)."""
-    groups, n, k, _, _ = _weight(w, "w", None, None, _FLOATS)
+    groups, n, k, _, _ = _weight(w, "w", None, _FLOATS)
     dt = _DT_CODE[w.dtype if dtype is None else dtype]
     nbytes = ctypes.c_size_t(0)
     a = LinearGradArgs(rows=rows, in_=k, out=n, groups=groups, offsets=1, dtype=dt, activation=_activation(activation))
