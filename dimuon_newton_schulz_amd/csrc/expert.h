@@ -75,16 +75,18 @@ struct LinArgs {
   int32_t groups, act, c_dt, accumulate, parts;
 };
 
-hipError_t launch_linear(const LinArgs& a, int mode, int dt, bool vec, hipStream_t s);
+// `align`: 16 where every row lies on 16-byte borders and holds whole runs of
+// eight, 4 where rows lie on 4-byte borders, else 2.
+hipError_t launch_linear(const LinArgs& a, int mode, int dt, int align, hipStream_t s);
 // Whether the product's tiles fit one launch.
-bool linear_fits(const LinArgs& a, int mode, int dt, bool vec);
+bool linear_fits(const LinArgs& a, int mode, int dt, int align);
 // Sum of the parts of a weight gradient.
 hipError_t launch_linear_join(const LinArgs& a, hipStream_t s);
 // Parts that the rows of a weight gradient (a bias gradient) are split in.
 int linear_weight_parts(int64_t rows, int64_t out, int64_t in, int64_t groups);
 // dz = dy act'(pre) on the groups' rows.
 hipError_t launch_linear_slope(const void* dy, int64_t ld_dy, const void* pre, int64_t ld_pre, void* dz, int64_t ld_dz,
-                               const int32_t* offsets, int groups, int64_t rows, int64_t out, int act, int dt, bool vec,
+                               const int32_t* offsets, int groups, int64_t rows, int64_t out, int act, int dt, int align,
                                hipStream_t s);
 int linear_bias_parts(int64_t rows, int64_t groups);
 // db (+)= column sums of every group's rows, in `parts` parts.

@@ -41,7 +41,7 @@ bool overlap(const Buffer& a, const Buffer& b) {
 // Buffers of a call, checked as they are named.
 struct Buffers {
   std::vector<Buffer> all;
-  bool vec = true;   // rows on 16-byte borders
+  bool vec = true, dword = true;   // rows on 16-byte borders, on 4-byte borders
 
   muon_status_t add(const void* p, const char* what, int64_t rows, int64_t width, int64_t stride, size_t es, bool written,
                     int64_t groups = 1, int64_t group_stride = 0) {
@@ -56,7 +56,11 @@ struct Buffers {
     if (groups > 1 && group_stride > kMaxSide * kMaxStride)
       return fail(MUON_ERR_UNSUPPORTED, "%s: group stride %lld too large", what, (long long)group_stride);
     const int64_t e = static_cast<int64_t>(es);
-    if (reinterpret_cast<uintptr_t>(p) % 16 || stride * e % 16 || (groups > 1 && group_stride * e % 16)) vec = false;
+    const auto off = [&](int64_t n) {
+      return reinterpret_cast<uintptr_t>(p) % n || stride * e % n || (groups > 1 && group_stride * e % n);
+    };
+    if (off(16)) vec = false;
+    if (off(4)) dword = false;
     all.push_back({reinterpret_cast<uintptr_t>(p), rows, width * e, stride * e, groups, group_stride * e, what, written});
     return MUON_OK;
   }
@@ -75,6 +79,11 @@ struct Buffers {
     if (reinterpret_cast<uintptr_t>(p) % kAlign != 0) return fail(MUON_ERR_WORKSPACE, "workspace not 256-byte aligned");
     if (have < need) return fail(MUON_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", have, need);
     return list(p, "the workspace", static_cast<int64_t>(need), 1, true);
+  }
+  // Alignment of a product's rows (launch_linear).
+  int align(int64_t in, int64_t out, size_t es) const {
+    if (vec && in % 8 == 0 && out % 8 == 0) return 16;
+    return dword && in * es % 4 == 0 && out * es % 4 == 0 ? 4 : 2;
   }
   // `same`: a written buffer that may be the read one itself.
   muon_status_t disjoint(const char* written = nullptr, const char* read = nullptr) const {
@@ -385,10 +394,10 @@ muon_status_t linear_forward(const linear_args_t* p, void* stream) {
     a.act = p->activation;
     a.parts = 1;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const bool vec = b.vec && p->in % 8 == 0 && p->out % 8 == 0;
-    if (!linear_fits(a, LIN_FORWARD, p->dtype, vec)) return fail(MUON_ERR_UNSUPPORTED, "the product is too large");
+    const int align = b.align(p->in, p->out, es);
+    if (!linear_fits(a, LIN_FORWARD, p->dtype, align)) return fail(MUON_ERR_UNSUPPORTED, "the product is too large");
     MUON_HOOK_START();
-    MUON_LAUNCH(MUON_LAUNCH_LINEAR, launch_linear(a, LIN_FORWARD, p->dtype, vec, s));
+    MUON_LAUNCH(MUON_LAUNCH_LINEAR, launch_linear(a, LIN_FORWARD, p->dtype, align, s));
     return launched();
   });
 }
@@ -427,7 +436,7 @@ muon_status_t linear_grad(const linear_grad_args_t* p, void* workspace, size_t w
     if (p->db) MUON_CHECK(b.list(p->db, "db", p->groups * p->out, gs, true));
     MUON_CHECK(b.workspace(workspace, workspace_bytes, l.bytes));
     MUON_CHECK(b.disjoint());
-    const bool vec = b.vec && p->in % 8 == 0 && p->out % 8 == 0;
+    const int align = b.align(p->in, p->out, es);
     char* ws = static_cast<char*>(workspace);
     const void* dz = has_act ? ws + l.dz : p->dy;
     const int64_t dz_ld = has_act ? l.dz_ld : p->dy_stride;
@@ -459,16 +468,16 @@ muon_status_t linear_grad(const linear_grad_args_t* p, void* workspace, size_t w
     wt.accumulate = p->accumulate;
     wt.parts = l.parts;
     wt.part = reinterpret_cast<float*>(ws + l.part);
-    if ((p->dx && !linear_fits(in, LIN_INPUT, p->dtype, vec)) || (p->dw && !linear_fits(wt, LIN_WEIGHT, p->dtype, vec)))
+    if ((p->dx && !linear_fits(in, LIN_INPUT, p->dtype, align)) || (p->dw && !linear_fits(wt, LIN_WEIGHT, p->dtype, align)))
       return fail(MUON_ERR_UNSUPPORTED, "the product is too large");
     MUON_HOOK_START();
     if (has_act && p->rows)
       MUON_LAUNCH(MUON_LAUNCH_LINEAR_SLOPE,
                   launch_linear_slope(p->dy, p->dy_stride, p->pre, p->pre_stride, ws + l.dz, dz_ld, p->offsets,
-                                      in.groups, p->rows, p->out, p->activation, p->dtype, vec, s));
-    if (p->dx && p->rows) MUON_LAUNCH(MUON_LAUNCH_LINEAR_INPUT, launch_linear(in, LIN_INPUT, p->dtype, vec, s));
+                                      in.groups, p->rows, p->out, p->activation, p->dtype, align, s));
+    if (p->dx && p->rows) MUON_LAUNCH(MUON_LAUNCH_LINEAR_INPUT, launch_linear(in, LIN_INPUT, p->dtype, align, s));
     if (p->dw) {
-      MUON_HIP_TRY(launch_linear(wt, LIN_WEIGHT, p->dtype, vec, s));
+      MUON_HIP_TRY(launch_linear(wt, LIN_WEIGHT, p->dtype, align, s));
       if (l.parts > 1) MUON_HIP_TRY(launch_linear_join(wt, s));
       MUON_HIP_TRY(hook_record(MUON_LAUNCH_LINEAR_WEIGHT, s));
     }

@@ -73,13 +73,13 @@ __device__ __forceinline__ float slope(float z) {
   return s + z * s * (1.0f - s) * kTanhScale * (1.0f + 3.0f * kTanhCubic * z * z);
 }
 
-// v = act(v), and v *= act'(z): one branch for eight values.
-template <bool EXACT>
-__device__ __forceinline__ void activate8(int act, float (&v)[8]) {
+// v = act(v), and v *= act'(z): one branch for a run of values.
+template <bool EXACT, int N>
+__device__ __forceinline__ void activate_run(int act, float (&v)[N]) {
 #define MUON_EACH(ACT)            \
   case ACT:                       \
     _Pragma("unroll")             \
-    for (int e = 0; e < 8; ++e) v[e] = activate<ACT, EXACT>(v[e]); \
+    for (int e = 0; e < N; ++e) v[e] = activate<ACT, EXACT>(v[e]); \
     break
   switch (act) {
     MUON_EACH(LINEAR_RELU);
@@ -90,12 +90,12 @@ __device__ __forceinline__ void activate8(int act, float (&v)[8]) {
   }
 #undef MUON_EACH
 }
-template <bool EXACT>
-__device__ __forceinline__ void times_slope8(int act, const float (&z)[8], float (&v)[8]) {
+template <bool EXACT, int N>
+__device__ __forceinline__ void times_slope(int act, const float (&z)[N], float (&v)[N]) {
 #define MUON_EACH(ACT)            \
   case ACT:                       \
     _Pragma("unroll")             \
-    for (int e = 0; e < 8; ++e) v[e] *= slope<ACT, EXACT>(z[e]); \
+    for (int e = 0; e < N; ++e) v[e] *= slope<ACT, EXACT>(z[e]); \
     break
   switch (act) {
     MUON_EACH(LINEAR_RELU);
@@ -118,9 +118,12 @@ __device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? 
 
 // Workgroups are dealt to the 8 XCDs in turn; runs of `run` neighbouring
 // tiles, which share operand panels, go to one XCD and so one L2.
-__device__ __forceinline__ int tile_of(int bid, int run) {
-  const int xcd = bid & 7, i = bid >> 3;
-  return ((i / run) * 8 + xcd) * run + i % run;
+// `turn`: every other round of runs goes to the XCDs in reverse, so that runs
+// in order of falling work even out.
+__device__ __forceinline__ int tile_of(int bid, int run, bool turn) {
+  const int i = bid >> 3, round = i / run;
+  const int xcd = turn && (round & 1) ? 7 - (bid & 7) : bid & 7;
+  return (round * 8 + xcd) * run + i % run;
 }
 
 // Tile idx of the list that has every group's tiles of bm rows x nt columns
@@ -164,6 +167,40 @@ __device__ __forceinline__ bool find_rows(const LinArgs& a, int idx, int bm, int
   return false;
 }
 
+// The group with the p-th most rows, of at most kRanked groups (ties: the
+// lower number first): a wave ranks them all.
+constexpr int kRanked = 128;
+__device__ __forceinline__ int group_by_size(const LinArgs& a, int p) {
+  const int lane = threadIdx.x & 63;
+  const MUON_GLOBAL int32_t* off = gmem(a.offsets);
+  int n[kRanked / 64], rank[kRanked / 64];
+#pragma unroll
+  for (int j = 0; j < kRanked / 64; ++j) {
+    const int g = 64 * j + lane;
+    n[j] = -1;
+    rank[j] = 0;
+    if (g < a.groups) {
+      const int lo = clamped(off[g], 0, a.rows);
+      n[j] = clamped(off[g + 1], lo, a.rows) - lo;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kRanked / 64; ++h)
+    if (64 * h < a.groups)
+      for (int l = 0; l < 64; ++l) {
+        const int other = __builtin_amdgcn_readlane(n[h], l), g = 64 * h + l;
+#pragma unroll
+        for (int j = 0; j < kRanked / 64; ++j)
+          rank[j] += other > n[j] || (other == n[j] && g < 64 * j + lane) ? 1 : 0;
+      }
+#pragma unroll
+  for (int j = 0; j < kRanked / 64; ++j) {
+    const uint64_t hit = __ballot(rank[j] == p);
+    if (hit) return 64 * j + __builtin_ctzll(hit);
+  }
+  return p;
+}
+
 // Tile `local` of mt x nt: blocks of up to eight row tiles by all columns,
 // rows first, so that neighbours share panels of both operands.
 __device__ __forceinline__ void block_order(int local, int mt, int nt, int& rt, int& ct) {
@@ -183,7 +220,6 @@ template <int BM_, int BN_, int WR_, int WC_, int U_, int UNIT_ = (BM_ > BN_ ? B
 struct Geo {
   static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, U = U_, UNIT = UNIT_;   // UNIT: bytes
   static constexpr int NW = WR * WC, NT = 64 * NW, WM = BM / WR, WN = BN / WC, MS = WM / 16, NS = WN / 16;
-  static constexpr int LP = BM * 8 / NT, LQ = BN * 8 / NT;      // 16-byte loads per thread and unit
   // Each wave stages 32 output rows at a time in a strip of its own.
   static constexpr int SP = WN + 4, STRIP = 32 * SP * 4;
 };
@@ -193,11 +229,15 @@ constexpr int KB = 128, NQ = 2;   // a stage's k: bytes, and steps of 32 (bf16) 
 // slot c ^ swz(r), so that the 16 rows of a fragment read's phase fall on
 // distinct banks.
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
-// k-major operand, rows of B values: bf16, chunk c of k-row r in slot
-// c ^ (4 (r & 3)) (the four k-rows of a transposing read on distinct banks);
-// float32, c ^ (4 ((r >> 2) & 3)) (the k-rows of a wave's four quarters).
-template <bool F32>
-__device__ __forceinline__ int kswz(int row) { return F32 ? 4 * ((row >> 2) & 3) : 4 * (row & 3); }
+// k-major operand, k-rows of B values: 16-byte chunk c of k-row r sits in slot
+// c ^ kswz(r).  bf16: the four k-rows of a transposing read (32 bytes of each)
+// on distinct banks; float32: the k-rows of a wave's four quarters.
+template <bool F32, int B>
+__device__ __forceinline__ int kswz(int row) {
+  static_assert(B % 128 == 0 || B == 64, "k-rows of whole 64-bank lines, or half of one");
+  if constexpr (F32) return 4 * ((row >> 2) & 3);
+  return (B == 64 ? 2 : 4) * (row & 3);
+}
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -205,88 +245,84 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 // One operand of a tile: B rows (or columns, k-major) of which `valid` exist.
-template <bool F32, bool KM, int B, int NT>
+// AL: bytes of a load.  16: rows on 16-byte borders; 4: on 4-byte borders
+// (every float32 matrix); 2: element by element through registers.
+template <bool F32, bool KM, int B, int NT, int AL>
 struct Operand {
-  static constexpr int ES = F32 ? 4 : 2, LBK = KB / ES, CR = KB / 16, L = B * CR / NT, CPR = B * ES / 16;
-  static_assert(L * NT == B * CR && NT / CR % 16 == 0, "whole loads; a thread's rows have one swizzle");
+  static constexpr int ES = F32 ? 4 : 2, LBK = KB / ES;
+  static constexpr int LINE = KM ? B * ES : KB;            // bytes of an LDS row
+  static constexpr int W = AL == 2 ? 16 : AL;              // bytes a thread stages at a time
+  static constexpr int L = B * KB / W / NT, PER = LINE / W;   // pieces per thread and unit, and per row
+  static_assert(L * NT * W == B * KB && (W != 16 || NT / 8 % 16 == 0), "whole pieces; one swizzle for a thread's rows");
   const char* base;
   uint32_t ld;         // bytes
   int valid, k;
-  uint32_t off[L];     // of this thread's chunks within a stage
+  uint32_t off[L];     // of this thread's pieces within a stage
+
+  // LDS row and byte within the operand's row of piece q.
+  static __device__ __forceinline__ void piece(int q, int& row, int& byte) {
+    const int i = q * NT + threadIdx.x;
+    row = i / PER;
+    const int at = i % PER * W, c = (at >> 4) ^ (KM ? kswz<F32, B>(row) : swz(row));
+    byte = c * 16 + (at & 15);
+  }
 
   __device__ __forceinline__ Operand(const void* p, int64_t ld_elems, int valid_, int k_)
       : base(static_cast<const char*>(p)), ld(static_cast<uint32_t>(ld_elems * ES)), valid(valid_), k(k_) {
 #pragma unroll
     for (int q = 0; q < L; ++q) {
-      const int i = q * NT + threadIdx.x;
-      if constexpr (KM) {
-        const int r = i / CPR, c = (i % CPR) ^ kswz<F32>(r);
-        off[q] = c * 16 < valid * ES ? r * ld + c * 16 : kNowhere;
-      } else {
-        const int r = i / CR, c = (i % CR) ^ swz(r);
-        off[q] = r * ld + c * 16;
-      }
+      int r, b;
+      piece(q, r, b);
+      off[q] = !KM || b < valid * ES ? r * ld + b : kNowhere;
     }
   }
 
-  // Loads of stage st into `buf` (this operand's part of a ring buffer).
+  // Loads of stage st into `buf`.
   __device__ __forceinline__ void issue(int st, char* buf) const {
     const int left = k - st * LBK, here = left < LBK ? left : LBK;
     const char* p = base + (KM ? static_cast<uint64_t>(st) * LBK * ld : static_cast<uint64_t>(st) * KB);
-    // (Behind the last slot nothing is read: the descriptor is empty.)
+    // (Behind the last stage nothing is read: the descriptor is empty.)
     const uint32_t end = here <= 0 ? 0 : KM ? (here - 1) * ld + valid * ES : (valid - 1) * ld + here * ES;
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, end, 0x00020000);
     const int wave = threadIdx.x >> 6;
-    // The ragged end of k: chunks behind it would read the next row.
-    const bool cut = !KM && here < LBK;
-    const int c = (threadIdx.x % CR) ^ swz(threadIdx.x / CR);   // the same chunk in each of the thread's rows
-    const bool out = cut && c * 16 >= here * ES;
-#pragma unroll
-    for (int q = 0; q < L; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (MUON_LDS void*)(buf + (q * NT + wave * 64) * 16), 16,
-                                               out ? kNowhere : off[q], 0, 0, 0);
-  }
-
-  // Operands whose rows do not lie on 16-byte borders, or whose sizes are not
-  // whole chunks: element by element, through registers.
-  __device__ __forceinline__ void fetch(int st, u32x4_t (&r)[L]) const {
-    const int k0 = st * LBK;
 #pragma unroll
     for (int q = 0; q < L; ++q) {
-      const int i = q * NT + threadIdx.x;
-      int row, col, rows, cols;   // of the chunk's first element, and the operand's end
-      if constexpr (KM) {
-        row = i / CPR;
-        col = ((i % CPR) ^ kswz<F32>(row)) * (16 / ES);
-        rows = k - k0;
-        cols = valid;
-      } else {
-        row = i / CR;
-        col = ((i % CR) ^ swz(row)) * (16 / ES);
-        rows = valid;
-        cols = k - k0;
+      uint32_t o = off[q];
+      // The ragged end of k: what lies behind it is the next row.
+      if (!KM) {
+        int r, b;
+        piece(W == 16 ? 0 : q, r, b);   // (16-byte pieces: the same chunk in all of the thread's rows)
+        o = b < here * ES ? o : kNowhere;
       }
-      const char* p = base + (KM ? static_cast<uint64_t>(k0) * ld : static_cast<uint64_t>(k0) * ES) +
-                      static_cast<uint64_t>(row) * ld + static_cast<uint64_t>(col) * ES;
-      uint32_t v[16 / ES];
-#pragma unroll
-      for (int e = 0; e < 16 / ES; ++e) {
-        v[e] = 0;
-        if (row < rows && col + e < cols) {
-          if constexpr (F32) v[e] = gmem(reinterpret_cast<const uint32_t*>(p))[e];
-          else v[e] = gmem(reinterpret_cast<const uint16_t*>(p))[e];
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if constexpr (F32) r[q][w] = v[w];
-        else r[q][w] = v[2 * w] | (v[2 * w + 1] << 16);
-      }
+      MUON_LDS void* to = (MUON_LDS void*)(buf + (q * NT + wave * 64) * W);
+      if constexpr (W == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 16, o, 0, 0, 0);
+      else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 4, o, 0, 0, 0);
     }
   }
-  __device__ __forceinline__ void put(const u32x4_t (&r)[L], char* buf) const {
+
+  // AL = 2: through registers.
+  __device__ __forceinline__ void fetch(int st, u32x4_t (&f)[L]) const {
+    const int left = k - st * LBK;
+    const char* p = base + (KM ? static_cast<uint64_t>(st) * LBK * ld : static_cast<uint64_t>(st) * KB);
 #pragma unroll
-    for (int q = 0; q < L; ++q) *reinterpret_cast<u32x4_t*>(buf + (q * NT + threadIdx.x) * 16) = r[q];
+    for (int q = 0; q < L; ++q) {
+      int r, b;
+      piece(q, r, b);
+      const int rows = KM ? left : valid, bytes = (KM ? valid : left) * ES;
+      uint32_t v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = 0;
+        if (r < rows && b + 2 * e < bytes)
+          v[e] = gmem(reinterpret_cast<const uint16_t*>(p + static_cast<uint64_t>(r) * ld + b))[e];
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) f[q][w] = v[2 * w] | (v[2 * w + 1] << 16);
+    }
+  }
+  __device__ __forceinline__ void put(const u32x4_t (&f)[L], char* buf) const {
+#pragma unroll
+    for (int q = 0; q < L; ++q) *reinterpret_cast<u32x4_t*>(buf + (q * NT + threadIdx.x) * 16) = f[q];
   }
 };
 
@@ -307,13 +343,13 @@ __device__ __forceinline__ void read_frags(const char* buf, int row0, int q, u32
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = 16 * q + 4 * g16 + e, col = row0 + t * 16 + m16;
-        f[t][e] = *reinterpret_cast<const uint32_t*>(buf + r * B * 4 + ((((col >> 2) ^ kswz<true>(r)) << 2) + (col & 3)) * 4);
+        f[t][e] = *reinterpret_cast<const uint32_t*>(buf + r * B * 4 + ((((col >> 2) ^ kswz<true, B>(r)) << 2) + (col & 3)) * 4);
       }
   } else {
     // Two transposing reads a block: in each group of 16 lanes, lane m
     // receives column m's values of four k-rows, of which lane i reads the
     // four columns 4 (i mod 4) of k-row i / 4.
-    const int r = 32 * q + 8 * g16 + (m16 >> 2), sw = 4 * (m16 >> 2);
+    const int r = 32 * q + 8 * g16 + (m16 >> 2), sw = kswz<false, B>(r);
 #pragma unroll
     for (int t = 0; t < N; ++t) {
       const int col = row0 + t * 16 + 4 * (m16 & 3);
@@ -375,9 +411,9 @@ __device__ __forceinline__ void pace() {
 }
 
 // acc += P Q over k.
-template <bool F32, bool PKM, bool QKM, typename G, bool VEC>
-__device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT>& P,
-                                        const Operand<F32, QKM, G::BN, G::NT>& Q, int k, char* const (&ring)[G::U],
+template <bool F32, bool PKM, bool QKM, typename G, int AL>
+__device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT, AL>& P,
+                                        const Operand<F32, QKM, G::BN, G::NT, AL>& Q, int k, char* const (&ring)[G::U],
                                         int row_p, int row_q, f32x4_t (&acc)[G::MS][G::NS]) {
   constexpr int LBK = KB / (F32 ? 4 : 2), U = G::U;
   const int nk = (k + LBK - 1) / LBK;
@@ -388,8 +424,9 @@ __device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT>& P
     read_frags<F32, QKM, G::BN, G::NS>(bq, row_q, q, fq[q & 1]);
   };
   auto mul = [&](int q) { multiply<F32, G::MS, G::NS>(fp[q & 1], fq[q & 1], acc); };
-  if constexpr (!VEC) {
-    u32x4_t rp[G::LP], rq[G::LQ];
+  constexpr int LP = G::BM * KB / (AL == 2 ? 16 : AL) / G::NT, LQ = G::BN * KB / (AL == 2 ? 16 : AL) / G::NT;
+  if constexpr (AL == 2) {
+    u32x4_t rp[LP], rq[LQ];
     P.fetch(0, rp);
     Q.fetch(0, rq);
     for (int st = 0; st < nk; ++st) {
@@ -412,7 +449,7 @@ __device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT>& P
     // Loads of this wave in units first .. U-1 of the order P Q P Q ...
     constexpr auto loads_from = [](int first) {
       int n = 0;
-      for (int u = first; u < U; ++u) n += u % 2 ? G::LQ : G::LP;
+      for (int u = first; u < U; ++u) n += u % 2 ? LQ : LP;
       return n;
     };
     auto issue = [&](int st, int operand, char* buf) {
@@ -455,11 +492,11 @@ __device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT>& P
       read(n0, n1, 0);
       issue(st + U / 2, ODD, c0);
       mul(NQ - 1);
-      pace<F32, PKM, QKM, G, ODD ? G::LQ : G::LP>();
+      pace<F32, PKM, QKM, G, ODD ? LQ : LP>();
       read(n0, n1, 1);
       issue(st + U / 2 + ODD, !ODD, c1);
       mul(0);
-      pace<F32, PKM, QKM, G, ODD ? G::LP : G::LQ>();
+      pace<F32, PKM, QKM, G, ODD ? LP : LQ>();
 #pragma unroll
       for (int q = 2; q < NQ; ++q) {
         read(n0, n1, q);
@@ -482,23 +519,20 @@ __device__ __forceinline__ void product(const Operand<F32, PKM, G::BM, G::NT>& P
   }
 }
 
-// Eight values at p (16-byte aligned).
-template <bool F32>
-__device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
-  const MUON_GLOBAL u32x4_t* q = reinterpret_cast<const MUON_GLOBAL u32x4_t*>(gmem(static_cast<const char*>(p)));
-  if constexpr (F32) {
-    const u32x4_t a = q[0], b = q[1];
+// Eight values of one (bf16) or two 16-byte loads.
+template <int W>
+__device__ __forceinline__ void unpack8(const u32x4_t (&u)[W], bool f32, float (&v)[8]) {
+  if (W == 2 && f32) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[e] = __uint_as_float(a[e]);
-      v[4 + e] = __uint_as_float(b[e]);
+      v[e] = __uint_as_float(u[0][e]);
+      v[4 + e] = __uint_as_float(u[W - 1][e]);
     }
   } else {
-    const u32x4_t a = q[0];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(a[e] << 16);
-      v[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
+      v[2 * e] = __uint_as_float(u[0][e] << 16);
+      v[2 * e + 1] = __uint_as_float(u[0][e] & 0xffff0000u);
     }
   }
 }
@@ -521,69 +555,72 @@ __device__ __forceinline__ void store8(void* p, const float (&v)[8], bool f32) {
   }
 }
 
-// Run of eight values (VEC), or as many as exist.
-template <bool VEC>
-__device__ __forceinline__ void load_run(const void* p, int64_t at, int n, bool f32, float (&v)[8]) {
-  if constexpr (VEC) {
-    const char* q = static_cast<const char*>(p) + at * (f32 ? 4 : 2);
-    if (f32) load8<true>(q, v);
-    else load8<false>(q, v);
+// A run of N values from element `at` on: eight on 16-byte borders, or one.
+template <int N>
+__device__ __forceinline__ void load_run(const void* p, int64_t at, bool f32, float (&v)[N]) {
+  if constexpr (N == 8) {
+    const MUON_GLOBAL u32x4_t* q =
+        reinterpret_cast<const MUON_GLOBAL u32x4_t*>(gmem(static_cast<const char*>(p) + at * (f32 ? 4 : 2)));
+    u32x4_t u[2] = {q[0], q[0]};
+    if (f32) u[1] = q[1];
+    unpack8(u, f32, v);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? load_elem(p, at + e, f32 ? DT_F32 : DT_BF16) : 0.0f;
+    v[0] = load_elem(p, at, f32 ? DT_F32 : DT_BF16);
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void store_run(void* p, int64_t at, int n, bool f32, const float (&v)[8]) {
-  if constexpr (VEC) {
-    store8(static_cast<char*>(p) + at * (f32 ? 4 : 2), v, f32);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) store_elem(p, at + e, f32 ? DT_F32 : DT_BF16, v[e]);
-  }
+template <int N>
+__device__ __forceinline__ void store_run(void* p, int64_t at, bool f32, const float (&v)[N]) {
+  if constexpr (N == 8) store8(static_cast<char*>(p) + at * (f32 ? 4 : 2), v, f32);
+  else store_elem(p, at, f32 ? DT_F32 : DT_BF16, v[0]);
 }
 
-// What becomes of eight sums of row m (of the operands' rows; of the weight
+// What a product's result is combined with, element by element: the residual
+// (forward), x_pre (input gradient), what dW holds (weight gradient,
+// accumulated).
+template <bool F32, int MODE>
+struct Old {
+  const void* p;   // NULL: none
+  int64_t ld, at;
+  bool f32;
+  __device__ __forceinline__ Old(const LinArgs& a, int g) {
+    if constexpr (MODE == LIN_WEIGHT) {
+      p = a.accumulate && a.parts == 1 ? a.c : nullptr;
+      ld = a.ldc;
+      at = g * a.gc;
+      f32 = a.c_dt == DT_F32;
+    } else {
+      p = a.aux;
+      ld = a.ldaux;
+      at = 0;
+      f32 = F32;
+    }
+  }
+};
+
+// What becomes of N sums of row m (of the operands' rows; of the weight
 // gradient: an output feature) from column n on, in group g.
-template <bool F32, int MODE, bool VEC>
-__device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_t m, int n, float (&v)[8]) {
-  const int left = a.n - n;
+template <bool F32, int MODE, int N>
+__device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_t m, int n, float (&v)[N],
+                                       const float (&bias)[N], bool has_old, const float (&old)[N]) {
+  auto add = [&](const float (&b)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] += b[e];
+  };
   if constexpr (MODE == LIN_FORWARD) {
-    if (a.bias) {
-      float b[8];
-      load_run<VEC>(a.bias, static_cast<int64_t>(g) * a.n + n, left, F32, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += b[e];
-    }
-    if (a.pre) store_run<VEC>(a.pre, m * a.ldpre + n, left, F32, v);
-    activate8<F32>(a.act, v);
-    if (a.aux) {
-      float r[8];
-      load_run<VEC>(a.aux, m * a.ldaux + n, left, F32, r);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += r[e];
-    }
-    store_run<VEC>(a.c, m * a.ldc + n, left, F32, v);
+    if (a.bias) add(bias);
+    if (a.pre) store_run(a.pre, m * a.ldpre + n, F32, v);
+    activate_run<F32>(a.act, v);
+    if (has_old) add(old);
+    store_run(a.c, m * a.ldc + n, F32, v);
   } else if constexpr (MODE == LIN_INPUT) {
-    if (a.aux) {
-      float z[8];
-      load_run<VEC>(a.aux, m * a.ldaux + n, left, F32, z);
-      times_slope8<F32>(a.act, z, v);
-    }
-    store_run<VEC>(a.c, m * a.ldc + n, left, F32, v);
+    if (has_old) times_slope<F32>(a.act, old, v);
+    store_run(a.c, m * a.ldc + n, F32, v);
   } else if (a.parts > 1) {
     const int64_t at = (static_cast<int64_t>(part) * a.groups + g) * a.m + m;
-    store_run<VEC>(a.part, at * a.n + n, left, true, v);
+    store_run(a.part, at * a.n + n, true, v);
   } else {
-    const int64_t at = g * a.gc + m * a.ldc + n;
-    if (a.accumulate) {
-      float o[8];
-      load_run<VEC>(a.c, at, left, a.c_dt == DT_F32, o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += o[e];
-    }
-    store_run<VEC>(a.c, at, left, a.c_dt == DT_F32, v);
+    if (has_old) add(old);
+    store_run(a.c, g * a.gc + m * a.ldc + n, a.c_dt == DT_F32, v);
   }
 }
 
@@ -596,7 +633,7 @@ struct Tile {
 };
 
 // One tile of at most G::BM x G::BN.
-template <bool F32, int MODE, typename G, bool VEC>
+template <bool F32, int MODE, typename G, int AL>
 __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* const (&ring)[G::U]) {
   constexpr bool PKM = MODE == LIN_WEIGHT, QKM = MODE != LIN_FORWARD;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -606,9 +643,9 @@ __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* cons
   for (int s = 0; s < G::MS; ++s)
 #pragma unroll
     for (int t = 0; t < G::NS; ++t) acc[s][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const Operand<F32, PKM, G::BM, G::NT> P(w.p, a.ldp, w.m_valid, w.k);
-  const Operand<F32, QKM, G::BN, G::NT> Q(w.q, a.ldq, w.n_valid, w.k);
-  product<F32, PKM, QKM, G, VEC>(P, Q, w.k, ring, row_p, row_q, acc);
+  const Operand<F32, PKM, G::BM, G::NT, AL> P(w.p, a.ldp, w.m_valid, w.k);
+  const Operand<F32, QKM, G::BN, G::NT, AL> Q(w.q, a.ldq, w.n_valid, w.k);
+  product<F32, PKM, QKM, G, AL>(P, Q, w.k, ring, row_p, row_q, acc);
 
   // Through the wave's strip: a lane puts four columns of one row at a time
   // and takes eight, so that global accesses are whole 16-byte runs.
@@ -620,11 +657,39 @@ __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* cons
   for (int b = 0; b < G::U; ++b)
     base = wave / PER == b ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MUON_LDS char*)ring[b])) : base;
   MUON_LDS float* strip = (MUON_LDS float*)(static_cast<uintptr_t>(base + (wave % PER) * G::STRIP));
+  const Old<F32, MODE> old(a, w.group);
+  constexpr int PASSES = 32 * CPR / 64;
+  const int c8 = lane % CPR * 8, r8 = lane / CPR, n8 = w.n0 + row_q + c8;   // a lane's column run is the same in all passes
+  float bias[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int OW = F32 || MODE == LIN_WEIGHT ? 2 : 1;   // loads of eight old values
+  u32x4_t now[PASSES][OW], next[PASSES][OW];
+  // What a strip's results are combined with is read a strip ahead (the
+  // compiler cannot move these reads before the stores, which may be to the
+  // same array).
+  auto fetch = [&](int s, u32x4_t (&o)[PASSES][OW]) {
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = row_p + s * 32 + r8 + i * (64 / CPR);
+      if (r < w.m_valid && n8 < a.n) {
+        const MUON_GLOBAL u32x4_t* p = reinterpret_cast<const MUON_GLOBAL u32x4_t*>(
+            gmem(static_cast<const char*>(old.p) + (old.at + (w.row0 + r) * old.ld + n8) * (old.f32 ? 4 : 2)));
+        o[i][0] = p[0];
+        if constexpr (OW == 2) {
+          if (old.f32) o[i][1] = p[1];
+        }
+      }
+    }
+  };
+  if constexpr (AL == 16) {
+    if (MODE == LIN_FORWARD && a.bias && n8 < a.n) load_run(a.bias, static_cast<int64_t>(w.group) * a.n + n8, F32, bias);
+    if (old.p) fetch(0, now);
+  }
   // (One copy of what follows the sums, for all blocks of rows.)
 #pragma unroll 1
   for (int s = 0; s < G::MS / 2; ++s) {
     const int ms = row_p + s * 32;
     if (ms >= w.m_valid) break;
+    if (AL == 16 && old.p && s + 1 < G::MS / 2) fetch(s + 1, next);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -636,26 +701,47 @@ __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* cons
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-    for (int i = lane; i < 32 * CPR; i += 64) {
-      const int r = i / CPR, c = (i % CPR) * 8;
-      const int n = w.n0 + row_q + c;
-      if (ms + r >= w.m_valid || n >= a.n) continue;
-      float v[8];
-      const f32x4_t lo = *(const MUON_LDS f32x4_t*)(strip + r * G::SP + c);
-      const f32x4_t hi = *(const MUON_LDS f32x4_t*)(strip + r * G::SP + c + 4);
+    if constexpr (AL == 16) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = lo[e];
-        v[4 + e] = hi[e];
+      for (int i = 0; i < PASSES; ++i) {
+        const int r = r8 + i * (64 / CPR);
+        if (ms + r >= w.m_valid || n8 >= a.n) continue;
+        float v[8], o[8];
+        const f32x4_t lo = *(const MUON_LDS f32x4_t*)(strip + r * G::SP + c8);
+        const f32x4_t hi = *(const MUON_LDS f32x4_t*)(strip + r * G::SP + c8 + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = lo[e];
+          v[4 + e] = hi[e];
+        }
+        if (old.p) unpack8(now[i], old.f32, o);
+        finish<F32, MODE, 8>(a, w.group, w.part, w.row0 + ms + r, n8, v, bias, old.p != nullptr, o);
       }
-      finish<F32, MODE, VEC>(a, w.group, w.part, w.row0 + ms + r, n, v);
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+#pragma unroll
+        for (int h = 0; h < OW; ++h) now[i][h] = next[i][h];
+      }
+    } else {
+      // Rows on no 16-byte borders: a lane per column.
+#pragma unroll 4
+      for (int i = lane; i < 32 * G::WN; i += 64) {
+        const int r = i / G::WN, c = i % G::WN;
+        const int n = w.n0 + row_q + c;
+        if (ms + r >= w.m_valid || n >= a.n) continue;
+        float v[1] = {strip[r * G::SP + c]}, b1[1] = {0.0f}, o1[1] = {0.0f};
+        const int64_t m = w.row0 + ms + r;
+        if (MODE == LIN_FORWARD && a.bias) load_run(a.bias, static_cast<int64_t>(w.group) * a.n + n, F32, b1);
+        if (old.p) load_run(old.p, old.at + m * old.ld + n, old.f32, o1);
+        finish<F32, MODE, 1>(a, w.group, w.part, m, n, v, b1, old.p != nullptr, o1);
+      }
     }
   }
 }
 
-template <bool F32, int MODE, typename G, bool VEC>
-__global__ __launch_bounds__(G::NT, 1) void k_linear(LinArgs a, int run) {
+// (Medium tiles run two workgroups on a CU.)
+template <bool F32, int MODE, typename G, int AL>
+__global__ __launch_bounds__(G::NT, G::UNIT * G::U <= 81920 ? 2 : 1) void k_linear(LinArgs a, int run) {
   constexpr int ES = F32 ? 4 : 2, LBK = KB / ES;
   // (Arrays of their own, so that the compiler can tell a read of one unit
   // from a load into another.)
@@ -664,7 +750,10 @@ __global__ __launch_bounds__(G::NT, 1) void k_linear(LinArgs a, int run) {
   __shared__ __attribute__((aligned(16))) char unit2[G::U > 2 ? G::UNIT : 16];
   __shared__ __attribute__((aligned(16))) char unit3[G::U > 3 ? G::UNIT : 16];
   __shared__ __attribute__((aligned(16))) char unit4[G::U > 4 ? G::UNIT : 16];
-  const int idx = tile_of(blockIdx.x, run), nt = (a.n + G::BN - 1) / G::BN;
+  __shared__ __attribute__((aligned(16))) char unit5[G::U > 5 ? G::UNIT : 16];
+  __shared__ __attribute__((aligned(16))) char unit6[G::U > 6 ? G::UNIT : 16];
+  __shared__ __attribute__((aligned(16))) char unit7[G::U > 7 ? G::UNIT : 16];
+  const int idx = tile_of(blockIdx.x, run, MODE == LIN_WEIGHT), nt = (a.n + G::BN - 1) / G::BN;
   Group g;
   Tile w;
   int rt, ct;
@@ -674,7 +763,10 @@ __global__ __launch_bounds__(G::NT, 1) void k_linear(LinArgs a, int run) {
     if (idx >= mt * nt * a.groups * a.parts) return;
     const int gi = idx / (mt * nt);
     w.part = gi / a.groups;
+    // Groups with many rows first: a tile's time is its rows, and a long one
+    // begun last would run alone.
     g.index = gi % a.groups;
+    if (a.offsets && a.groups > 1 && a.groups <= kRanked) g.index = group_by_size(a, g.index);
     g.lo = a.offsets ? clamped(gmem(a.offsets)[g.index], 0, a.rows) : 0;
     g.hi = a.offsets ? clamped(gmem(a.offsets)[g.index + 1], g.lo, a.rows) : a.rows;
     block_order(idx % (mt * nt), mt, nt, rt, ct);
@@ -701,27 +793,101 @@ __global__ __launch_bounds__(G::NT, 1) void k_linear(LinArgs a, int run) {
   w.group = g.index;
   w.n0 = ct * G::BN;
   w.n_valid = min(G::BN, a.n - w.n0);
-  if constexpr (G::U == 5) {
+  if constexpr (G::U == 8) {
+    char* const ring[8] = {unit0, unit1, unit2, unit3, unit4, unit5, unit6, unit7};
+    tile<F32, MODE, G, AL>(a, w, ring);
+  } else if constexpr (G::U == 5) {
     char* const ring[5] = {unit0, unit1, unit2, unit3, unit4};
     // A tile that is less than half full in one direction takes half the time.
     if constexpr (G::BM == 256 && G::BN == 256) {
       if (w.n_valid <= 128) {
-        tile<F32, MODE, Geo<256, 128, 4, 1, 5, G::UNIT>, VEC>(a, w, ring);
+        tile<F32, MODE, Geo<256, 128, 4, 1, 5, G::UNIT>, AL>(a, w, ring);
         return;
       }
       if (w.m_valid <= 128) {
-        tile<F32, MODE, Geo<128, 256, 1, 4, 5, G::UNIT>, VEC>(a, w, ring);
+        tile<F32, MODE, Geo<128, 256, 1, 4, 5, G::UNIT>, AL>(a, w, ring);
         return;
       }
     }
-    tile<F32, MODE, G, VEC>(a, w, ring);
+    tile<F32, MODE, G, AL>(a, w, ring);
   } else if constexpr (G::U == 4) {
     char* const ring[4] = {unit0, unit1, unit2, unit3};
-    tile<F32, MODE, G, VEC>(a, w, ring);
+    tile<F32, MODE, G, AL>(a, w, ring);
   } else {
     char* const ring[2] = {unit0, unit1};
-    tile<F32, MODE, G, VEC>(a, w, ring);
+    tile<F32, MODE, G, AL>(a, w, ring);
   }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (serving): the weights are read once and everything else is small.
+// A workgroup takes 16 columns of a group's 16 rows; its two waves take the
+// 128-byte blocks of k in turn, straight from global memory into MFMA
+// fragments (no element is used twice), and add their sums up in LDS.
+// ---------------------------------------------------------------------------
+constexpr int kThinRows = 16, kThinCols = 16, kThinWaves = 2;
+
+template <bool F32>
+__global__ __launch_bounds__(64 * kThinWaves) void k_linear_thin(LinArgs a) {
+  constexpr int ES = F32 ? 4 : 2, STEPS = 2, AHEAD = 4;   // k-steps (64 bytes) of a block; blocks in flight
+  __shared__ __attribute__((aligned(16))) float sums[kThinWaves][kThinRows][kThinCols + 4];
+  const int nt = (a.n + kThinCols - 1) / kThinCols;
+  Group g;
+  int local;
+  if (!find_rows(a, blockIdx.x, kThinRows, nt, g, local)) return;
+  const int mt = (g.hi - g.lo + kThinRows - 1) / kThinRows, rt = local % mt, n0 = local / mt * kThinCols;
+  const int row0 = g.lo + rt * kThinRows, m_valid = min(kThinRows, g.hi - row0), n_valid = min(kThinCols, a.n - n0);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15;
+  const uint32_t bytes = static_cast<uint32_t>(a.k) * ES, blocks = (bytes + 127) / 128;
+  const uint32_t ldp = static_cast<uint32_t>(a.ldp) * ES, ldq = static_cast<uint32_t>(a.ldq) * ES;
+  char* const p = const_cast<char*>(static_cast<const char*>(a.p)) + static_cast<int64_t>(row0) * a.ldp * ES;
+  char* const q = const_cast<char*>(static_cast<const char*>(a.q)) + (g.index * a.gq + n0 * a.ldq) * ES;
+  const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(p, 0, (m_valid - 1) * ldp + bytes, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(q, 0, (n_valid - 1) * ldq + bytes, 0x00020000);
+  u32x4_t fp[2][AHEAD][STEPS], fq[2][AHEAD][STEPS];
+  auto load = [&](uint32_t b0, u32x4_t (&vp)[AHEAD][STEPS], u32x4_t (&vq)[AHEAD][STEPS]) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const uint32_t k = (b0 + i * kThinWaves) * 128 + s * 64 + (lane >> 4) * 16;
+        vq[i][s] = __builtin_amdgcn_raw_buffer_load_b128(rq, k < bytes ? l16 * ldq + k : kNowhere, 0, 0);
+        vp[i][s] = __builtin_amdgcn_raw_buffer_load_b128(rp, k < bytes ? l16 * ldp + k : kNowhere, 0, 0);
+      }
+  };
+  f32x4_t acc[1][1] = {{f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}}};
+  auto mul = [&](const u32x4_t (&vp)[AHEAD][STEPS], const u32x4_t (&vq)[AHEAD][STEPS]) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const u32x4_t one_p[1] = {vp[i][s]}, one_q[1] = {vq[i][s]};
+        multiply<F32, 1, 1>(one_p, one_q, acc);
+      }
+  };
+  constexpr uint32_t HOP = AHEAD * kThinWaves;
+  load(wave, fp[0], fq[0]);
+  for (uint32_t b = wave; b < blocks; b += 2 * HOP) {
+    load(b + HOP, fp[1], fq[1]);   // (behind the end: zeros, without a fetch)
+    mul(fp[0], fq[0]);
+    load(b + 2 * HOP, fp[0], fq[0]);
+    mul(fp[1], fq[1]);
+  }
+  *reinterpret_cast<f32x4_t*>(&sums[wave][l16][4 * (lane >> 4)]) = acc[0][0];
+  __syncthreads();
+  const int r = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
+  if (r >= m_valid || n0 + c >= a.n) return;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = sums[0][r][c + e];
+#pragma unroll
+    for (int w = 1; w < kThinWaves; ++w) v[e] += sums[w][r][c + e];
+  }
+  float bias[8], old[8];
+  if (a.bias) load_run(a.bias, static_cast<int64_t>(g.index) * a.n + n0 + c, F32, bias);
+  if (a.aux) load_run(a.aux, static_cast<int64_t>(row0 + r) * a.ldaux + n0 + c, F32, old);
+  finish<F32, LIN_FORWARD, 8>(a, g.index, 0, row0 + r, n0 + c, v, bias, a.aux != nullptr, old);
 }
 
 // ---------------------------------------------------------------------------
@@ -734,32 +900,36 @@ __device__ __forceinline__ int rows_used(const int32_t* offsets, int groups, int
   return offsets ? clamped(gmem(offsets)[groups], 0, rows) : rows;
 }
 
-template <bool F32, bool VEC>
+// N: values of a thread (eight on 16-byte borders, or one).
+template <bool F32, int N>
 __global__ __launch_bounds__(kPassThreads) void k_linear_slope(const void* dy, int64_t ld_dy, const void* pre,
                                                               int64_t ld_pre, void* dz, int64_t ld_dz,
                                                               const int32_t* offsets, int groups, int rows, int out,
                                                               int act) {
-  const int runs = (out + 7) / 8;
+  const int runs = out / N;
   const int64_t n = static_cast<int64_t>(rows_used(offsets, groups, rows)) * runs;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPassThreads + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * kPassThreads) {
     const int64_t r = i / runs;
-    const int c = static_cast<int>(i % runs) * 8;
-    float g[8], z[8];
-    load_run<VEC>(dy, r * ld_dy + c, out - c, F32, g);
-    load_run<VEC>(pre, r * ld_pre + c, out - c, F32, z);
-    times_slope8<F32>(act, z, g);
-    store_run<VEC>(dz, r * ld_dz + c, out - c, F32, g);
+    const int c = static_cast<int>(i % runs) * N;
+    float g[N], z[N];
+    load_run(dy, r * ld_dy + c, F32, g);
+    load_run(pre, r * ld_pre + c, F32, z);
+    times_slope<F32>(act, z, g);
+    store_run(dz, r * ld_dz + c, F32, g);
   }
 }
 
-// Column sums of a group's rows (or of one part of them): four waves take
-// every fourth row, 64 columns each, and are added in wave order.
+// Column sums of a group's rows (or of one part of them): sixteen waves take
+// every sixteenth row, 64 columns each, eight rows in flight, and are added in
+// wave order.
+constexpr int kBiasThreads = 1024;
 template <bool F32>
-__global__ __launch_bounds__(kPassThreads) void k_linear_bias(const void* dz, int64_t ld, const int32_t* offsets,
+__global__ __launch_bounds__(kBiasThreads) void k_linear_bias(const void* dz, int64_t ld, const int32_t* offsets,
                                                              int rows, int out, void* db, int grad_dt, int accumulate,
                                                              float* part, int parts) {
-  __shared__ float red[4][64];
+  constexpr int NW = kBiasThreads / 64, AHEAD = 8;
+  __shared__ float red[NW][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int blocks = (out + 63) / 64, g = blockIdx.x / blocks, c = (blockIdx.x % blocks) * 64 + lane;
   const int lo = offsets ? clamped(gmem(offsets)[g], 0, rows) : 0;
@@ -769,11 +939,21 @@ __global__ __launch_bounds__(kPassThreads) void k_linear_bias(const void* dz, in
   const int last = min(hi, first + per);
   float s = 0.0f;
   if (c < out)
-    for (int r = first + wave; r < last; r += 4) s += load_elem(dz, r * ld + c, F32 ? DT_F32 : DT_BF16);
+    for (int r0 = first + wave; r0 < last; r0 += NW * AHEAD) {
+      float v[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int r = r0 + i * NW;
+        v[i] = r < last ? load_elem(dz, r * ld + c, F32 ? DT_F32 : DT_BF16) : 0.0f;
+      }
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
   red[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < out) {
-    s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    s = red[0][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) s += red[w][lane];
     const int64_t at = static_cast<int64_t>(g) * out + c;
     if (parts > 1) {
       part[static_cast<int64_t>(blockIdx.y) * (gridDim.x / blocks) * out + at] = s;
@@ -803,6 +983,8 @@ using Large = Geo<256, 256, 2, 2, 5>;
 using Medium = Geo<128, 128, 2, 2, 5>;
 using Plain = Geo<128, 128, 2, 2, 2, 2 * Medium::STRIP>;   // operands through registers
 using Small = Geo<64, 128, 1, 4, 4>;
+using MediumDeep = Geo<128, 128, 2, 2, 8>;
+using SmallDeep = Geo<64, 128, 1, 4, 8>;
 
 int64_t ceil_of(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -817,27 +999,74 @@ int64_t tiles_at_most(const LinArgs& a, int mode) {
   return mt * nt;
 }
 
-template <bool F32, int MODE, typename G, bool VEC>
+template <bool F32, int MODE, typename G, int AL>
 hipError_t go(const LinArgs& a, bool dry, hipStream_t s) {
   const int64_t tiles = tiles_at_most<G>(a, MODE);
   const int64_t run = std::max<int64_t>(1, std::min<int64_t>(32, tiles / 16));
   const int64_t blocks = ceil_of(tiles, 8 * run) * 8 * run;
   if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   if (blocks == 0 || dry) return hipSuccess;
-  hipLaunchKernelGGL((k_linear<F32, MODE, G, VEC>), dim3(static_cast<uint32_t>(blocks)), dim3(G::NT), 0, s, a,
+  hipLaunchKernelGGL((k_linear<F32, MODE, G, AL>), dim3(static_cast<uint32_t>(blocks)), dim3(G::NT), 0, s, a,
                      static_cast<int>(run));
   return hipGetLastError();
 }
 
+template <bool F32>
+hipError_t go_thin(const LinArgs& a, bool dry, hipStream_t s) {
+  const int64_t mt = a.offsets ? std::min<int64_t>(a.rows, a.rows / kThinRows + a.groups) : ceil_of(a.rows, kThinRows);
+  const int64_t blocks = mt * ceil_of(a.n, kThinCols);
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
+  if (dry) return hipSuccess;
+  hipLaunchKernelGGL(k_linear_thin<F32>, dim3(static_cast<uint32_t>(blocks)), dim3(64 * kThinWaves), 0, s, a);
+  return hipGetLastError();
+}
+
+// Rounds that `tiles` take on the GPU (in halves): whole ones while they are few.
+int64_t half_rounds(int64_t tiles, int64_t at_once) {
+  return tiles <= 4 * at_once ? 2 * ceil_of(tiles, at_once) : 2 * tiles / at_once + 1;
+}
+// Tiles of a launch as expected: a group's last tile is half full on average.
+template <typename G>
+int64_t tiles_expected(const LinArgs& a, int mode) {
+  const int64_t nt = ceil_of(a.n, G::BN);
+  if (mode == LIN_WEIGHT || !a.offsets) return tiles_at_most<G>(a, mode);
+  return std::max<int64_t>(1, a.rows / G::BM + a.groups / 2) * nt;
+}
+
+// The kernel of a product.  `align`: 16 (rows of whole 16-byte runs on 16-byte
+// borders), 4 or 2.
 template <int MODE>
-hipError_t pick(const LinArgs& a, int dt, bool vec, bool dry, hipStream_t s) {
-  if (dt == DT_F32) return vec ? go<true, MODE, Medium, true>(a, dry, s) : go<true, MODE, Plain, false>(a, dry, s);
-  if (!vec) return go<false, MODE, Plain, false>(a, dry, s);
-  if constexpr (MODE != LIN_WEIGHT) {
-    if (a.rows / a.groups <= 96) return go<false, MODE, Small, true>(a, dry, s);
+hipError_t pick(const LinArgs& a, int dt, int align, bool dry, hipStream_t s) {
+  const int64_t small = tiles_expected<Small>(a, MODE), medium = tiles_expected<Medium>(a, MODE);
+  const int64_t mean = a.rows / a.groups;   // rows of a group
+  if constexpr (MODE == LIN_FORWARD) {
+    // Few rows: every 16 of a group's read its weight again (from the L2 or
+    // the Infinity Cache).  64 experts of 2048 x 1408: 66 us against 97 (Small)
+    // at three rows an expert, 85 against 100 at nine, 101 against 92 at twelve;
+    // 4096 x 4096, one group: 19 us against 23 (SmallDeep) at 32 rows, 32
+    // against 24 at 64.
+    if (align == 16 && (mean <= 10 || (mean <= 40 && small <= 256)))
+      return dt == DT_F32 ? go_thin<true>(a, dry, s) : go_thin<false>(a, dry, s);
   }
-  if (tiles_at_most<Large>(a, MODE) >= 256) return go<false, MODE, Large, true>(a, dry, s);
-  return go<false, MODE, Medium, true>(a, dry, s);
+  if (dt == DT_F32) {
+    // (A float32 product is slow enough that 64-row tiles lose nothing.)
+    if (align == 16) return medium <= 512 ? go<true, MODE, Small, 16>(a, dry, s) : go<true, MODE, Medium, 16>(a, dry, s);
+    return medium <= 512 ? go<true, MODE, Small, 4>(a, dry, s) : go<true, MODE, Medium, 4>(a, dry, s);
+  }
+  if (align == 4) return medium <= 512 ? go<false, MODE, Small, 4>(a, dry, s) : go<false, MODE, Medium, 4>(a, dry, s);
+  if (align != 16) return go<false, MODE, Plain, 2>(a, dry, s);
+  if constexpr (MODE != LIN_WEIGHT) {
+    // No more tiles than CUs: a ring over most of a CU's LDS (4096 x 4096: 23
+    // instead of 40 us at 32 to 96 rows).
+    if (small <= 256) return go<false, MODE, SmallDeep, 16>(a, dry, s);
+    if (mean <= 96) return go<false, MODE, Small, 16>(a, dry, s);
+  }
+  if (medium <= 256) return go<false, MODE, MediumDeep, 16>(a, dry, s);
+  // In units of time: a CU runs one Large tile, or two Medium ones at once,
+  // which take 1.2 times as long per element.
+  if (half_rounds(tiles_expected<Large>(a, MODE), 256) * 40 <= half_rounds(medium, 512) * 24)
+    return go<false, MODE, Large, 16>(a, dry, s);
+  return go<false, MODE, Medium, 16>(a, dry, s);
 }
 
 uint32_t pass_blocks(int64_t n) {
@@ -846,16 +1075,16 @@ uint32_t pass_blocks(int64_t n) {
 
 }  // namespace
 
-static hipError_t linear(const LinArgs& a, int mode, int dt, bool vec, bool dry, hipStream_t s) {
-  if (mode == LIN_FORWARD) return pick<LIN_FORWARD>(a, dt, vec, dry, s);
-  if (mode == LIN_INPUT) return pick<LIN_INPUT>(a, dt, vec, dry, s);
-  return pick<LIN_WEIGHT>(a, dt, vec, dry, s);
+static hipError_t linear(const LinArgs& a, int mode, int dt, int align, bool dry, hipStream_t s) {
+  if (mode == LIN_FORWARD) return pick<LIN_FORWARD>(a, dt, align, dry, s);
+  if (mode == LIN_INPUT) return pick<LIN_INPUT>(a, dt, align, dry, s);
+  return pick<LIN_WEIGHT>(a, dt, align, dry, s);
 }
-hipError_t launch_linear(const LinArgs& a, int mode, int dt, bool vec, hipStream_t s) {
-  return linear(a, mode, dt, vec, false, s);
+hipError_t launch_linear(const LinArgs& a, int mode, int dt, int align, hipStream_t s) {
+  return linear(a, mode, dt, align, false, s);
 }
-bool linear_fits(const LinArgs& a, int mode, int dt, bool vec) {
-  return linear(a, mode, dt, vec, true, nullptr) == hipSuccess;
+bool linear_fits(const LinArgs& a, int mode, int dt, int align) {
+  return linear(a, mode, dt, align, true, nullptr) == hipSuccess;
 }
 
 int linear_weight_parts(int64_t rows, int64_t out, int64_t in, int64_t groups) {
@@ -871,16 +1100,17 @@ hipError_t launch_linear_join(const LinArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_linear_slope(const void* dy, int64_t ld_dy, const void* pre, int64_t ld_pre, void* dz, int64_t ld_dz,
-                               const int32_t* offsets, int groups, int64_t rows, int64_t out, int act, int dt, bool vec,
+                               const int32_t* offsets, int groups, int64_t rows, int64_t out, int act, int dt, int align,
                                hipStream_t s) {
-  const dim3 grid(pass_blocks(rows * ceil_of(out, 8))), threads(kPassThreads);
-#define MUON_SLOPE(F32, VEC)                                                                                         \
-  hipLaunchKernelGGL((k_linear_slope<F32, VEC>), grid, threads, 0, s, dy, ld_dy, pre, ld_pre, dz, ld_dz, offsets,    \
+  const bool runs = align == 16;
+  const dim3 grid(pass_blocks(rows * (runs ? out / 8 : out))), threads(kPassThreads);
+#define MUON_SLOPE(F32, N)                                                                                           \
+  hipLaunchKernelGGL((k_linear_slope<F32, N>), grid, threads, 0, s, dy, ld_dy, pre, ld_pre, dz, ld_dz, offsets,      \
                      groups, (int)rows, (int)out, act)
   if (dt == DT_F32) {
-    if (vec) MUON_SLOPE(true, true); else MUON_SLOPE(true, false);
+    if (runs) MUON_SLOPE(true, 8); else MUON_SLOPE(true, 1);
   } else {
-    if (vec) MUON_SLOPE(false, true); else MUON_SLOPE(false, false);
+    if (runs) MUON_SLOPE(false, 8); else MUON_SLOPE(false, 1);
   }
 #undef MUON_SLOPE
   return hipGetLastError();
@@ -892,7 +1122,7 @@ int linear_bias_parts(int64_t rows, int64_t groups) {
 
 hipError_t launch_linear_bias(const void* dz, int64_t ld, const int32_t* offsets, int groups, int64_t rows, int64_t out,
                               void* db, int dt, int grad_dt, int accumulate, float* part, int parts, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>(ceil_of(out, 64) * groups), static_cast<uint32_t>(parts)), threads(kPassThreads);
+  const dim3 grid(static_cast<uint32_t>(ceil_of(out, 64) * groups), static_cast<uint32_t>(parts)), threads(kBiasThreads);
   if (dt == DT_F32)
     hipLaunchKernelGGL(k_linear_bias<true>, grid, threads, 0, s, dz, ld, offsets, (int)rows, (int)out, db, grad_dt,
                        accumulate, part, parts);
@@ -901,7 +1131,7 @@ hipError_t launch_linear_bias(const void* dz, int64_t ld, const int32_t* offsets
                        accumulate, part, parts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || parts == 1) return e;
-  hipLaunchKernelGGL(k_linear_join, dim3(pass_blocks(out * groups)), threads, 0, s, part, parts, groups, 1, (int)out, db,
+  hipLaunchKernelGGL(k_linear_join, dim3(pass_blocks(out * groups)), dim3(kPassThreads), 0, s, part, parts, groups, 1, (int)out, db,
                      out, out, grad_dt, accumulate);
   return hipGetLastError();
 }

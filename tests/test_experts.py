@@ -526,7 +526,9 @@ LINEAR = [
     (200, 264, 264, 1, "layer", 8), (300, 64, 512, 2, "random", 0), (129, 8, 129, 1, "layer", 0),
     (257, 200, 96, 5, "tail", 0), (400, 96, 320, 70, "random", 0), (64, 40, 24, 6, "empty", 0),
     (500, 77, 51, 3, "random", 0), (130, 129, 255, 1, "layer", 1), (260, 65, 9, 4, "tail", 3),
-    (1100, 520, 136, 3, "random", 0), (2100, 72, 1032, 2, "tail", 0),
+    (1100, 520, 136, 3, "random", 0), (2100, 72, 1032, 2, "tail", 0), (333, 98, 150, 3, "random", 2),
+    (150, 6, 10, 2, "tail", 0), (700, 260, 12, 3, "random", 4), (20000, 34, 514, 90, "random", 0),
+    (40000, 40, 136, 12, "random", 0), (40000, 33, 130, 12, "tail", 1),
 ]
 
 
