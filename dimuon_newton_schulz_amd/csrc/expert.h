@@ -17,20 +17,19 @@ struct Routes {
 };
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortAlone = 8192;        // slots up to which one workgroup sorts alone
-constexpr int kSortMaxBlocks = 256;     // workgroups of a longer sort
+constexpr int kSortAlone = 8192;        // slots that one workgroup sorts, alone if they are all
+constexpr int kSortSummed = 256;        // workgroups up to which each adds up the others' counts itself
 constexpr int kMaxExperts = 1024;
 
-// Slots of a workgroup and number of workgroups of a sort.
+// Slots of a workgroup, number of workgroups and rows of counts of a sort.
 inline void sort_shape(int64_t slots, int64_t& per, int64_t& blocks) {
-  if (slots <= kSortAlone) {
-    per = slots;
-    blocks = 1;
-    return;
+  per = slots;
+  if (slots > kSortAlone) {
+    per = (slots + kSortSummed - 1) / kSortSummed;
+    per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
+    per = per < kSortAlone ? per : kSortAlone;
   }
-  per = (slots + kSortMaxBlocks - 1) / kSortMaxBlocks;
-  per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
-  blocks = (slots + per - 1) / per;
+  blocks = slots > kSortAlone ? (slots + per - 1) / per : 1;
 }
 
 // Rows between tokens and experts.  Strides in elements.

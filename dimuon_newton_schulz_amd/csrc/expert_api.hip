@@ -149,7 +149,7 @@ muon_status_t check_routes(const expert_routes_t* r, Buffers& b, bool written) {
 size_t sort_bytes(int64_t slots, int32_t experts) {
   int64_t per, blocks;
   sort_shape(slots, per, blocks);
-  return blocks > 1 ? static_cast<size_t>(round_up(blocks * (experts + 1) * 4, kAlign)) : 0;
+  return blocks > 1 ? static_cast<size_t>(round_up((blocks + 1) * (experts + 1) * 4, kAlign)) : 0;
 }
 
 muon_status_t check_width(int64_t width) {

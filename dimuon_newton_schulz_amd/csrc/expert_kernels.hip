@@ -4,6 +4,7 @@
 // rows lie in the order of their slots, so results repeat bit for bit and no
 // atomic decides a place.
 #include <algorithm>
+#include <type_traits>
 
 #include "expert.h"
 
@@ -34,93 +35,141 @@ __global__ __launch_bounds__(kSortThreads) void k_expert_count(const I* ids, int
     counts[static_cast<int64_t>(blockIdx.x) * (experts + 1) + e] = hist[e];
 }
 
-// Places of workgroup b's slots.  base[e] starts as the place of its first
-// slot of bucket e: all slots of lower buckets, and bucket e's in the
-// workgroups before.  Then 1024 slots at a time, in order: a wave finds the
-// lanes with its bucket by one ballot per bit; the sixteen waves' counts are
-// added up in wave order.
-// ALONE: one workgroup, which counts by itself.
-template <typename I, bool ALONE>
-__global__ __launch_bounds__(kSortThreads) void k_expert_place(const I* ids, int slots, int per, int bits, Routes r,
-                                                              const int32_t* counts) {
-  constexpr int NW = kSortThreads / 64;
-  __shared__ int total[kMaxExperts + 1], base[kMaxExperts + 1], wave_sum[NW];
-  extern __shared__ uint16_t wave_count[];   // NW x (experts + 1), within the 1024 slots
-  const int ne = r.experts + 1, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lo = blockIdx.x * per, hi = min(slots, lo + per);
-  for (int e = tid; e < ne; e += kSortThreads) total[e] = base[e] = 0;
-  __syncthreads();
-  if constexpr (ALONE) {
-    for (int i = tid; i < slots; i += kSortThreads) atomicAdd(&total[bucket(ids, i, r.experts)], 1);
-  } else {
-    for (int e = lane; e < ne; e += 64) {
-      int all = 0, before = 0;
-      for (int b = wave; b < static_cast<int>(gridDim.x); b += NW) {
-        const int c = gmem(counts)[static_cast<int64_t>(b) * ne + e];
-        all += c;
-        if (b < static_cast<int>(blockIdx.x)) before += c;
-      }
-      atomicAdd(&total[e], all);
-      atomicAdd(&base[e], before);
-    }
-  }
-  __syncthreads();
-  // Exclusive sums of total (one bucket a thread, and the last one).
-  {
-    const int v = tid < ne ? total[tid] : 0;
-    int sum = v;
+// Many workgroups: counts[b][e] becomes the number of slots of bucket e in the
+// workgroups before b, and the row behind the last one their number in all.
+// A workgroup per bucket.
+__global__ __launch_bounds__(kSortThreads) void k_expert_scan(int32_t* counts, int blocks, int ne) {
+  __shared__ int wave_sum[kSortThreads / 64];
+  const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int before = 0;
+  for (int b0 = 0; b0 <= blocks; b0 += kSortThreads) {
+    const int b = b0 + tid;
+    const int c = b < blocks ? counts[static_cast<int64_t>(b) * ne + e] : 0;
+    int sum = c;
     for (int d = 1; d < 64; d <<= 1) {
       const int up = __shfl_up(sum, d);
       if (lane >= d) sum += up;
     }
     if (lane == 63) wave_sum[wave] = sum;
     __syncthreads();
-    int below = 0;
-    for (int w = 0; w < wave; ++w) below += wave_sum[w];
-    const int first = below + sum - v;
-    if (tid < ne) {
-      base[tid] += first;
-      if (blockIdx.x == 0) r.offsets[tid] = first;
+    int below = before, all = 0;
+    for (int w = 0; w < kSortThreads / 64; ++w) {
+      if (w < wave) below += wave_sum[w];
+      all += wave_sum[w];
     }
-    if (ne > kSortThreads && tid == kSortThreads - 1) {
-      base[kSortThreads] += first + v;
-      if (blockIdx.x == 0) r.offsets[kSortThreads] = first + v;
-    }
+    if (b <= blocks) counts[static_cast<int64_t>(b) * ne + e] = below + sum - c;
+    before += all;
+    __syncthreads();
+  }
+}
+
+// Places of workgroup b's slots.  Wave w has a run of consecutive slots of its
+// own, taken 64 at a time: the lanes with one bucket are found by a ballot per
+// bit, and the wave's own counters (LDS, no barrier) say how many came before.
+// Then the waves' counts, the workgroups' (counts[], k_expert_count) and the
+// buckets' are added up, and every slot's place is its bucket's start + the
+// counts before + its number within the wave.
+constexpr int kSortWaves = kSortThreads / 64;
+enum SortOthers { SORT_ALONE, SORT_SUMMED, SORT_SCANNED };   // no other workgroup; counts[]; k_expert_scan's
+
+template <typename I, SortOthers OTHERS>
+__global__ __launch_bounds__(kSortThreads) void k_expert_place(const I* ids, int slots, int per, int bits, Routes r,
+                                                              const int32_t* counts) {
+  constexpr int MOST = kSortAlone / kSortThreads;   // turns of 64 slots of a wave
+  __shared__ int base[kMaxExperts + 1], totals[kMaxExperts + 1], wave_sum[kSortWaves];
+  extern __shared__ uint16_t wave_count[];   // waves x (experts + 1); a wave has at most 64 * MOST slots
+  const int ne = r.experts + 1, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lo = blockIdx.x * per, hi = min(slots, lo + per);
+  const int turns = (hi - lo + kSortThreads - 1) / kSortThreads, from = lo + wave * turns * 64;
+  uint16_t* mine = wave_count + wave * ne;
+  for (int e = lane; e < ne; e += 64) mine[e] = 0;
+  for (int e = tid; e < ne; e += kSortThreads) base[e] = totals[e] = 0;
+  int bucket_of[MOST], before[MOST];   // of the lane's slots
+#pragma unroll
+  for (int t = 0; t < MOST; ++t) {
+    const int i = from + t * 64 + lane;
+    bucket_of[t] = t < turns && i < hi ? bucket(ids, i, r.experts) : -1;
   }
   __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += kSortThreads) {
-    for (int e = tid; e < NW * ne; e += kSortThreads) wave_count[e] = 0;
-    __syncthreads();
-    const int i = i0 + tid;
-    const bool in = i < hi;
-    const int b = in ? bucket(ids, i, r.experts) : -1;
-    uint64_t same = __ballot(in);
+#pragma unroll
+  for (int t = 0; t < MOST; ++t) {
+    if (t >= turns) break;
+    const int b = bucket_of[t];
+    uint64_t same = __ballot(b >= 0);
     for (int k = 0; k < bits; ++k) {
       const bool bit = (b >> k) & 1;
       const uint64_t v = __ballot(bit);
       same &= bit ? v : ~v;
     }
     const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
-    if (in && rank == 0) wave_count[wave * ne + b] = static_cast<uint16_t>(__popcll(same));
-    __syncthreads();
-    for (int e = tid; e < ne; e += kSortThreads) {
-      int at = 0;
-      for (int w = 0; w < NW; ++w) {
-        const int c = wave_count[w * ne + e];
-        wave_count[w * ne + e] = static_cast<uint16_t>(at);
-        at += c;
+    const int seen = b >= 0 ? mine[b] : 0;
+    before[t] = seen + rank;
+    // (The wave's reads of its counters come before the update, which one
+    // lane of each bucket makes, and that before the next turn's reads.)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (b >= 0 && rank == 0) mine[b] = static_cast<uint16_t>(seen + __popcll(same));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  if constexpr (OTHERS == SORT_SUMMED) {
+    for (int e = lane; e < ne; e += 64) {
+      int all = 0, sum = 0;
+#pragma unroll 4
+      for (int b = wave; b < static_cast<int>(gridDim.x); b += kSortWaves) {
+        const int c = gmem(counts)[static_cast<int64_t>(b) * ne + e];
+        all += c;
+        sum += b < static_cast<int>(blockIdx.x) ? c : 0;
       }
-      total[e] = at;
+      if (all) atomicAdd(&totals[e], all);
+      if (sum) atomicAdd(&base[e], sum);
     }
-    __syncthreads();
-    if (in) {
-      const int at = base[b] + wave_count[wave * ne + b] + rank;
-      const bool routed = b < r.experts;
-      r.order[at] = routed ? i : -1;
-      r.place[i] = routed ? at : -1;
+  } else if constexpr (OTHERS == SORT_SCANNED) {
+    for (int e = tid; e < ne; e += kSortThreads) {
+      base[e] = gmem(counts)[static_cast<int64_t>(blockIdx.x) * ne + e];
+      totals[e] = gmem(counts)[static_cast<int64_t>(gridDim.x) * ne + e];
     }
-    __syncthreads();
-    for (int e = tid; e < ne; e += kSortThreads) base[e] += total[e];
+  }
+  __syncthreads();
+  // Thread e < ne: the waves' counts become what came before them; the
+  // bucket's slots in all.
+  int total = 0;
+  for (int e = tid; e < ne; e += kSortThreads) {
+    int at = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = wave_count[w * ne + e];
+      wave_count[w * ne + e] = static_cast<uint16_t>(at);
+      at += c;
+    }
+    if (e == tid) total = OTHERS == SORT_ALONE ? at : totals[e];
+  }
+  // Exclusive sums over the buckets (one a thread; bucket 1024, of the
+  // unrouted slots, starts where the last thread's ends).
+  int sum = total;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(sum, d);
+    if (lane >= d) sum += up;
+  }
+  if (lane == 63) wave_sum[wave] = sum;
+  __syncthreads();
+  int below = 0;
+  for (int w = 0; w < wave; ++w) below += wave_sum[w];
+  const int first = below + sum - total;
+  auto start = [&](int e, int at) {
+    base[e] += at;
+    if (blockIdx.x == 0) r.offsets[e] = at;
+  };
+  if (tid < ne) start(tid, first);
+  if (ne > kSortThreads && tid == kSortThreads - 1) start(kSortThreads, first + total);
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < MOST; ++t) {
+    const int b = bucket_of[t];
+    if (b < 0) continue;
+    const int i = from + t * 64 + lane, at = base[b] + mine[b] + before[t];
+    const bool routed = b < r.experts;
+    r.order[at] = routed ? i : -1;
+    r.place[i] = routed ? at : -1;
   }
 }
 
@@ -134,17 +183,13 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <typename T, bool VEC>
 struct Run {
   static constexpr int V = VEC ? 16 / sizeof(T) : 1;
+  using Raw = typename std::conditional<VEC, u32x4, T>::type;   // as loaded
   float v[V];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (VEC) {
-      set(*reinterpret_cast<const MUON_GLOBAL u32x4*>(gmem(p)));
-    } else if constexpr (sizeof(T) == 4) {
-      v[0] = gmem(reinterpret_cast<const float*>(p))[0];
-    } else {
-      v[0] = bf16_to_f32(gmem(reinterpret_cast<const uint16_t*>(p))[0]);
-    }
+  static __device__ __forceinline__ Raw read(const T* p) {
+    return *reinterpret_cast<const MUON_GLOBAL Raw*>(gmem(p));
   }
-  __device__ __forceinline__ void set(u32x4 u) {
+  __device__ __forceinline__ void load(const T* p) { set(read(p)); }
+  __device__ __forceinline__ void set(Raw u) {
     if constexpr (VEC) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -155,6 +200,10 @@ struct Run {
           v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
         }
       }
+    } else if constexpr (sizeof(T) == 4) {
+      v[0] = u;
+    } else {
+      v[0] = bf16_to_f32(u);
     }
   }
   __device__ __forceinline__ void store(T* p) const {
@@ -182,6 +231,21 @@ __device__ __forceinline__ int place_of(const MoveArgs& a, int64_t slot) {
   return (p >= 0 && p < a.slots) ? p : -1;
 }
 
+// Choices of a token that are handled at once, their rows' loads in flight together.
+constexpr int kAtOnce = 8;
+
+// Places (and weights) of the choices j0 .. j0 + 7 of the token whose slots
+// start at `slot0`; -1 where there is none.
+__device__ __forceinline__ void places_of(const MoveArgs& a, int64_t slot0, int j0, int (&p)[kAtOnce]) {
+#pragma unroll
+  for (int j = 0; j < kAtOnce; ++j) p[j] = j0 + j < a.top ? place_of(a, slot0 + j0 + j) : -1;
+}
+__device__ __forceinline__ void weights_of(const MoveArgs& a, int64_t slot0, int j0, float (&w)[kAtOnce]) {
+#pragma unroll
+  for (int j = 0; j < kAtOnce; ++j)
+    w[j] = j0 + j < a.top && a.weights ? load_elem(a.weights, slot0 + j0 + j, a.w_dt) : 1.0f;
+}
+
 // xs[place[t][j]] = x[t]: a thread reads one run of a token and writes it to
 // every row of the token.
 template <typename T, bool VEC>
@@ -190,12 +254,15 @@ __global__ __launch_bounds__(kMoveThreads) void k_expert_gather(MoveArgs a, int 
   const int64_t n = static_cast<int64_t>(a.tokens) * runs, step = static_cast<int64_t>(gridDim.x) * kMoveThreads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; i < n; i += step) {
     const int64_t t = i / runs;
-    const int col = static_cast<int>(i % runs) * R::V;
+    const int col = static_cast<int>(i - t * runs) * R::V;
     R x;
     x.load(static_cast<const T*>(a.tok) + t * a.tok_ld + col);
-    for (int j = 0; j < a.top; ++j) {
-      const int p = place_of(a, t * a.top + j);
-      if (p >= 0) x.store(static_cast<T*>(a.rows_out) + p * a.rows_out_ld + col);
+    for (int j0 = 0; j0 < a.top; j0 += kAtOnce) {
+      int p[kAtOnce];
+      places_of(a, t * a.top, j0, p);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (p[j] >= 0) x.store(static_cast<T*>(a.rows_out) + p[j] * a.rows_out_ld + col);
     }
   }
 }
@@ -208,7 +275,7 @@ __global__ __launch_bounds__(kMoveThreads) void k_expert_combine(MoveArgs a, int
   const int64_t n = static_cast<int64_t>(a.tokens) * runs, step = static_cast<int64_t>(gridDim.x) * kMoveThreads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; i < n; i += step) {
     const int64_t t = i / runs;
-    const int col = static_cast<int>(i % runs) * R::V;
+    const int col = static_cast<int>(i - t * runs) * R::V;
     R y;
     if (a.tok) {
       y.load(static_cast<const T*>(a.tok) + t * a.tok_ld + col);
@@ -216,50 +283,93 @@ __global__ __launch_bounds__(kMoveThreads) void k_expert_combine(MoveArgs a, int
 #pragma unroll
       for (int e = 0; e < R::V; ++e) y.v[e] = 0.0f;
     }
-    for (int j = 0; j < a.top; ++j) {
-      const int64_t slot = t * a.top + j;
-      const int p = place_of(a, slot);
-      if (p < 0) continue;
-      const float w = a.weights ? load_elem(a.weights, slot, a.w_dt) : 1.0f;
-      R x;
-      x.load(static_cast<const T*>(a.rows) + p * a.rows_ld + col);
+    for (int j0 = 0; j0 < a.top; j0 += kAtOnce) {
+      int p[kAtOnce];
+      float w[kAtOnce];
+      typename R::Raw x[kAtOnce];
+      places_of(a, t * a.top, j0, p);
+      weights_of(a, t * a.top, j0, w);
 #pragma unroll
-      for (int e = 0; e < R::V; ++e) y.v[e] = __builtin_fmaf(w, x.v[e], y.v[e]);
+      for (int j = 0; j < kAtOnce; ++j)
+        if (p[j] >= 0) x[j] = R::read(static_cast<const T*>(a.rows) + p[j] * a.rows_ld + col);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (p[j] < 0) continue;
+        R v;
+        v.set(x[j]);
+#pragma unroll
+        for (int e = 0; e < R::V; ++e) y.v[e] = __builtin_fmaf(w[j], v.v[e], y.v[e]);
+      }
     }
     y.store(static_cast<T*>(a.tok_out) + t * a.tok_out_ld + col);
   }
 }
 
-// dys[place[t][j]] = w[t][j] dy[t];  dw[t][j] = <dy[t], ys[place[t][j]]>: a
-// workgroup per token and choice.
-template <typename T, bool VEC>
+// dys[place[t][j]] = w[t][j] dy[t];  dw[t][j] = <dy[t], ys[place[t][j]]>: WPT
+// waves per token (four for wide rows, one for narrow ones).
+template <typename T, bool VEC, int WPT>
 __global__ __launch_bounds__(kMoveThreads) void k_expert_combine_grad(MoveArgs a, int runs) {
   using R = Run<T, VEC>;
-  __shared__ float red[kMoveThreads / 64];
-  for (int64_t slot = blockIdx.x; slot < a.slots; slot += gridDim.x) {
-    const int64_t t = slot / a.top;
-    const int p = place_of(a, slot);
-    float dot = 0.0f;
-    if (p >= 0) {
-      const float w = load_elem(a.weights, slot, a.w_dt);
-      for (int c = threadIdx.x; c < runs; c += kMoveThreads) {
-        const int col = c * R::V;
-        R g, x;
-        g.load(static_cast<const T*>(a.tok) + t * a.tok_ld + col);
-        x.load(static_cast<const T*>(a.rows) + p * a.rows_ld + col);
+  constexpr int TPW = kMoveThreads / 64 / WPT, LANES = 64 * WPT;   // tokens of a workgroup, threads of a token
+  __shared__ float red[kAtOnce][kMoveThreads / 64];
+  const int wave = threadIdx.x >> 6, thread = threadIdx.x % LANES;
+  const int64_t groups = (static_cast<int64_t>(a.tokens) + TPW - 1) / TPW;
+  for (int64_t b = blockIdx.x; b < groups; b += gridDim.x) {
+    const int64_t t = b * TPW + wave / WPT;
+    const bool in = t < a.tokens;
+    for (int j0 = 0; j0 < a.top; j0 += kAtOnce) {
+      float dot[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < R::V; ++e) {
-          dot = __builtin_fmaf(g.v[e], x.v[e], dot);
-          g.v[e] *= w;
+      for (int j = 0; j < kAtOnce; ++j) dot[j] = 0.0f;
+      if (in) {
+        int p[kAtOnce];
+        float w[kAtOnce];
+        places_of(a, t * a.top, j0, p);
+        weights_of(a, t * a.top, j0, w);
+        for (int c = thread; c < runs; c += LANES) {
+          const int col = c * R::V;
+          R g;
+          typename R::Raw x[kAtOnce];
+          g.load(static_cast<const T*>(a.tok) + t * a.tok_ld + col);
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            if (p[j] >= 0) x[j] = R::read(static_cast<const T*>(a.rows) + p[j] * a.rows_ld + col);
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            if (p[j] < 0) continue;
+            R v;
+            v.set(x[j]);
+#pragma unroll
+            for (int e = 0; e < R::V; ++e) {
+              dot[j] = __builtin_fmaf(g.v[e], v.v[e], dot[j]);
+              v.v[e] = g.v[e] * w[j];
+            }
+            v.store(static_cast<T*>(a.rows_out) + p[j] * a.rows_out_ld + col);
+          }
         }
-        g.store(static_cast<T*>(a.rows_out) + p * a.rows_out_ld + col);
       }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        dot[j] = wave_tree_sum(dot[j]);
+        if (WPT > 1 && (threadIdx.x & 63) == 0) red[j][wave] = dot[j];
+      }
+      if constexpr (WPT > 1) __syncthreads();
+      if (thread < kAtOnce && in && j0 + thread < a.top) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          float v = dot[j];
+          if constexpr (WPT > 1) {
+            v = red[j][wave / WPT * WPT];
+#pragma unroll
+            for (int w = 1; w < WPT; ++w) v += red[j][wave / WPT * WPT + w];
+          }
+          s = j == thread ? v : s;
+        }
+        store_elem(a.dweights, t * a.top + j0 + thread, a.w_dt, s);
+      }
+      if constexpr (WPT > 1) __syncthreads();
     }
-    dot = wave_tree_sum(dot);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) store_elem(a.dweights, slot, a.w_dt, (red[0] + red[1]) + (red[2] + red[3]));
-    __syncthreads();
   }
 }
 
@@ -283,22 +393,25 @@ hipError_t launch_expert_sort(const void* ids, int id_bytes, const Routes& r, in
   while ((1 << bits) <= r.experts) ++bits;
   const size_t lds = sizeof(uint16_t) * (kSortThreads / 64) * (r.experts + 1);
   const dim3 grid(static_cast<uint32_t>(blocks)), threads(kSortThreads);
+  const int n = static_cast<int>(per);
 #define MUON_SORT(I)                                                                                                  \
-  if (blocks > 1) {                                                                                                   \
-    hipLaunchKernelGGL(k_expert_count<I>, grid, threads, 0, s, static_cast<const I*>(ids), r.slots, (int)per,         \
-                       r.experts, counts);                                                                            \
-    hipError_t e = hipGetLastError();                                                                                 \
-    if (e != hipSuccess) return e;                                                                                    \
-    hipLaunchKernelGGL((k_expert_place<I, false>), grid, threads, lds, s, static_cast<const I*>(ids), r.slots,        \
-                       (int)per, bits, r, counts);                                                                    \
-  } else {                                                                                                            \
-    hipLaunchKernelGGL((k_expert_place<I, true>), grid, threads, lds, s, static_cast<const I*>(ids), r.slots,         \
-                       (int)per, bits, r, counts);                                                                    \
-  }
+  do {                                                                                                                \
+    const I* p = static_cast<const I*>(ids);                                                                          \
+    if (blocks > 1)                                                                                                   \
+      hipLaunchKernelGGL(k_expert_count<I>, grid, threads, 0, s, p, r.slots, n, r.experts, counts);                   \
+    if (blocks > kSortSummed)                                                                                         \
+      hipLaunchKernelGGL(k_expert_scan, dim3(r.experts + 1), threads, 0, s, counts, (int)blocks, r.experts + 1);      \
+    if (blocks == 1)                                                                                                  \
+      hipLaunchKernelGGL((k_expert_place<I, SORT_ALONE>), grid, threads, lds, s, p, r.slots, n, bits, r, counts);     \
+    else if (blocks <= kSortSummed)                                                                                   \
+      hipLaunchKernelGGL((k_expert_place<I, SORT_SUMMED>), grid, threads, lds, s, p, r.slots, n, bits, r, counts);    \
+    else                                                                                                              \
+      hipLaunchKernelGGL((k_expert_place<I, SORT_SCANNED>), grid, threads, lds, s, p, r.slots, n, bits, r, counts);   \
+  } while (0)
   if (id_bytes == 8) {
-    MUON_SORT(int64_t)
+    MUON_SORT(int64_t);
   } else {
-    MUON_SORT(int32_t)
+    MUON_SORT(int32_t);
   }
 #undef MUON_SORT
   return hipGetLastError();
@@ -327,7 +440,21 @@ hipError_t launch_expert_combine(const MoveArgs& a, int dt, bool vec, hipStream_
   MUON_MOVE(k_expert_combine, blocks_of(a, runs));
 }
 hipError_t launch_expert_combine_grad(const MoveArgs& a, int dt, bool vec, hipStream_t s) {
-  MUON_MOVE(k_expert_combine_grad, std::min<int64_t>(kMaxBlocks, a.slots));
+  const bool wide = a.width / (vec ? (dt == DT_BF16 ? 8 : 4) : 1) > 128;
+  const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(kMaxBlocks, wide ? a.tokens : (a.tokens + 3) / 4)));
+#define MUON_GRAD(T, VEC)                                                                                              \
+  do {                                                                                                                 \
+    const int runs = runs_of<T>(a, VEC);                                                                               \
+    if (wide) hipLaunchKernelGGL((k_expert_combine_grad<T, VEC, 4>), grid, dim3(kMoveThreads), 0, s, a, runs);         \
+    else hipLaunchKernelGGL((k_expert_combine_grad<T, VEC, 1>), grid, dim3(kMoveThreads), 0, s, a, runs);              \
+  } while (0)
+  if (dt == DT_BF16) {
+    if (vec) MUON_GRAD(uint16_t, true); else MUON_GRAD(uint16_t, false);
+  } else {
+    if (vec) MUON_GRAD(float, true); else MUON_GRAD(float, false);
+  }
+#undef MUON_GRAD
+  return hipGetLastError();
 }
 #undef MUON_MOVE
 

@@ -381,7 +381,8 @@ def make_ids(tokens, top, experts, drop, seed, dtype):
 SORTS = [(1, 1, 1, 0.0, "i64"), (1, 1, 1, 1.0, "i32"), (0, 2, 5, 0.0, "i32"), (8, 6, 64, 0.0, "i64"), (63, 1, 3, 0.2, "i32"),
          (64, 1, 2, 0.0, "i64"), (65, 2, 7, 0.3, "i64"), (1000, 3, 37, 0.14, "i32"), (1024, 8, 128, 0.0, "i64"),
          (8193, 1, 1, 0.0, "i32"), (4097, 2, 64, 0.1, "i64"), (1500, 7, 1024, 0.05, "i64"), (40, 3, 1024, 0.5, "i32"),
-         (300000, 1, 9, 0.5, "i32"), (9000, 1, 4, 1.0, "i64")]
+         (300000, 1, 9, 0.5, "i32"), (9000, 1, 4, 1.0, "i64"),
+         (1100000, 2, 5, 0.1, "i32"), (2730, 3, 200, 0.1, "i64"), (2731, 3, 1023, 0.3, "i32")]
 
 
 @gpu
