@@ -185,6 +185,10 @@ struct Run {
   static constexpr int V = VEC ? 16 / sizeof(T) : 1;
   using Raw = typename std::conditional<VEC, u32x4, T>::type;   // as loaded
   float v[V];
+  // Rows that are read once, past the caches' lines in use.
+  static __device__ __forceinline__ Raw read_once(const T* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const MUON_GLOBAL Raw*>(gmem(p)));
+  }
   static __device__ __forceinline__ Raw read(const T* p) {
     return *reinterpret_cast<const MUON_GLOBAL Raw*>(gmem(p));
   }
@@ -247,7 +251,8 @@ __device__ __forceinline__ void weights_of(const MoveArgs& a, int64_t slot0, int
 }
 
 // xs[place[t][j]] = x[t]: a thread reads one run of a token and writes it to
-// every row of the token.
+// every row of the token (rows in their own order, each reading its token,
+// take 40% longer: the training batch's 403 MB 130 instead of 91 us).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kMoveThreads) void k_expert_gather(MoveArgs a, int runs) {
   using R = Run<T, VEC>;
@@ -291,7 +296,7 @@ __global__ __launch_bounds__(kMoveThreads) void k_expert_combine(MoveArgs a, int
       weights_of(a, t * a.top, j0, w);
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
-        if (p[j] >= 0) x[j] = R::read(static_cast<const T*>(a.rows) + p[j] * a.rows_ld + col);
+        if (p[j] >= 0) x[j] = R::read_once(static_cast<const T*>(a.rows) + p[j] * a.rows_ld + col);
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         if (p[j] < 0) continue;
@@ -380,8 +385,8 @@ int runs_of(const MoveArgs& a, bool vec) {
 
 // Workgroups for n threads' work; longer work is walked in strides.
 constexpr int64_t kMaxBlocks = int64_t{1} << 22;
-int64_t blocks_of(const MoveArgs& a, int runs) {
-  return std::min(kMaxBlocks, (static_cast<int64_t>(a.tokens) * runs + kMoveThreads - 1) / kMoveThreads);
+int64_t blocks_of(int64_t rows, int runs) {
+  return std::min(kMaxBlocks, (rows * runs + kMoveThreads - 1) / kMoveThreads);
 }
 
 }  // namespace
@@ -434,10 +439,10 @@ hipError_t launch_expert_sort(const void* ids, int id_bytes, const Routes& r, in
   } while (0)
 
 hipError_t launch_expert_gather(const MoveArgs& a, int dt, bool vec, hipStream_t s) {
-  MUON_MOVE(k_expert_gather, blocks_of(a, runs));
+  MUON_MOVE(k_expert_gather, blocks_of(a.tokens, runs));
 }
 hipError_t launch_expert_combine(const MoveArgs& a, int dt, bool vec, hipStream_t s) {
-  MUON_MOVE(k_expert_combine, blocks_of(a, runs));
+  MUON_MOVE(k_expert_combine, blocks_of(a.tokens, runs));
 }
 hipError_t launch_expert_combine_grad(const MoveArgs& a, int dt, bool vec, hipStream_t s) {
   const bool wide = a.width / (vec ? (dt == DT_BF16 ? 8 : 4) : 1) > 128;

@@ -985,6 +985,7 @@ using Plain = Geo<128, 128, 2, 2, 2, 2 * Medium::STRIP>;   // operands through r
 using Small = Geo<64, 128, 1, 4, 4>;
 using MediumDeep = Geo<128, 128, 2, 2, 8>;
 using SmallDeep = Geo<64, 128, 1, 4, 8>;
+using Tiny = Geo<64, 64, 2, 2, 8>;
 
 int64_t ceil_of(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -1049,8 +1050,14 @@ hipError_t pick(const LinArgs& a, int dt, int align, bool dry, hipStream_t s) {
       return dt == DT_F32 ? go_thin<true>(a, dry, s) : go_thin<false>(a, dry, s);
   }
   if (dt == DT_F32) {
-    // (A float32 product is slow enough that 64-row tiles lose nothing.)
-    if (align == 16) return medium <= 512 ? go<true, MODE, Small, 16>(a, dry, s) : go<true, MODE, Medium, 16>(a, dry, s);
+    // A float32 product is slow enough (an eighth of the bf16 rate) that small
+    // tiles lose nothing, and few large ones leave CUs idle: 9 groups of 300
+    // rows, 517 x 259: 33 us in 64 x 128 tiles.
+    if (align == 16) {
+      if (small <= 256) return go<true, MODE, Tiny, 16>(a, dry, s);
+      return medium <= 512 ? go<true, MODE, Small, 16>(a, dry, s) : go<true, MODE, Medium, 16>(a, dry, s);
+    }
+    if (small <= 256) return go<true, MODE, Tiny, 4>(a, dry, s);
     return medium <= 512 ? go<true, MODE, Small, 4>(a, dry, s) : go<true, MODE, Medium, 4>(a, dry, s);
   }
   if (align == 4) return medium <= 512 ? go<false, MODE, Small, 4>(a, dry, s) : go<false, MODE, Medium, 4>(a, dry, s);
