@@ -88,6 +88,7 @@ hipError_t launch_linear_slope(const void* dy, int64_t ld_dy, const void* pre, i
                                const int32_t* offsets, int groups, int64_t rows, int64_t out, int act, int dt, int align,
                                hipStream_t s);
 int linear_bias_parts(int64_t rows, int64_t groups);
+bool linear_bias_fits(int64_t out, int64_t groups);
 // db (+)= column sums of every group's rows, in `parts` parts.
 hipError_t launch_linear_bias(const void* dz, int64_t ld, const int32_t* offsets, int groups, int64_t rows, int64_t out,
                               void* db, int dt, int grad_dt, int accumulate, float* part, int parts, hipStream_t s);

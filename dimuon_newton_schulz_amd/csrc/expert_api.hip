@@ -470,6 +470,7 @@ muon_status_t linear_grad(const linear_grad_args_t* p, void* workspace, size_t w
     wt.part = reinterpret_cast<float*>(ws + l.part);
     if ((p->dx && !linear_fits(in, LIN_INPUT, p->dtype, align)) || (p->dw && !linear_fits(wt, LIN_WEIGHT, p->dtype, align)))
       return fail(MUON_ERR_UNSUPPORTED, "the product is too large");
+    if (p->db && !linear_bias_fits(p->out, p->groups)) return fail(MUON_ERR_UNSUPPORTED, "the bias is too large");
     MUON_HOOK_START();
     if (has_act && p->rows)
       MUON_LAUNCH(MUON_LAUNCH_LINEAR_SLOPE,

@@ -1123,6 +1123,9 @@ hipError_t launch_linear_slope(const void* dy, int64_t ld_dy, const void* pre, i
   return hipGetLastError();
 }
 
+// (A launch has fewer than 2^32 threads.)
+bool linear_bias_fits(int64_t out, int64_t groups) { return ceil_of(out, 64) * groups * kBiasThreads < int64_t{1} << 32; }
+
 int linear_bias_parts(int64_t rows, int64_t groups) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows / groups / 256, 64)));
 }

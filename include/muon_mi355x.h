@@ -547,7 +547,9 @@ muon_status_t expert_combine_grad(const void* dy, int64_t dy_stride, const void*
  * With `accumulate`, dW and db are added to what the buffers hold; without,
  * groups without rows get zeros.  Rows of no group (before offsets[0], behind
  * offsets[groups]) are left as they were in y, pre and dx.  offsets are
- * nondecreasing and within 0 .. rows; others are cut to that.
+ * nondecreasing and within 0 .. rows.  Those outside that range are cut to it;
+ * with decreasing ones the results are undefined, but nothing outside the
+ * buffers is touched.
  *
  * Products of bf16 values with float32 sums (MFMA), or of float32 values
  * (dtype F32).  y and pre are rounded once from float32, y from the unrounded
@@ -557,7 +559,8 @@ muon_status_t expert_combine_grad(const void* dy, int64_t dy_stride, const void*
  * Strides are in elements, rows' elements consecutive, strides at most 2^20.
  * The fast case: in and out multiples of 8, rows and group strides on 16-byte
  * borders.  bias, db: groups x out, consecutive.  Limits: rows < 2^30; in and
- * out 1 .. 65536 (as for muon_step); groups 1 .. 4096.  rows = 0 is allowed
+ * out 1 .. 65536 (as for muon_step); groups 1 .. 4096; at most 2^23 - 1 tiles
+ * of 64 x 128 (16 x 16 where a group has few rows).  rows = 0 is allowed
  * (dW and db are then zero, or unchanged).  A written buffer overlaps no other
  * buffer, except that y may be the residual itself (same pointer and stride).
  * offsets live on the device: no call waits for the host.

@@ -272,7 +272,8 @@ GRAD_REFUSALS = {
     "grad_dtype": (dict(grad_dtype=4), 2), "x_activation": (dict(x_activation=-1), 1),
     "dw_stride": (dict(dw_stride=60), 1), "dw_groups": (dict(dw_group_stride=1024), 1),
     "dx_on_dy": (dict(dx=BASE + STEP), 4), "dw_on_w": (dict(dw=BASE + 4 * STEP), 4), "db_in_dw": (dict(db=BASE + 7 * STEP), 4),
-    "dx_on_x": (dict(dx=BASE + 3 * STEP), 4), "ws_null": ({}, 3), "ws_small": ({}, 3), "ws_misaligned": ({}, 3),
+    "dx_on_x": (dict(dx=BASE + 3 * STEP), 4),
+    "db_many": (dict(out=65536, groups=4096, dy_stride=65536, pre_stride=65536, dx=None, dw=None, rows=10), 6), "ws_null": ({}, 3), "ws_small": ({}, 3), "ws_misaligned": ({}, 3),
     "ws_alias": ({}, 4),
 }
 
