@@ -220,7 +220,7 @@ template <int BM_, int BN_, int WR_, int WC_, int U_, int UNIT_ = (BM_ > BN_ ? B
 struct Geo {
   static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, U = U_, UNIT = UNIT_;   // UNIT: bytes
   static constexpr int NW = WR * WC, NT = 64 * NW, WM = BM / WR, WN = BN / WC, MS = WM / 16, NS = WN / 16;
-  // Each wave stages 32 output rows at a time in a strip of its own.
+  // A wave's strip of 32 output rows (where they lie on no 16-byte borders).
   static constexpr int SP = WN + 4, STRIP = 32 * SP * 4;
 };
 constexpr int KB = 128, NQ = 2;   // a stage's k: bytes, and steps of 32 (bf16) or 16 (f32) values
@@ -536,6 +536,22 @@ __device__ __forceinline__ void unpack8(const u32x4_t (&u)[W], bool f32, float (
     }
   }
 }
+__device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
+  u32x4_t u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) u[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+  return u;
+}
+// Lanes 8-15 of each row of 16 take u[1] of the lane eight below, lanes 0-7
+// u[0] of the lane eight above (its own inverse).
+__device__ __forceinline__ void exchange8(u32x4_t (&u)[2]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int x = static_cast<int>(u[0][e]), y = static_cast<int>(u[1][e]);
+    u[0][e] = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false));   // row_ror:8
+    u[1][e] = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false));
+  }
+}
 __device__ __forceinline__ void store8(void* p, const float (&v)[8], bool f32) {
   MUON_GLOBAL u32x4_t* q = reinterpret_cast<MUON_GLOBAL u32x4_t*>(gmem(static_cast<char*>(p)));
   if (f32) {
@@ -548,10 +564,7 @@ __device__ __forceinline__ void store8(void* p, const float (&v)[8], bool f32) {
     q[0] = a;
     q[1] = b;
   } else {
-    u32x4_t a;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-    q[0] = a;
+    q[0] = pack8(v);
   }
 }
 
@@ -647,83 +660,159 @@ __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* cons
   const Operand<F32, QKM, G::BN, G::NT, AL> Q(w.q, a.ldq, w.n_valid, w.k);
   product<F32, PKM, QKM, G, AL>(P, Q, w.k, ring, row_p, row_q, acc);
 
-  // Through the wave's strip: a lane puts four columns of one row at a time
-  // and takes eight, so that global accesses are whole 16-byte runs.
-  __syncthreads();
-  constexpr int PER = G::UNIT / G::STRIP, CPR = G::WN / 8;   // strips of a unit
-  static_assert(PER * G::U >= G::NW, "strips fit the ring");
-  uint32_t base = 0;
-#pragma unroll
-  for (int b = 0; b < G::U; ++b)
-    base = wave / PER == b ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MUON_LDS char*)ring[b])) : base;
-  MUON_LDS float* strip = (MUON_LDS float*)(static_cast<uintptr_t>(base + (wave % PER) * G::STRIP));
   const Old<F32, MODE> old(a, w.group);
-  constexpr int PASSES = 32 * CPR / 64;
-  const int c8 = lane % CPR * 8, r8 = lane / CPR, n8 = w.n0 + row_q + c8;   // a lane's column run is the same in all passes
-  float bias[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int OW = F32 || MODE == LIN_WEIGHT ? 2 : 1;   // loads of eight old values
-  u32x4_t now[PASSES][OW], next[PASSES][OW];
-  // What a strip's results are combined with is read a strip ahead (the
-  // compiler cannot move these reads before the stores, which may be to the
-  // same array).
-  auto fetch = [&](int s, u32x4_t (&o)[PASSES][OW]) {
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int r = row_p + s * 32 + r8 + i * (64 / CPR);
-      if (r < w.m_valid && n8 < a.n) {
-        const MUON_GLOBAL u32x4_t* p = reinterpret_cast<const MUON_GLOBAL u32x4_t*>(
-            gmem(static_cast<const char*>(old.p) + (old.at + (w.row0 + r) * old.ld + n8) * (old.f32 ? 4 : 2)));
-        o[i][0] = p[0];
-        if constexpr (OW == 2) {
-          if (old.f32) o[i][1] = p[1];
-        }
-      }
-    }
-  };
   if constexpr (AL == 16) {
-    if (MODE == LIN_FORWARD && a.bias && n8 < a.n) load_run(a.bias, static_cast<int64_t>(w.group) * a.n + n8, F32, bias);
+    // A lane holds columns 4 (l / 16) .. + 3 of row l mod 16 of each 16 x 16
+    // block.  Swapping the odd rows of 16 lanes of one block with the even
+    // ones of the next gives every lane a run of eight columns, without a way
+    // through LDS.  Two such runs, 32 columns apart, are handled together: in
+    // bf16 their halves are exchanged (exchange8), so that an access covers
+    // whole 128-byte lines of eight rows instead of half lines of sixteen.
+    constexpr int RUNS = G::NS / 2, H = RUNS >= 2 ? 2 : 1, OW = F32 || MODE == LIN_WEIGHT ? 2 : 1;
+    const int r16 = lane & 15, n8 = w.n0 + row_q + 16 * (lane >> 4 & 1) + 8 * (lane >> 5);
+    // Runs i .. i+H-1 of the 16 rows from s on, to (and from) element
+    // at + row * ld + column.
+    auto each = [&](bool halves, int s, int i, auto&& f) {   // f(which, row, column)
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const bool x = H == 2 && halves;
+        const int r = row_p + s * 16 + (x ? (r16 & 7) + 8 * h : r16), n = n8 + 32 * (i + (x ? r16 >> 3 : h));
+        if (r < w.m_valid && n < a.n) f(h, r, n);
+      }
+    };
+    auto put = [&](void* p, int64_t at, int64_t ld, bool f32, int s, int i, const float (&v)[H][8]) {
+      if (f32) {
+        each(false, s, i, [&](int h, int r, int n) { store8(static_cast<char*>(p) + (at + (w.row0 + r) * ld + n) * 4, v[h], true); });
+        return;
+      }
+      u32x4_t u[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) u[h] = pack8(v[h]);
+      if constexpr (H == 2) exchange8(u);
+      each(true, s, i, [&](int h, int r, int n) {
+        *reinterpret_cast<MUON_GLOBAL u32x4_t*>(gmem(static_cast<char*>(p) + (at + (w.row0 + r) * ld + n) * 2)) = u[h];
+      });
+    };
+    float bias[MODE == LIN_FORWARD ? RUNS : 1][8];
+    if (MODE == LIN_FORWARD && a.bias) {
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i)
+        if (n8 + 32 * i < a.n) load_run(a.bias, static_cast<int64_t>(w.group) * a.n + n8 + 32 * i, F32, bias[i]);
+    }
+    // Old values are read a row of blocks ahead (the compiler cannot move these
+    // reads before the stores, which may be to the same array).
+    u32x4_t now[RUNS][OW], next[RUNS][OW];
+    auto fetch = [&](int s, u32x4_t (&o)[RUNS][OW]) {
+#pragma unroll
+      for (int i = 0; i < RUNS; i += H)
+        each(!old.f32, s, i, [&](int h, int r, int n) {
+          const MUON_GLOBAL u32x4_t* p = reinterpret_cast<const MUON_GLOBAL u32x4_t*>(
+              gmem(static_cast<const char*>(old.p) + (old.at + (w.row0 + r) * old.ld + n) * (old.f32 ? 4 : 2)));
+          o[i + h][0] = p[0];
+          if constexpr (OW == 2) {
+            if (old.f32) o[i + h][1] = p[1];
+          }
+        });
+    };
     if (old.p) fetch(0, now);
-  }
-  // (One copy of what follows the sums, for all blocks of rows.)
+    // (One copy of what follows the sums, for all rows of blocks.)
 #pragma unroll 1
-  for (int s = 0; s < G::MS / 2; ++s) {
-    const int ms = row_p + s * 32;
-    if (ms >= w.m_valid) break;
-    if (AL == 16 && old.p && s + 1 < G::MS / 2) fetch(s + 1, next);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    for (int s = 0; s < G::MS; ++s) {
+      if (row_p + s * 16 >= w.m_valid) break;
+      if (old.p && s + 1 < G::MS) fetch(s + 1, next);
+      f32x4_t row[G::NS];
 #pragma unroll
-    for (int b = 0; b < G::MS; ++b)
-      if (b / 2 == s) {
+      for (int b = 0; b < G::MS; ++b)
+        if (b == s) {
 #pragma unroll
-        for (int t = 0; t < G::NS; ++t)
-          *(MUON_LDS f32x4_t*)(strip + (b % 2 * 16 + (lane & 15)) * G::SP + t * 16 + 4 * (lane >> 4)) = acc[b][t];
-      }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if constexpr (AL == 16) {
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int r = r8 + i * (64 / CPR);
-        if (ms + r >= w.m_valid || n8 >= a.n) continue;
-        float v[8], o[8];
-        const f32x4_t lo = *(const MUON_LDS f32x4_t*)(strip + r * G::SP + c8);
-        const f32x4_t hi = *(const MUON_LDS f32x4_t*)(strip + r * G::SP + c8 + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = lo[e];
-          v[4 + e] = hi[e];
+          for (int t = 0; t < G::NS; ++t) row[t] = acc[b][t];
         }
-        if (old.p) unpack8(now[i], old.f32, o);
-        finish<F32, MODE, 8>(a, w.group, w.part, w.row0 + ms + r, n8, v, bias, old.p != nullptr, o);
+#pragma unroll
+      for (int i = 0; i < RUNS; i += H) {
+        float v[H][8], o[H][8];
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(row[2 * (i + h)][e]),
+                                                            __float_as_uint(row[2 * (i + h) + 1][e]), false, false);
+            v[h][e] = __uint_as_float(x[0]);
+            v[h][4 + e] = __uint_as_float(x[1]);
+          }
+        if (old.p) {
+          if constexpr (H == 2) {
+            if (!old.f32) {
+              u32x4_t u[2] = {now[i][0], now[i + 1][0]};
+              exchange8(u);
+              now[i][0] = u[0];
+              now[i + 1][0] = u[1];
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < H; ++h) unpack8(now[i + h], old.f32, o[h]);
+        }
+        auto add = [&](const float (&x)[8], int h) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[h][e] += x[e];
+        };
+        if constexpr (MODE == LIN_FORWARD) {
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (a.bias) add(bias[i + h], h);
+          if (a.pre) put(a.pre, 0, a.ldpre, F32, s, i, v);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            activate_run<F32>(a.act, v[h]);
+            if (old.p) add(o[h], h);
+          }
+          put(a.c, 0, a.ldc, F32, s, i, v);
+        } else if constexpr (MODE == LIN_INPUT) {
+          if (old.p) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) times_slope<F32>(a.act, o[h], v[h]);
+          }
+          put(a.c, 0, a.ldc, F32, s, i, v);
+        } else if (a.parts > 1) {
+          put(a.part, (static_cast<int64_t>(w.part) * a.groups + w.group) * a.m * a.n, a.n, true, s, i, v);
+        } else {
+          if (old.p) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) add(o[h], h);
+          }
+          put(a.c, w.group * a.gc, a.ldc, a.c_dt == DT_F32, s, i, v);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
+      for (int i = 0; i < RUNS; ++i)
 #pragma unroll
         for (int h = 0; h < OW; ++h) now[i][h] = next[i][h];
-      }
-    } else {
-      // Rows on no 16-byte borders: a lane per column.
+    }
+  } else {
+    // Rows on no 16-byte borders: through LDS, 32 rows at a time in a strip of
+    // the wave's own, then a lane per column.
+    __syncthreads();
+    constexpr int PER = G::UNIT / G::STRIP;   // strips of a unit
+    static_assert(PER * G::U >= G::NW, "strips fit the ring");
+    uint32_t base = 0;
+#pragma unroll
+    for (int b = 0; b < G::U; ++b)
+      base = wave / PER == b ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MUON_LDS char*)ring[b])) : base;
+    MUON_LDS float* strip = (MUON_LDS float*)(static_cast<uintptr_t>(base + (wave % PER) * G::STRIP));
+#pragma unroll 1
+    for (int s = 0; s < G::MS / 2; ++s) {
+      const int ms = row_p + s * 32;
+      if (ms >= w.m_valid) break;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int b = 0; b < G::MS; ++b)
+        if (b / 2 == s) {
+#pragma unroll
+          for (int t = 0; t < G::NS; ++t)
+            *(MUON_LDS f32x4_t*)(strip + (b % 2 * 16 + (lane & 15)) * G::SP + t * 16 + 4 * (lane >> 4)) = acc[b][t];
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll 4
       for (int i = lane; i < 32 * G::WN; i += 64) {
         const int r = i / G::WN, c = i % G::WN;
