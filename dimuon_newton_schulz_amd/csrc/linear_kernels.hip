@@ -645,6 +645,181 @@ struct Tile {
   int64_t row0;   // of c: a row (forward, input gradient) or an output feature
 };
 
+// A tile's part of a matrix in memory: rows m_valid, columns up to a.n; what
+// lies outside is neither read nor written (no branches, so that the stores
+// of one row of blocks need not end before the next one's begin).
+struct Window {
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t ld;     // bytes
+  bool f32;
+  __device__ __forceinline__ Window(const void* p, int64_t at, int64_t ld_elems, bool f32_, const LinArgs& a, const Tile& w)
+      : ld(static_cast<uint32_t>(ld_elems) * (f32_ ? 4 : 2)), f32(f32_) {
+    const uint32_t es = f32 ? 4 : 2, end = (w.m_valid - 1) * ld + (a.n - w.n0) * es;
+    rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(p)) + (at + w.row0 * ld_elems + w.n0) * es, 0, end, 0x00020000);
+  }
+  // Byte of row r, column n of the tile (at columns behind the matrix: nowhere).
+  __device__ __forceinline__ uint32_t at(int r, int n, int columns) const {
+    return n < columns ? r * ld + n * (f32 ? 4 : 2) : kNowhere;
+  }
+};
+
+// A tile's results from the accumulators to memory, where rows lie on 16-byte
+// borders.
+//
+// A lane holds columns 4 (l / 16) .. + 3 of row l mod 16 of each 16 x 16
+// block.  Swapping the odd rows of 16 lanes of one block with the even ones of
+// the next gives every lane a run of eight columns, without a way through LDS.
+// Two such runs, 32 columns apart, are handled together: in bf16 their halves
+// are exchanged (exchange8), so that an access covers whole 128-byte lines of
+// eight rows instead of half lines of sixteen.
+//
+// Old values come through the ring: every lane's go straight into LDS slots of
+// its own, a batch of block rows at a time, before the batch's first store.
+// The loop then waits for no memory: a wait for loads between the stores would
+// wait for the stores too (one counter), 1 us for each of a tile's block rows.
+template <bool F32, int MODE, typename G>
+__device__ __forceinline__ void leave(const LinArgs& a, const Tile& w, const Old<F32, MODE>& old, char* const (&ring)[G::U],
+                                      int row_p, int row_q, const f32x4_t (&acc)[G::MS][G::NS]) {
+  constexpr int RUNS = G::NS / 2, H = RUNS >= 2 ? 2 : 1, OW = F32 || MODE == LIN_WEIGHT ? 2 : 1;
+  constexpr int FIT = G::UNIT / (RUNS * OW * 1024), BATCH = FIT < G::MS ? FIT : G::MS;   // block rows in a unit
+  static_assert(BATCH >= 1 && G::U >= G::NW, "a unit per wave");
+  const int lane = threadIdx.x & 63, r16 = lane & 15, columns = a.n - w.n0;
+  const int c8 = row_q + 16 * (lane >> 4 & 1) + 8 * (lane >> 5);   // of the lane's first run
+  // Runs i .. i+H-1 of the 16 rows from block row s on: f(which, byte).  In
+  // halves (bf16, two runs): after exchange8.
+  auto each = [&](const Window& m, int s, int i, auto&& f) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const bool x = H == 2 && !m.f32;
+      f(h, m.at(row_p + s * 16 + (x ? (r16 & 7) + 8 * h : r16), c8 + 32 * (i + (x ? r16 >> 3 : h)), columns));
+    }
+  };
+  auto put = [&](const Window& m, int s, int i, const float (&v)[H][8]) {
+    u32x4_t u[H];
+    if (m.f32) {
+      each(m, s, i, [&](int h, uint32_t at) {
+        u32x4_t lo, hi;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          lo[e] = __float_as_uint(v[h][e]);
+          hi[e] = __float_as_uint(v[h][4 + e]);
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(lo, m.rs, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(hi, m.rs, at, 16, 0);
+      });
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) u[h] = pack8(v[h]);
+    if constexpr (H == 2) exchange8(u);
+    each(m, s, i, [&](int h, uint32_t at) { __builtin_amdgcn_raw_buffer_store_b128(u[h], m.rs, at, 0, 0); });
+  };
+  const bool parts = MODE == LIN_WEIGHT && a.parts > 1;
+  const Window to = parts ? Window(a.part, (static_cast<int64_t>(w.part) * a.groups + w.group) * a.m * a.n, a.n, true, a, w)
+                          : Window(a.c, MODE == LIN_WEIGHT ? w.group * a.gc : 0, a.ldc, MODE == LIN_WEIGHT ? a.c_dt == DT_F32 : F32, a, w);
+  const bool has_pre = MODE == LIN_FORWARD && a.pre;
+  const Window pre(has_pre ? a.pre : a.c, 0, a.ldpre, F32, a, w);
+  const Window from(old.p ? old.p : a.c, old.at, old.ld, old.f32, a, w);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t unit = 0;
+#pragma unroll
+  for (int b = 0; b < G::NW; ++b)
+    unit = wave == b ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MUON_LDS char*)ring[b])) : unit;
+  auto slot = [&](int s, int i, int o) { return unit + ((s % BATCH * RUNS + i) * OW + o) * 1024; };
+  float bias[MODE == LIN_FORWARD ? RUNS : 1][8];
+#pragma unroll
+  for (int i = 0; i < (MODE == LIN_FORWARD ? RUNS : 1); ++i) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bias[i][e] = 0.0f;
+    const int n = w.n0 + c8 + 32 * i;
+    if (MODE == LIN_FORWARD && a.bias && n < a.n) load_run(a.bias, static_cast<int64_t>(w.group) * a.n + n, F32, bias[i]);
+  }
+  if (old.p) __syncthreads();   // (the other waves have read the ring's last stage)
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the bias is here
+  // (One copy of what follows the sums, for all rows of blocks.)
+#pragma unroll 1
+  for (int s = 0; s < G::MS; ++s) {
+    if (row_p + s * 16 >= w.m_valid) break;
+    if (old.p && s % BATCH == 0) {
+#pragma unroll 1
+      for (int t = s; t < s + BATCH; ++t)
+#pragma unroll
+        for (int i = 0; i < RUNS; i += H)
+          each(from, t, i, [&](int h, uint32_t at) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(from.rs, (MUON_LDS void*)static_cast<uintptr_t>(slot(t, i + h, 0)), 16,
+                                                     at, 0, 0, 0);
+            if constexpr (OW == 2) {
+              if (from.f32)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(from.rs, (MUON_LDS void*)static_cast<uintptr_t>(slot(t, i + h, 1)),
+                                                         16, at + 16, 0, 0, 0);
+            }
+          });
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    }
+    f32x4_t row[G::NS];
+#pragma unroll
+    for (int b = 0; b < G::MS; ++b)
+      if (b == s) {
+#pragma unroll
+        for (int t = 0; t < G::NS; ++t) row[t] = acc[b][t];
+      }
+#pragma unroll
+    for (int i = 0; i < RUNS; i += H) {
+      float v[H][8], o[H][8];
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(row[2 * (i + h)][e]),
+                                                          __float_as_uint(row[2 * (i + h) + 1][e]), false, false);
+          v[h][e] = __uint_as_float(x[0]);
+          v[h][4 + e] = __uint_as_float(x[1]);
+        }
+      if (old.p) {
+        u32x4_t u[OW][H];
+#pragma unroll
+        for (int q = 0; q < OW; ++q)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            u[q][h] = *(const MUON_LDS u32x4_t*)static_cast<uintptr_t>(slot(s, i + h, q) + lane * 16);
+        if constexpr (H == 2) {
+          if (!from.f32) exchange8(u[0]);
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const u32x4_t both[2] = {u[0][h], u[OW - 1][h]};
+          unpack8(both, from.f32, o[h]);
+        }
+      }
+      auto add = [&](const float (&x)[8], int h) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[h][e] += x[e];
+      };
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        if constexpr (MODE == LIN_FORWARD) add(bias[i + h], h);
+        if constexpr (MODE == LIN_INPUT) {
+          if (old.p) times_slope<F32>(a.act, o[h], v[h]);
+        }
+        if constexpr (MODE == LIN_WEIGHT) {
+          if (old.p) add(o[h], h);
+        }
+      }
+      if (has_pre) put(pre, s, i, v);
+      if constexpr (MODE == LIN_FORWARD) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          activate_run<F32>(a.act, v[h]);
+          if (old.p) add(o[h], h);
+        }
+      }
+      put(to, s, i, v);
+    }
+  }
+}
+
 // One tile of at most G::BM x G::BN.
 template <bool F32, int MODE, typename G, int AL>
 __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* const (&ring)[G::U]) {
@@ -662,131 +837,7 @@ __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* cons
 
   const Old<F32, MODE> old(a, w.group);
   if constexpr (AL == 16) {
-    // A lane holds columns 4 (l / 16) .. + 3 of row l mod 16 of each 16 x 16
-    // block.  Swapping the odd rows of 16 lanes of one block with the even
-    // ones of the next gives every lane a run of eight columns, without a way
-    // through LDS.  Two such runs, 32 columns apart, are handled together: in
-    // bf16 their halves are exchanged (exchange8), so that an access covers
-    // whole 128-byte lines of eight rows instead of half lines of sixteen.
-    constexpr int RUNS = G::NS / 2, H = RUNS >= 2 ? 2 : 1, OW = F32 || MODE == LIN_WEIGHT ? 2 : 1;
-    const int r16 = lane & 15, n8 = w.n0 + row_q + 16 * (lane >> 4 & 1) + 8 * (lane >> 5);
-    // Runs i .. i+H-1 of the 16 rows from s on, to (and from) element
-    // at + row * ld + column.
-    auto each = [&](bool halves, int s, int i, auto&& f) {   // f(which, row, column)
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const bool x = H == 2 && halves;
-        const int r = row_p + s * 16 + (x ? (r16 & 7) + 8 * h : r16), n = n8 + 32 * (i + (x ? r16 >> 3 : h));
-        if (r < w.m_valid && n < a.n) f(h, r, n);
-      }
-    };
-    auto put = [&](void* p, int64_t at, int64_t ld, bool f32, int s, int i, const float (&v)[H][8]) {
-      if (f32) {
-        each(false, s, i, [&](int h, int r, int n) { store8(static_cast<char*>(p) + (at + (w.row0 + r) * ld + n) * 4, v[h], true); });
-        return;
-      }
-      u32x4_t u[H];
-#pragma unroll
-      for (int h = 0; h < H; ++h) u[h] = pack8(v[h]);
-      if constexpr (H == 2) exchange8(u);
-      each(true, s, i, [&](int h, int r, int n) {
-        *reinterpret_cast<MUON_GLOBAL u32x4_t*>(gmem(static_cast<char*>(p) + (at + (w.row0 + r) * ld + n) * 2)) = u[h];
-      });
-    };
-    float bias[MODE == LIN_FORWARD ? RUNS : 1][8];
-    if (MODE == LIN_FORWARD && a.bias) {
-#pragma unroll
-      for (int i = 0; i < RUNS; ++i)
-        if (n8 + 32 * i < a.n) load_run(a.bias, static_cast<int64_t>(w.group) * a.n + n8 + 32 * i, F32, bias[i]);
-    }
-    // Old values are read a row of blocks ahead (the compiler cannot move these
-    // reads before the stores, which may be to the same array).
-    u32x4_t now[RUNS][OW], next[RUNS][OW];
-    auto fetch = [&](int s, u32x4_t (&o)[RUNS][OW]) {
-#pragma unroll
-      for (int i = 0; i < RUNS; i += H)
-        each(!old.f32, s, i, [&](int h, int r, int n) {
-          const MUON_GLOBAL u32x4_t* p = reinterpret_cast<const MUON_GLOBAL u32x4_t*>(
-              gmem(static_cast<const char*>(old.p) + (old.at + (w.row0 + r) * old.ld + n) * (old.f32 ? 4 : 2)));
-          o[i + h][0] = p[0];
-          if constexpr (OW == 2) {
-            if (old.f32) o[i + h][1] = p[1];
-          }
-        });
-    };
-    if (old.p) fetch(0, now);
-    // (One copy of what follows the sums, for all rows of blocks.)
-#pragma unroll 1
-    for (int s = 0; s < G::MS; ++s) {
-      if (row_p + s * 16 >= w.m_valid) break;
-      if (old.p && s + 1 < G::MS) fetch(s + 1, next);
-      f32x4_t row[G::NS];
-#pragma unroll
-      for (int b = 0; b < G::MS; ++b)
-        if (b == s) {
-#pragma unroll
-          for (int t = 0; t < G::NS; ++t) row[t] = acc[b][t];
-        }
-#pragma unroll
-      for (int i = 0; i < RUNS; i += H) {
-        float v[H][8], o[H][8];
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(row[2 * (i + h)][e]),
-                                                            __float_as_uint(row[2 * (i + h) + 1][e]), false, false);
-            v[h][e] = __uint_as_float(x[0]);
-            v[h][4 + e] = __uint_as_float(x[1]);
-          }
-        if (old.p) {
-          if constexpr (H == 2) {
-            if (!old.f32) {
-              u32x4_t u[2] = {now[i][0], now[i + 1][0]};
-              exchange8(u);
-              now[i][0] = u[0];
-              now[i + 1][0] = u[1];
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < H; ++h) unpack8(now[i + h], old.f32, o[h]);
-        }
-        auto add = [&](const float (&x)[8], int h) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[h][e] += x[e];
-        };
-        if constexpr (MODE == LIN_FORWARD) {
-#pragma unroll
-          for (int h = 0; h < H; ++h)
-            if (a.bias) add(bias[i + h], h);
-          if (a.pre) put(a.pre, 0, a.ldpre, F32, s, i, v);
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            activate_run<F32>(a.act, v[h]);
-            if (old.p) add(o[h], h);
-          }
-          put(a.c, 0, a.ldc, F32, s, i, v);
-        } else if constexpr (MODE == LIN_INPUT) {
-          if (old.p) {
-#pragma unroll
-            for (int h = 0; h < H; ++h) times_slope<F32>(a.act, o[h], v[h]);
-          }
-          put(a.c, 0, a.ldc, F32, s, i, v);
-        } else if (a.parts > 1) {
-          put(a.part, (static_cast<int64_t>(w.part) * a.groups + w.group) * a.m * a.n, a.n, true, s, i, v);
-        } else {
-          if (old.p) {
-#pragma unroll
-            for (int h = 0; h < H; ++h) add(o[h], h);
-          }
-          put(a.c, w.group * a.gc, a.ldc, a.c_dt == DT_F32, s, i, v);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < RUNS; ++i)
-#pragma unroll
-        for (int h = 0; h < OW; ++h) now[i][h] = next[i][h];
-    }
+    leave<F32, MODE, G>(a, w, old, ring, row_p, row_q, acc);
   } else {
     // Rows on no 16-byte borders: through LDS, 32 rows at a time in a strip of
     // the wave's own, then a lane per column.
