@@ -73,13 +73,13 @@ __device__ __forceinline__ float slope(float z) {
   return s + z * s * (1.0f - s) * kTanhScale * (1.0f + 3.0f * kTanhCubic * z * z);
 }
 
-// v = act(v), and v *= act'(z): one branch for a run of values.
-template <bool EXACT, int N>
-__device__ __forceinline__ void activate_run(int act, float (&v)[N]) {
+// v = act(v), and v *= act'(z): one branch for H runs of N values.
+template <bool EXACT, int H, int N>
+__device__ __forceinline__ void activate_runs(int act, float (&v)[H][N]) {
 #define MUON_EACH(ACT)            \
   case ACT:                       \
     _Pragma("unroll")             \
-    for (int e = 0; e < N; ++e) v[e] = activate<ACT, EXACT>(v[e]); \
+    for (int e = 0; e < H * N; ++e) v[e / N][e % N] = activate<ACT, EXACT>(v[e / N][e % N]); \
     break
   switch (act) {
     MUON_EACH(LINEAR_RELU);
@@ -90,12 +90,12 @@ __device__ __forceinline__ void activate_run(int act, float (&v)[N]) {
   }
 #undef MUON_EACH
 }
-template <bool EXACT, int N>
-__device__ __forceinline__ void times_slope(int act, const float (&z)[N], float (&v)[N]) {
+template <bool EXACT, int H, int N>
+__device__ __forceinline__ void times_slopes(int act, const float (&z)[H][N], float (&v)[H][N]) {
 #define MUON_EACH(ACT)            \
   case ACT:                       \
     _Pragma("unroll")             \
-    for (int e = 0; e < N; ++e) v[e] *= slope<ACT, EXACT>(z[e]); \
+    for (int e = 0; e < H * N; ++e) v[e / N][e % N] *= slope<ACT, EXACT>(z[e / N][e % N]); \
     break
   switch (act) {
     MUON_EACH(LINEAR_RELU);
@@ -613,8 +613,9 @@ struct Old {
 // What becomes of N sums of row m (of the operands' rows; of the weight
 // gradient: an output feature) from column n on, in group g.
 template <bool F32, int MODE, int N>
-__device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_t m, int n, float (&v)[N],
-                                       const float (&bias)[N], bool has_old, const float (&old)[N]) {
+__device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_t m, int n, float (&run)[1][N],
+                                       const float (&bias)[N], bool has_old, const float (&old)[1][N]) {
+  float (&v)[N] = run[0];
   auto add = [&](const float (&b)[N]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) v[e] += b[e];
@@ -622,17 +623,17 @@ __device__ __forceinline__ void finish(const LinArgs& a, int g, int part, int64_
   if constexpr (MODE == LIN_FORWARD) {
     if (a.bias) add(bias);
     if (a.pre) store_run(a.pre, m * a.ldpre + n, F32, v);
-    activate_run<F32>(a.act, v);
-    if (has_old) add(old);
+    activate_runs<F32>(a.act, run);
+    if (has_old) add(old[0]);
     store_run(a.c, m * a.ldc + n, F32, v);
   } else if constexpr (MODE == LIN_INPUT) {
-    if (has_old) times_slope<F32>(a.act, old, v);
+    if (has_old) times_slopes<F32>(a.act, old, run);
     store_run(a.c, m * a.ldc + n, F32, v);
   } else if (a.parts > 1) {
     const int64_t at = (static_cast<int64_t>(part) * a.groups + g) * a.m + m;
     store_run(a.part, at * a.n + n, true, v);
   } else {
-    if (has_old) add(old);
+    if (has_old) add(old[0]);
     store_run(a.c, g * a.gc + m * a.ldc + n, a.c_dt == DT_F32, v);
   }
 }
@@ -678,7 +679,9 @@ struct Window {
 // its own, a batch of block rows at a time, before the batch's first store.
 // The loop then waits for no memory: a wait for loads between the stores would
 // wait for the stores too (one counter), 1 us for each of a tile's block rows.
-template <bool F32, int MODE, typename G>
+// PLAIN: the sums alone are the results, and all block rows are unrolled (the
+// loop's branches take half of its time).
+template <bool F32, int MODE, typename G, bool PLAIN>
 __device__ __forceinline__ void leave(const LinArgs& a, const Tile& w, const Old<F32, MODE>& old, char* const (&ring)[G::U],
                                       int row_p, int row_q, const f32x4_t (&acc)[G::MS][G::NS]) {
   constexpr int RUNS = G::NS / 2, H = RUNS >= 2 ? 2 : 1, OW = F32 || MODE == LIN_WEIGHT ? 2 : 1;
@@ -715,6 +718,18 @@ __device__ __forceinline__ void leave(const LinArgs& a, const Tile& w, const Old
     if constexpr (H == 2) exchange8(u);
     each(m, s, i, [&](int h, uint32_t at) { __builtin_amdgcn_raw_buffer_store_b128(u[h], m.rs, at, 0, 0); });
   };
+  // Runs i .. i+H-1 of a row of blocks.
+  auto turn = [&](const f32x4_t (&row)[G::NS], int i, float (&v)[H][8]) {
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(row[2 * (i + h)][e]),
+                                                        __float_as_uint(row[2 * (i + h) + 1][e]), false, false);
+        v[h][e] = __uint_as_float(x[0]);
+        v[h][4 + e] = __uint_as_float(x[1]);
+      }
+  };
   const bool parts = MODE == LIN_WEIGHT && a.parts > 1;
   const Window to = parts ? Window(a.part, (static_cast<int64_t>(w.part) * a.groups + w.group) * a.m * a.n, a.n, true, a, w)
                           : Window(a.c, MODE == LIN_WEIGHT ? w.group * a.gc : 0, a.ldc, MODE == LIN_WEIGHT ? a.c_dt == DT_F32 : F32, a, w);
@@ -737,6 +752,18 @@ __device__ __forceinline__ void leave(const LinArgs& a, const Tile& w, const Old
   }
   if (old.p) __syncthreads();   // (the other waves have read the ring's last stage)
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the bias is here
+  if constexpr (PLAIN) {
+#pragma unroll
+    for (int s = 0; s < G::MS; ++s) {
+#pragma unroll
+      for (int i = 0; i < RUNS; i += H) {
+        float v[H][8];
+        turn(acc[s], i, v);
+        put(to, s, i, v);
+      }
+    }
+    return;
+  }
   // (One copy of what follows the sums, for all rows of blocks.)
 #pragma unroll 1
   for (int s = 0; s < G::MS; ++s) {
@@ -759,24 +786,24 @@ __device__ __forceinline__ void leave(const LinArgs& a, const Tile& w, const Old
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     }
     f32x4_t row[G::NS];
+    auto take = [&](auto b) {
 #pragma unroll
-    for (int b = 0; b < G::MS; ++b)
-      if (b == s) {
-#pragma unroll
-        for (int t = 0; t < G::NS; ++t) row[t] = acc[b][t];
-      }
+      for (int t = 0; t < G::NS; ++t) row[t] = acc[b][t];
+    };
+    switch (s) {   // (accumulators have no run-time index)
+      case 0: take(std::integral_constant<int, 0>{}); break;
+      case 1: take(std::integral_constant<int, 1>{}); break;
+      case 2: take(std::integral_constant<int, (G::MS > 2 ? 2 : 0)>{}); break;
+      case 3: take(std::integral_constant<int, (G::MS > 3 ? 3 : 0)>{}); break;
+      case 4: take(std::integral_constant<int, (G::MS > 4 ? 4 : 0)>{}); break;
+      case 5: take(std::integral_constant<int, (G::MS > 5 ? 5 : 0)>{}); break;
+      case 6: take(std::integral_constant<int, (G::MS > 6 ? 6 : 0)>{}); break;
+      default: take(std::integral_constant<int, (G::MS > 7 ? 7 : 0)>{}); break;
+    }
 #pragma unroll
     for (int i = 0; i < RUNS; i += H) {
       float v[H][8], o[H][8];
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(row[2 * (i + h)][e]),
-                                                          __float_as_uint(row[2 * (i + h) + 1][e]), false, false);
-          v[h][e] = __uint_as_float(x[0]);
-          v[h][4 + e] = __uint_as_float(x[1]);
-        }
+      turn(row, i, v);
       if (old.p) {
         u32x4_t u[OW][H];
 #pragma unroll
@@ -797,23 +824,22 @@ __device__ __forceinline__ void leave(const LinArgs& a, const Tile& w, const Old
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[h][e] += x[e];
       };
+      if constexpr (MODE == LIN_INPUT) {
+        if (old.p) times_slopes<F32>(a.act, o, v);
+      }
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         if constexpr (MODE == LIN_FORWARD) add(bias[i + h], h);
-        if constexpr (MODE == LIN_INPUT) {
-          if (old.p) times_slope<F32>(a.act, o[h], v[h]);
-        }
         if constexpr (MODE == LIN_WEIGHT) {
           if (old.p) add(o[h], h);
         }
       }
       if (has_pre) put(pre, s, i, v);
       if constexpr (MODE == LIN_FORWARD) {
+        activate_runs<F32>(a.act, v);
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-          activate_run<F32>(a.act, v[h]);
+        for (int h = 0; h < H; ++h)
           if (old.p) add(o[h], h);
-        }
       }
       put(to, s, i, v);
     }
@@ -821,7 +847,7 @@ __device__ __forceinline__ void leave(const LinArgs& a, const Tile& w, const Old
 }
 
 // One tile of at most G::BM x G::BN.
-template <bool F32, int MODE, typename G, int AL>
+template <bool F32, int MODE, typename G, int AL, bool PLAIN>
 __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* const (&ring)[G::U]) {
   constexpr bool PKM = MODE == LIN_WEIGHT, QKM = MODE != LIN_FORWARD;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -837,7 +863,7 @@ __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* cons
 
   const Old<F32, MODE> old(a, w.group);
   if constexpr (AL == 16) {
-    leave<F32, MODE, G>(a, w, old, ring, row_p, row_q, acc);
+    leave<F32, MODE, G, PLAIN>(a, w, old, ring, row_p, row_q, acc);
   } else {
     // Rows on no 16-byte borders: through LDS, 32 rows at a time in a strip of
     // the wave's own, then a lane per column.
@@ -869,10 +895,10 @@ __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* cons
         const int r = i / G::WN, c = i % G::WN;
         const int n = w.n0 + row_q + c;
         if (ms + r >= w.m_valid || n >= a.n) continue;
-        float v[1] = {strip[r * G::SP + c]}, b1[1] = {0.0f}, o1[1] = {0.0f};
+        float v[1][1] = {{strip[r * G::SP + c]}}, b1[1] = {0.0f}, o1[1][1] = {{0.0f}};
         const int64_t m = w.row0 + ms + r;
         if (MODE == LIN_FORWARD && a.bias) load_run(a.bias, static_cast<int64_t>(w.group) * a.n + n, F32, b1);
-        if (old.p) load_run(old.p, old.at + m * old.ld + n, old.f32, o1);
+        if (old.p) load_run(old.p, old.at + m * old.ld + n, old.f32, o1[0]);
         finish<F32, MODE, 1>(a, w.group, w.part, m, n, v, b1, old.p != nullptr, o1);
       }
     }
@@ -880,7 +906,7 @@ __device__ __forceinline__ void tile(const LinArgs& a, const Tile& w, char* cons
 }
 
 // (Medium tiles run two workgroups on a CU.)
-template <bool F32, int MODE, typename G, int AL>
+template <bool F32, int MODE, typename G, int AL, bool PLAIN>
 __global__ __launch_bounds__(G::NT, G::UNIT * G::U <= 81920 ? 2 : 1) void k_linear(LinArgs a, int run) {
   constexpr int ES = F32 ? 4 : 2, LBK = KB / ES;
   // (Arrays of their own, so that the compiler can tell a read of one unit
@@ -935,27 +961,27 @@ __global__ __launch_bounds__(G::NT, G::UNIT * G::U <= 81920 ? 2 : 1) void k_line
   w.n_valid = min(G::BN, a.n - w.n0);
   if constexpr (G::U == 8) {
     char* const ring[8] = {unit0, unit1, unit2, unit3, unit4, unit5, unit6, unit7};
-    tile<F32, MODE, G, AL>(a, w, ring);
+    tile<F32, MODE, G, AL, PLAIN>(a, w, ring);
   } else if constexpr (G::U == 5) {
     char* const ring[5] = {unit0, unit1, unit2, unit3, unit4};
     // A tile that is less than half full in one direction takes half the time.
     if constexpr (G::BM == 256 && G::BN == 256) {
       if (w.n_valid <= 128) {
-        tile<F32, MODE, Geo<256, 128, 4, 1, 5, G::UNIT>, AL>(a, w, ring);
+        tile<F32, MODE, Geo<256, 128, 4, 1, 5, G::UNIT>, AL, PLAIN>(a, w, ring);
         return;
       }
       if (w.m_valid <= 128) {
-        tile<F32, MODE, Geo<128, 256, 1, 4, 5, G::UNIT>, AL>(a, w, ring);
+        tile<F32, MODE, Geo<128, 256, 1, 4, 5, G::UNIT>, AL, PLAIN>(a, w, ring);
         return;
       }
     }
-    tile<F32, MODE, G, AL>(a, w, ring);
+    tile<F32, MODE, G, AL, PLAIN>(a, w, ring);
   } else if constexpr (G::U == 4) {
     char* const ring[4] = {unit0, unit1, unit2, unit3};
-    tile<F32, MODE, G, AL>(a, w, ring);
+    tile<F32, MODE, G, AL, PLAIN>(a, w, ring);
   } else {
     char* const ring[2] = {unit0, unit1};
-    tile<F32, MODE, G, AL>(a, w, ring);
+    tile<F32, MODE, G, AL, PLAIN>(a, w, ring);
   }
 }
 
@@ -1017,16 +1043,16 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_linear_thin(LinArgs a) {
   __syncthreads();
   const int r = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
   if (r >= m_valid || n0 + c >= a.n) return;
-  float v[8];
+  float v[1][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    v[e] = sums[0][r][c + e];
+    v[0][e] = sums[0][r][c + e];
 #pragma unroll
-    for (int w = 1; w < kThinWaves; ++w) v[e] += sums[w][r][c + e];
+    for (int w = 1; w < kThinWaves; ++w) v[0][e] += sums[w][r][c + e];
   }
-  float bias[8], old[8];
+  float bias[8], old[1][8];
   if (a.bias) load_run(a.bias, static_cast<int64_t>(g.index) * a.n + n0 + c, F32, bias);
-  if (a.aux) load_run(a.aux, static_cast<int64_t>(row0 + r) * a.ldaux + n0 + c, F32, old);
+  if (a.aux) load_run(a.aux, static_cast<int64_t>(row0 + r) * a.ldaux + n0 + c, F32, old[0]);
   finish<F32, LIN_FORWARD, 8>(a, g.index, 0, row0 + r, n0 + c, v, bias, a.aux != nullptr, old);
 }
 
@@ -1052,11 +1078,11 @@ __global__ __launch_bounds__(kPassThreads) void k_linear_slope(const void* dy, i
        i += static_cast<int64_t>(gridDim.x) * kPassThreads) {
     const int64_t r = i / runs;
     const int c = static_cast<int>(i % runs) * N;
-    float g[N], z[N];
-    load_run(dy, r * ld_dy + c, F32, g);
-    load_run(pre, r * ld_pre + c, F32, z);
-    times_slope<F32>(act, z, g);
-    store_run(dz, r * ld_dz + c, F32, g);
+    float g[1][N], z[1][N];
+    load_run(dy, r * ld_dy + c, F32, g[0]);
+    load_run(pre, r * ld_pre + c, F32, z[0]);
+    times_slopes<F32>(act, z, g);
+    store_run(dz, r * ld_dz + c, F32, g[0]);
   }
 }
 
@@ -1140,14 +1166,14 @@ int64_t tiles_at_most(const LinArgs& a, int mode) {
   return mt * nt;
 }
 
-template <bool F32, int MODE, typename G, int AL>
+template <bool F32, int MODE, typename G, int AL, bool PLAIN = false>
 hipError_t go(const LinArgs& a, bool dry, hipStream_t s) {
   const int64_t tiles = tiles_at_most<G>(a, MODE);
   const int64_t run = std::max<int64_t>(1, std::min<int64_t>(32, tiles / 16));
   const int64_t blocks = ceil_of(tiles, 8 * run) * 8 * run;
   if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   if (blocks == 0 || dry) return hipSuccess;
-  hipLaunchKernelGGL((k_linear<F32, MODE, G, AL>), dim3(static_cast<uint32_t>(blocks)), dim3(G::NT), 0, s, a,
+  hipLaunchKernelGGL((k_linear<F32, MODE, G, AL, PLAIN>), dim3(static_cast<uint32_t>(blocks)), dim3(G::NT), 0, s, a,
                      static_cast<int>(run));
   return hipGetLastError();
 }
@@ -1172,6 +1198,12 @@ int64_t tiles_expected(const LinArgs& a, int mode) {
   const int64_t nt = ceil_of(a.n, G::BN);
   if (mode == LIN_WEIGHT || !a.offsets) return tiles_at_most<G>(a, mode);
   return std::max<int64_t>(1, a.rows / G::BM + a.groups / 2) * nt;
+}
+
+// Whether a product's sums alone are its result.
+bool plain(const LinArgs& a, int mode) {
+  if (mode == LIN_WEIGHT) return a.parts > 1 || !a.accumulate;
+  return !a.aux && (mode == LIN_INPUT || (!a.bias && !a.pre && a.act == LINEAR_NONE));
 }
 
 // The kernel of a product.  `align`: 16 (rows of whole 16-byte runs on 16-byte
@@ -1212,7 +1244,7 @@ hipError_t pick(const LinArgs& a, int dt, int align, bool dry, hipStream_t s) {
   // In units of time: a CU runs one Large tile, or two Medium ones at once,
   // which take 1.2 times as long per element.
   if (half_rounds(tiles_expected<Large>(a, MODE), 256) * 40 <= half_rounds(medium, 512) * 24)
-    return go<false, MODE, Large, 16>(a, dry, s);
+    return plain(a, MODE) ? go<false, MODE, Large, 16, true>(a, dry, s) : go<false, MODE, Large, 16>(a, dry, s);
   return go<false, MODE, Medium, 16>(a, dry, s);
 }
 
