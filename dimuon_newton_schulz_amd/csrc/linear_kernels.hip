@@ -1241,9 +1241,14 @@ hipError_t pick(const LinArgs& a, int dt, int align, bool dry, hipStream_t s) {
     if (mean <= 96) return go<false, MODE, Small, 16>(a, dry, s);
   }
   if (medium <= 256) return go<false, MODE, MediumDeep, 16>(a, dry, s);
-  // In units of time: a CU runs one Large tile, or two Medium ones at once,
-  // which take 1.2 times as long per element.
-  if (half_rounds(tiles_expected<Large>(a, MODE), 256) * 40 <= half_rounds(medium, 512) * 24)
+  // Time in units of a Large tile's step of k: a CU runs one Large tile, whose
+  // beginning and end take as long as 600 steps, or two Medium ones at once,
+  // 7/8 of a step (their fragment reads take the LDS 1.5 times as long as
+  // their products the matrix units) and no more.  Experts of 2048 x 1408, 1536
+  // rows each: 610 us (Large) against 711; 16384 rows, 768 x 768, residual: 34
+  // against 32.
+  const int64_t k = MODE == LIN_WEIGHT ? mean / a.parts : a.k;
+  if (half_rounds(tiles_expected<Large>(a, MODE), 256) * (k + 600) <= half_rounds(medium, 512) * (k * 7 / 8))
     return plain(a, MODE) ? go<false, MODE, Large, 16, true>(a, dry, s) : go<false, MODE, Large, 16>(a, dry, s);
   return go<false, MODE, Medium, 16>(a, dry, s);
 }
