@@ -23,6 +23,8 @@ decltype(&expert_gather) f_gather = nullptr;
 decltype(&expert_combine) f_combine = nullptr;
 decltype(&expert_combine_grad) f_combine_grad = nullptr;
 decltype(&linear_forward) f_linear = nullptr;
+decltype(&linear_grad_workspace_bytes) f_grad_bytes = nullptr;
+decltype(&linear_grad) f_grad = nullptr;
 
 constexpr int64_t kSortAlone = 8192, kMaxExperts = 1024, kMaxStride = int64_t{1} << 20;
 
@@ -288,15 +290,112 @@ PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Row and group strides of a weight (or its gradient) of groups x out x in.
+bool weight_strides(const at::Tensor* t, int dims, int64_t groups, int64_t out, int64_t in, int64_t& ld, int64_t& group) {
+  if (!t || t->dim() != dims || t->size(dims - 2) != out || t->size(dims - 1) != in || t->stride(dims - 1) != 1 ||
+      (dims == 3 && t->size(0) != groups))
+    return false;
+  ld = t->stride(dims - 2);
+  group = dims == 3 ? t->stride(0) : out * ld;
+  return ld >= in && group >= out * ld;
+}
+
+// dy, x, w, activation, pre, offsets, dx, dw, db (tensors or None), accumulate
+// (bool), x_activation, x_pre, workspace (tensor or None)
+PyObject* py_linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const int gpu = current_gpu();
+  MUON_ORDINARY(n == 13 && f_grad && f_grad_bytes && PyLong_Check(a[3]) && PyBool_Check(a[9]) && PyLong_Check(a[10]));
+  const at::Tensor* dy = tensor_on(a[0], gpu);
+  MUON_ORDINARY(dy && dy->dim() == 2 && dtype_of(*dy) >= 0);
+  const int dt = dtype_of(*dy);
+  linear_grad_args_t p{};
+  p.rows = dy->size(0);
+  p.out = dy->size(1);
+  p.dtype = dt;
+  p.grad_dtype = dt;
+  p.activation = static_cast<int32_t>(PyLong_AsLong(a[3]));
+  p.x_activation = static_cast<int32_t>(PyLong_AsLong(a[10]));
+  p.accumulate = a[9] == Py_True;
+  MUON_ORDINARY((p.dy_stride = row_stride(dy, p.rows, p.out, dt)) >= 0);
+  p.dy = dy->data_ptr();
+  // The weight, or its gradient, says what the groups and the columns are.
+  const at::Tensor* weight = tensor_on(a[2] != Py_None ? a[2] : a[7], gpu);
+  MUON_ORDINARY(weight && (weight->dim() == 2 || weight->dim() == 3));
+  const int d = static_cast<int>(weight->dim());
+  p.groups = d == 3 ? weight->size(0) : 1;
+  p.in = weight->size(d - 1);
+  if (a[5] != Py_None) {
+    const at::Tensor* t = tensor_on(a[5], gpu);
+    MUON_ORDINARY(ints(t, p.groups + 1) && t->dim() == 1);
+    p.offsets = static_cast<const int32_t*>(t->data_ptr());
+  }
+  MUON_ORDINARY(p.offsets || p.groups == 1);
+  if (p.activation) {
+    const at::Tensor* t = tensor_on(a[4], gpu);
+    MUON_ORDINARY((p.pre_stride = row_stride(t, p.rows, p.out, dt)) >= 0);
+    p.pre = t->data_ptr();
+  }
+  if (a[6] != Py_None) {
+    const at::Tensor *dx = tensor_on(a[6], gpu), *w = tensor_on(a[2], gpu);
+    MUON_ORDINARY(weight_strides(w, d, p.groups, p.out, p.in, p.w_stride, p.w_group_stride) && dtype_of(*w) == dt &&
+                  (p.dx_stride = row_stride(dx, p.rows, p.in, dt)) >= 0);
+    p.w = w->data_ptr();
+    p.dx = dx->data_ptr();
+    if (p.x_activation) {
+      const at::Tensor* t = tensor_on(a[11], gpu);
+      MUON_ORDINARY((p.x_pre_stride = row_stride(t, p.rows, p.in, dt)) >= 0);
+      p.x_pre = t->data_ptr();
+    }
+  }
+  if (a[7] != Py_None) {
+    const at::Tensor *dw = tensor_on(a[7], gpu), *x = tensor_on(a[1], gpu);
+    MUON_ORDINARY(weight_strides(dw, d, p.groups, p.out, p.in, p.dw_stride, p.dw_group_stride) && dtype_of(*dw) >= 0 &&
+                  (p.x_stride = row_stride(x, p.rows, p.in, dt)) >= 0);
+    p.grad_dtype = dtype_of(*dw);
+    p.x = x->data_ptr();
+    p.dw = dw->data_ptr();
+  }
+  if (a[8] != Py_None) {
+    const at::Tensor* db = tensor_on(a[8], gpu);
+    MUON_ORDINARY(db && db->is_contiguous() && db->dim() == d - 1 && db->size(d - 2) == p.out &&
+                  db->numel() == p.groups * p.out && dtype_of(*db) >= 0 && (!p.dw || dtype_of(*db) == p.grad_dtype));
+    p.grad_dtype = dtype_of(*db);
+    p.db = db->data_ptr();
+  }
+  MUON_ORDINARY(p.dx || p.dw || p.db);
+  size_t bytes = 0;
+  muon_status_t st = f_grad_bytes(&p, &bytes);
+  MUON_ORDINARY(st == MUON_OK);
+  // A new workspace belongs to the current stream, where the kernels run: the
+  // allocator hands it out again behind them.
+  at::Tensor ws;
+  if (a[12] != Py_None) {
+    const at::Tensor* t = tensor_on(a[12], gpu);
+    MUON_ORDINARY(t && t->scalar_type() == at::kByte && t->is_contiguous());
+    ws = *t;
+  } else if (bytes) {
+    ws = at::empty({static_cast<int64_t>(bytes)}, dy->options().dtype(at::kByte));
+  }
+  void *w_ptr = ws.defined() ? ws.data_ptr() : nullptr, *s = stream_of(gpu);
+  const size_t w_bytes = ws.defined() ? static_cast<size_t>(ws.numel()) : 0;
+  st = released([&] { return f_grad(&p, w_ptr, w_bytes, s); });
+  if (st != MUON_OK) return PyLong_FromLong(st);
+  Py_RETURN_TRUE;
+  END_HANDLE_TH_ERRORS
+}
+
 // Addresses of the library's entry points, in this order: expert_sort,
-// expert_gather, expert_combine, expert_combine_grad, linear_forward.
+// expert_gather, expert_combine, expert_combine_grad, linear_forward,
+// linear_grad_workspace_bytes, linear_grad.
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
+  constexpr int kEntries = 7;
+  if (n != kEntries) {
+    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
     return nullptr;
   }
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
+  void* p[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "address 0");
@@ -308,13 +407,16 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   f_combine = reinterpret_cast<decltype(f_combine)>(p[2]);
   f_combine_grad = reinterpret_cast<decltype(f_combine_grad)>(p[3]);
   f_linear = reinterpret_cast<decltype(f_linear)>(p[4]);
+  f_grad_bytes = reinterpret_cast<decltype(f_grad_bytes)>(p[5]);
+  f_grad = reinterpret_cast<decltype(f_grad)>(p[6]);
   Py_RETURN_NONE;
 }
 
 #define MUON_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MUON_METHOD(bind),         MUON_METHOD(sort),   MUON_METHOD(gather), MUON_METHOD(combine),
-                         MUON_METHOD(combine_grad), MUON_METHOD(linear), {nullptr, nullptr, 0, nullptr}};
+                         MUON_METHOD(combine_grad), MUON_METHOD(linear), MUON_METHOD(linear_grad),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -238,15 +238,17 @@ __device__ __forceinline__ int place_of(const MoveArgs& a, int64_t slot) {
 // Choices of a token that are handled at once, their rows' loads in flight together.
 constexpr int kAtOnce = 8;
 
-// Places (and weights) of the choices j0 .. j0 + 7 of the token whose slots
+// Places (and weights) of the choices j0 .. j0 + N - 1 of the token whose slots
 // start at `slot0`; -1 where there is none.
-__device__ __forceinline__ void places_of(const MoveArgs& a, int64_t slot0, int j0, int (&p)[kAtOnce]) {
+template <int N>
+__device__ __forceinline__ void places_of(const MoveArgs& a, int64_t slot0, int j0, int (&p)[N]) {
 #pragma unroll
-  for (int j = 0; j < kAtOnce; ++j) p[j] = j0 + j < a.top ? place_of(a, slot0 + j0 + j) : -1;
+  for (int j = 0; j < N; ++j) p[j] = j0 + j < a.top ? place_of(a, slot0 + j0 + j) : -1;
 }
-__device__ __forceinline__ void weights_of(const MoveArgs& a, int64_t slot0, int j0, float (&w)[kAtOnce]) {
+template <int N>
+__device__ __forceinline__ void weights_of(const MoveArgs& a, int64_t slot0, int j0, float (&w)[N]) {
 #pragma unroll
-  for (int j = 0; j < kAtOnce; ++j)
+  for (int j = 0; j < N; ++j)
     w[j] = j0 + j < a.top && a.weights ? load_elem(a.weights, slot0 + j0 + j, a.w_dt) : 1.0f;
 }
 
@@ -311,70 +313,70 @@ __global__ __launch_bounds__(kMoveThreads) void k_expert_combine(MoveArgs a, int
 }
 
 // dys[place[t][j]] = w[t][j] dy[t];  dw[t][j] = <dy[t], ys[place[t][j]]>: WPT
-// waves per token (four for wide rows, one for narrow ones).
-template <typename T, bool VEC, int WPT>
+// waves per token (four for wide rows, one for narrow ones) and N of its
+// choices (all together where tokens are many; one, where that many waves
+// would not fill the GPU).
+template <typename T, bool VEC, int WPT, int N>
 __global__ __launch_bounds__(kMoveThreads) void k_expert_combine_grad(MoveArgs a, int runs) {
   using R = Run<T, VEC>;
   constexpr int TPW = kMoveThreads / 64 / WPT, LANES = 64 * WPT;   // tokens of a workgroup, threads of a token
-  __shared__ float red[kAtOnce][kMoveThreads / 64];
-  const int wave = threadIdx.x >> 6, thread = threadIdx.x % LANES;
+  __shared__ float red[N][kMoveThreads / 64];
+  const int wave = threadIdx.x >> 6, thread = threadIdx.x % LANES, j0 = blockIdx.y * N;
   const int64_t groups = (static_cast<int64_t>(a.tokens) + TPW - 1) / TPW;
   for (int64_t b = blockIdx.x; b < groups; b += gridDim.x) {
     const int64_t t = b * TPW + wave / WPT;
     const bool in = t < a.tokens;
-    for (int j0 = 0; j0 < a.top; j0 += kAtOnce) {
-      float dot[kAtOnce];
+    float dot[N];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) dot[j] = 0.0f;
-      if (in) {
-        int p[kAtOnce];
-        float w[kAtOnce];
-        places_of(a, t * a.top, j0, p);
-        weights_of(a, t * a.top, j0, w);
-        for (int c = thread; c < runs; c += LANES) {
-          const int col = c * R::V;
-          R g;
-          typename R::Raw x[kAtOnce];
-          g.load(static_cast<const T*>(a.tok) + t * a.tok_ld + col);
+    for (int j = 0; j < N; ++j) dot[j] = 0.0f;
+    if (in) {
+      int p[N];
+      float w[N];
+      places_of(a, t * a.top, j0, p);
+      weights_of(a, t * a.top, j0, w);
+      for (int c = thread; c < runs; c += LANES) {
+        const int col = c * R::V;
+        R g;
+        typename R::Raw x[N];
+        g.load(static_cast<const T*>(a.tok) + t * a.tok_ld + col);
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j)
-            if (p[j] >= 0) x[j] = R::read(static_cast<const T*>(a.rows) + p[j] * a.rows_ld + col);
+        for (int j = 0; j < N; ++j)
+          if (p[j] >= 0) x[j] = R::read(static_cast<const T*>(a.rows) + p[j] * a.rows_ld + col);
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) {
-            if (p[j] < 0) continue;
-            R v;
-            v.set(x[j]);
+        for (int j = 0; j < N; ++j) {
+          if (p[j] < 0) continue;
+          R v;
+          v.set(x[j]);
 #pragma unroll
-            for (int e = 0; e < R::V; ++e) {
-              dot[j] = __builtin_fmaf(g.v[e], v.v[e], dot[j]);
-              v.v[e] = g.v[e] * w[j];
-            }
-            v.store(static_cast<T*>(a.rows_out) + p[j] * a.rows_out_ld + col);
+          for (int e = 0; e < R::V; ++e) {
+            dot[j] = __builtin_fmaf(g.v[e], v.v[e], dot[j]);
+            v.v[e] = g.v[e] * w[j];
           }
+          v.store(static_cast<T*>(a.rows_out) + p[j] * a.rows_out_ld + col);
         }
       }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        dot[j] = wave_tree_sum(dot[j]);
-        if (WPT > 1 && (threadIdx.x & 63) == 0) red[j][wave] = dot[j];
-      }
-      if constexpr (WPT > 1) __syncthreads();
-      if (thread < kAtOnce && in && j0 + thread < a.top) {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          float v = dot[j];
-          if constexpr (WPT > 1) {
-            v = red[j][wave / WPT * WPT];
-#pragma unroll
-            for (int w = 1; w < WPT; ++w) v += red[j][wave / WPT * WPT + w];
-          }
-          s = j == thread ? v : s;
-        }
-        store_elem(a.dweights, t * a.top + j0 + thread, a.w_dt, s);
-      }
-      if constexpr (WPT > 1) __syncthreads();
     }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      dot[j] = wave_tree_sum(dot[j]);
+      if (WPT > 1 && (threadIdx.x & 63) == 0) red[j][wave] = dot[j];
+    }
+    if constexpr (WPT > 1) __syncthreads();
+    if (thread < N && in && j0 + thread < a.top) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        float v = dot[j];
+        if constexpr (WPT > 1) {
+          v = red[j][wave / WPT * WPT];
+#pragma unroll
+          for (int w = 1; w < WPT; ++w) v += red[j][wave / WPT * WPT + w];
+        }
+        s = j == thread ? v : s;
+      }
+      store_elem(a.dweights, t * a.top + j0 + thread, a.w_dt, s);
+    }
+    if constexpr (WPT > 1) __syncthreads();
   }
 }
 
@@ -446,12 +448,23 @@ hipError_t launch_expert_combine(const MoveArgs& a, int dt, bool vec, hipStream_
 }
 hipError_t launch_expert_combine_grad(const MoveArgs& a, int dt, bool vec, hipStream_t s) {
   const bool wide = a.width / (vec ? (dt == DT_BF16 ? 8 : 4) : 1) > 128;
-  const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(kMaxBlocks, wide ? a.tokens : (a.tokens + 3) / 4)));
+  const int64_t blocks = std::min<int64_t>(kMaxBlocks, wide ? a.tokens : (a.tokens + 3) / 4);
+  // (1009 tokens of three choices, 769 float32: 7.0 us one by one, 8.2
+  // together; 16384 of six, 2048 bf16: 178 against 168.)
+  const bool one = blocks <= 2048 && a.top <= 65535;
+  const int n = one ? 1 : kAtOnce;
+  const dim3 grid(static_cast<uint32_t>(blocks), static_cast<uint32_t>((a.top + n - 1) / n));
 #define MUON_GRAD(T, VEC)                                                                                              \
   do {                                                                                                                 \
     const int runs = runs_of<T>(a, VEC);                                                                               \
-    if (wide) hipLaunchKernelGGL((k_expert_combine_grad<T, VEC, 4>), grid, dim3(kMoveThreads), 0, s, a, runs);         \
-    else hipLaunchKernelGGL((k_expert_combine_grad<T, VEC, 1>), grid, dim3(kMoveThreads), 0, s, a, runs);              \
+    if (wide && one)                                                                                                   \
+      hipLaunchKernelGGL((k_expert_combine_grad<T, VEC, 4, 1>), grid, dim3(kMoveThreads), 0, s, a, runs);              \
+    else if (wide)                                                                                                     \
+      hipLaunchKernelGGL((k_expert_combine_grad<T, VEC, 4, kAtOnce>), grid, dim3(kMoveThreads), 0, s, a, runs);        \
+    else if (one)                                                                                                      \
+      hipLaunchKernelGGL((k_expert_combine_grad<T, VEC, 1, 1>), grid, dim3(kMoveThreads), 0, s, a, runs);              \
+    else                                                                                                               \
+      hipLaunchKernelGGL((k_expert_combine_grad<T, VEC, 1, kAtOnce>), grid, dim3(kMoveThreads), 0, s, a, runs);        \
   } while (0)
   if (dt == DT_BF16) {
     if (vec) MUON_GRAD(uint16_t, true); else MUON_GRAD(uint16_t, false);

@@ -71,7 +71,8 @@ def bind(lib):
     except ImportError as e:
         raise RuntimeError(f"{__package__}._binding is missing: build it with `python -m {__package__}.build`") from e
     _binding.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in
-                    ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "linear_forward")))
+                    ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "linear_forward",
+                     "linear_grad_workspace_bytes", "linear_grad")))
     _fast = _binding
 
 
@@ -452,6 +453,12 @@ def linear_grad(dy: torch.Tensor, x: Optional[torch.Tensor] = None, w: Optional[
     through the activation that made x, so that dx becomes the gradient of
     x_pre.  Returns (dx, dw, db)."""
     act, x_act = _activation(activation), _activation(x_activation)
+    if stream is None and accumulate.__class__ is bool:
+        done = _native().linear_grad(dy, x, w, act, pre, offsets, dx, dw, db, accumulate, x_act, x_pre, workspace)
+        if done is not None:
+            if done is not True:
+                _check(done)
+            return dx, dw, db
     if dx is None and dw is None and db is None:
         raise ValueError("give at least one of dx, dw and db")
     (rows, n), dt = _matrix(dy, "dy")

@@ -421,7 +421,7 @@ def test_native_and_python_marshalling_refuse_alike():
 def stage_reads(code):
     """(16-byte reads, transposing reads) on every path from one barrier to the
     next that multiplies and reads fragments.  A path ends where the epilogue
-    begins to write LDS."""
+    begins (it takes the accumulators out, turns or writes them)."""
     place = {address: i for i, (address, _, _) in enumerate(code)}
     counts, seen = set(), set()
     todo = [(i + 1, 0, 0, 0) for i, (_, text, _) in enumerate(code) if text.split()[0] == "s_barrier"]
@@ -439,7 +439,7 @@ def stage_reads(code):
             if mfma and (wide or turned):
                 counts.add((wide, turned))
             continue
-        if op == "s_endpgm" or op.startswith("ds_write"):
+        if op == "s_endpgm" or op.startswith(("ds_write", "v_permlane16_swap", "v_accvgpr_read", "buffer_store")):
             continue
         wide, turned, mfma = wide + (op == "ds_read_b128"), turned + (op == "ds_read_b64_tr_b16"), mfma + op.startswith("v_mfma")
         if op == "s_branch":
