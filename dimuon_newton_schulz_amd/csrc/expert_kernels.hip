@@ -3,6 +3,12 @@
 // A token's choice j is slot t * top + j.  The sort is stable: an expert's
 // rows lie in the order of their slots, so results repeat bit for bit and no
 // atomic decides a place.
+//
+// Sort: bound by latency (a launch and a few barriers: 48 slots 3.4 us, 98304
+// slots of 64 experts 12 us in two launches).  Rows: bound by memory; 16384
+// tokens of six choices, 2048 bf16: gather 91 us (5.2 TB/s), combine with
+// weights and residual 89 to 97 (5.5 to 6), its gradient 168 (5.2); a copy reaches 4.8 on
+// the same card, writes alone 6.8.
 #include <algorithm>
 #include <type_traits>
 

@@ -7,12 +7,25 @@
 //   weight gradient C(m, n) = sum_k dz[k][m] x[k][n]   both k-major, k the group's rows
 //
 // A BM x BN tile per workgroup; both operands go from global memory straight
-// into a ring of two LDS stages of 128 bytes of k per row (64 bf16 or 32
-// float32 values).  Buffer loads carry the bounds: their descriptor ends
-// with the operand, so that rows behind a group's last one, columns behind
-// the matrix and the ragged end of k arrive as zeros and no operand is
-// padded.  The products run with W's (or x's) fragment first, so that a lane
-// holds runs of four output columns of one row.
+// into a ring of LDS units, stages of 128 bytes of k per row (64 bf16 or 32
+// float32 values; whole lines: half lines cost the forward product 10%).
+// Buffer loads carry the bounds: their descriptor ends with the operand, so
+// that rows behind a group's last one, columns behind the matrix and the
+// ragged end of k arrive as zeros and no operand is padded.  The products run
+// with W's (or x's) fragment first, so that a lane holds runs of four output
+// columns of one row.
+//
+// What bounds the large tiles (256 x 256, four waves of 128 x 128, one per
+// SIMD): per stage and CU 2048 cycles of MFMA, 1024 of fragment reads and 512
+// of loads into LDS.  Eight waves of 128 x 64 read half as much again and
+// were held by the LDS.  The products are 16 x 16 x 32 (5% faster than
+// 32 x 32 x 16: half the accumulator traffic), and every step's order is
+// given (pace): without it the compiler put a step's reads behind its
+// products, before the wait.  A ring of five units gives one operand two
+// stages' time to arrive: 8192^3 bf16 985 -> 868 us forward, 999 -> 771 and
+// 834 -> 767 for the gradients (the library's: 725, 816, 957).  The GPU holds
+// about 1.6 GHz there, the matrix units busy 72% of cycles.  A tile costs
+// 10 us beside its k (16 with an activation, 20 with a residual).
 #include <algorithm>
 #include <type_traits>
 
@@ -1218,8 +1231,10 @@ hipError_t pick(const LinArgs& a, int dt, int align, bool dry, hipStream_t s) {
     // at three rows an expert, 85 against 100 at nine, 101 against 92 at twelve;
     // 4096 x 4096, one group: 19 us against 23 (SmallDeep) at 32 rows, 32
     // against 24 at 64.
-    if (align == 16 && (mean <= 10 || (mean <= 40 && small <= 256)))
-      return dt == DT_F32 ? go_thin<true>(a, dry, s) : go_thin<false>(a, dry, s);
+    if (align == 16 && (mean <= 10 || (mean <= 40 && small <= 256))) {
+      const hipError_t e = dt == DT_F32 ? go_thin<true>(a, dry, s) : go_thin<false>(a, dry, s);
+      if (e != hipErrorInvalidValue) return e;   // (more workgroups than a launch has: the tiles are larger)
+    }
   }
   if (dt == DT_F32) {
     // A float32 product is slow enough (an eighth of the bf16 rate) that small
