@@ -243,13 +243,13 @@ constexpr int KB = 128, NQ = 2;   // a stage's k: bytes, and steps of 32 (bf16) 
 // distinct banks.
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 // k-major operand, k-rows of B values: 16-byte chunk c of k-row r sits in slot
-// c ^ kswz(r).  bf16: the four k-rows of a transposing read (32 bytes of each)
-// on distinct banks; float32: the k-rows of a wave's four quarters.
+// c ^ kswz(r).  bf16: the four k-rows of a transposing read (32 bytes of each),
+// and those of the 16 lanes beside, eight k-rows on, on distinct banks; float32: the k-rows of a wave's four quarters.
 template <bool F32, int B>
 __device__ __forceinline__ int kswz(int row) {
   static_assert(B % 128 == 0 || B == 64, "k-rows of whole 64-bank lines, or half of one");
   if constexpr (F32) return 4 * ((row >> 2) & 3);
-  return (B == 64 ? 2 : 4) * (row & 3);
+  return (B == 64 ? 2 : 4) * (row & 3) ^ 2 * ((row >> 3) & 1);
 }
 
 template <int N>
