@@ -128,6 +128,7 @@ muon_status_t check_dtype(int32_t dt, const char* what) {
 muon_status_t check_counts(int64_t tokens, int32_t top, int32_t experts) {
   if (tokens < 0) return fail(MUON_ERR_INVALID_ARG, "tokens %lld < 0", (long long)tokens);
   if (top < 1) return fail(MUON_ERR_INVALID_ARG, "top %d < 1", top);
+  if (top > kMaxExperts) return fail(MUON_ERR_UNSUPPORTED, "top %d above %d", top, kMaxExperts);
   if (experts < 1) return fail(MUON_ERR_INVALID_ARG, "experts %d < 1", experts);
   if (experts > kMaxExperts) return fail(MUON_ERR_UNSUPPORTED, "experts %d above %d", experts, kMaxExperts);
   if (tokens > kMaxRows / top) return fail(MUON_ERR_UNSUPPORTED, "more than 2^30 slots");

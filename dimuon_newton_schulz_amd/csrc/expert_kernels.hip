@@ -457,7 +457,7 @@ hipError_t launch_expert_combine_grad(const MoveArgs& a, int dt, bool vec, hipSt
   const int64_t blocks = std::min<int64_t>(kMaxBlocks, wide ? a.tokens : (a.tokens + 3) / 4);
   // (1009 tokens of three choices, 769 float32: 7.0 us one by one, 8.2
   // together; 16384 of six, 2048 bf16: 178 against 168.)
-  const bool one = blocks <= 2048 && a.top <= 65535;
+  const bool one = blocks <= 2048;
   const int n = one ? 1 : kAtOnce;
   const dim3 grid(static_cast<uint32_t>(blocks), static_cast<uint32_t>((a.top + n - 1) / n));
 #define MUON_GRAD(T, VEC)                                                                                              \

@@ -494,8 +494,8 @@ void muon_grad_norm_plan_destroy(muon_grad_norm_plan_t* plan);
  * Rows have `width` consecutive elements of `dtype` and a stride in elements
  * (at least width, at most 2^20); rows of whole 16-byte runs on 16-byte
  * borders are the fast case.  weights and dweights are of weights_dtype, one
- * a slot.  Sorted buffers have `slots` rows.  Limits: 1 <= top, 1 <= experts
- * <= 1024, slots <= 2^30, width <= 65536; tokens = 0 is allowed (the sort
+ * a slot.  Sorted buffers have `slots` rows.  Limits: top and experts 1 ..
+ * 1024, slots <= 2^30, width <= 65536; tokens = 0 is allowed (the sort
  * then writes offsets only).  A written buffer overlaps no other buffer,
  * except that y may be the residual itself (same pointer and stride).
  * Entries of place outside 0 .. slots-1 count as -1, whatever wrote them.

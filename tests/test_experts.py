@@ -127,7 +127,7 @@ def fake_routes(tokens=100, top=2, experts=8):
     return X.ExpertRoutesC(BASE, BASE + STEP, BASE + 2 * STEP, tokens, top, experts)
 
 
-SORT_REFUSALS = {"null_ids": 1, "null_routes": 1, "null_place": 1, "tokens": 1, "top": 1, "experts0": 1, "experts_many": 6,
+SORT_REFUSALS = {"null_ids": 1, "null_routes": 1, "null_place": 1, "tokens": 1, "top": 1, "experts0": 1, "experts_many": 6, "top_many": 6,
                  "slots": 6, "id_bytes": 2, "alias": 4, "alias_ids": 4, "misaligned": 1, "ws_null": 3, "ws_small": 3,
                  "ws_misaligned": 3, "ws_alias": 4}
 
@@ -152,6 +152,8 @@ def test_expert_sort_refusals(kind):
         r.experts = 0
     elif kind == "experts_many":
         r.experts = 1025
+    elif kind == "top_many":
+        r.top = 1025
     elif kind == "slots":
         r.tokens, r.top = 1 << 29, 3
     elif kind == "id_bytes":
@@ -472,9 +474,10 @@ def test_expert_combine_grad(width, pad, dtype, w_dtype):
 
 
 @gpu
-@pytest.mark.parametrize("tokens,top", [(1, 1), (1, 8), (5000, 2)])
+@pytest.mark.parametrize("tokens,top", [(1, 1), (1, 8), (5000, 2), (3, 16), (2500, 11)])
 def test_expert_rows_sizes(tokens, top):
-    """One token, many tokens, and choices that are all dropped."""
+    """One token, many tokens, more choices than are handled at once, and
+    choices that are all dropped."""
     for drop in (0.0, 1.0):
         announce(f"rows {tokens} x {top}, drop {drop}")
         r, _, place = routed(tokens, top, 16, drop)
