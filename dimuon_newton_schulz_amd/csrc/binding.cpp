@@ -13,6 +13,7 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "muon_mi355x.h"
 
@@ -421,4 +422,16 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+#define MUON_TEXT_OF(x) #x
+#define MUON_TEXT(x) MUON_TEXT_OF(x)
+
+// The caller compares the versions that this was compiled against with the running ones.
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && (PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0 ||
+            PyModule_AddStringConstant(m, "python_version", MUON_TEXT(PY_MAJOR_VERSION) "." MUON_TEXT(PY_MINOR_VERSION)) < 0)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -10,6 +10,8 @@ on ``stream`` (the current stream if None) and can be captured into a graph.
 from __future__ import annotations
 
 import ctypes
+import sys
+import warnings
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -65,15 +67,6 @@ def bind(lib):
                        ("linear_grad", [ctypes.POINTER(LinearGradArgs), vp, size, vp])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
-    global _fast
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise RuntimeError(f"{__package__}._binding is missing: build it with `python -m {__package__}.build`") from e
-    _binding.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in
-                    ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "linear_forward",
-                     "linear_grad_workspace_bytes", "linear_grad")))
-    _fast = _binding
 
 
 # The ordinary case of a call (current GPU and stream, tensors as expected) is
@@ -82,9 +75,35 @@ def bind(lib):
 _fast = None
 
 
+class _NoBinding:
+    """In the extension module's place where there is none: every call goes on
+    in Python, which takes 7 to 10 us more of host time."""
+    sort = gather = combine = combine_grad = linear = linear_grad = staticmethod(lambda *args: None)
+
+
+def _load_binding(lib):
+    """The extension module, or _NoBinding if it is missing or was built for
+    another torch or Python: nothing else in the package needs it."""
+    try:
+        from . import _binding
+        made_for = _binding.torch_version, _binding.python_version
+        here = torch.__version__.split("+")[0], f"{sys.version_info.major}.{sys.version_info.minor}"
+        if made_for != here:
+            raise ImportError(f"built for torch {made_for[0]} and Python {made_for[1]}, not {here[0]} and {here[1]}")
+    except (ImportError, AttributeError) as e:
+        warnings.warn(f"{__package__}._binding cannot be used ({e}): short calls take longer on the host; build it with "
+                      f"`python -m {__package__}.build`", RuntimeWarning, stacklevel=4)
+        return _NoBinding
+    _binding.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in
+                    ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "linear_forward",
+                     "linear_grad_workspace_bytes", "linear_grad")))
+    return _binding
+
+
 def _native():
+    global _fast
     if _fast is None:
-        load_library()
+        _fast = _load_binding(load_library())
     return _fast
 
 
