@@ -68,10 +68,10 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, SOURCES))
-        binding.result()
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    binding.result()   # (the library is complete without it)
     return LIB
 
 

@@ -56,6 +56,21 @@ def test_module_of_another_build_is_not_used(monkeypatch, field, value):
         assert X._load_binding(D.load_library()) is not _binding
 
 
+def test_library_is_linked_before_a_module_that_does_not_build(monkeypatch):
+    from dimuon_newton_schulz_amd import build as B
+    commands = []
+
+    def no_module():
+        raise RuntimeError("no host compiler")
+
+    monkeypatch.setattr(B, "_run", lambda cmd: commands.append(cmd) or "")
+    monkeypatch.setattr(B, "build_binding", no_module)
+    monkeypatch.setattr(B.os, "replace", lambda a, b: None)
+    with pytest.raises(RuntimeError, match="no host compiler"):
+        B.build()
+    assert commands[-1][-len(B.SOURCES):] == [os.path.join(B.BUILD, s.replace(".hip", ".o")) for s in B.SOURCES]
+
+
 @gpu
 def test_calls_without_the_extension_module(monkeypatch):
     """The same bits as with it."""
