@@ -87,6 +87,13 @@ int linear_weight_parts(int64_t rows, int64_t out, int64_t in, int64_t groups);
 hipError_t launch_linear_slope(const void* dy, int64_t ld_dy, const void* pre, int64_t ld_pre, void* dz, int64_t ld_dz,
                                const int32_t* offsets, int groups, int64_t rows, int64_t out, int act, int dt, int align,
                                hipStream_t s);
+// The same for bf16, with the unrounded terms' column sums per tile of rows,
+// linear_slope_tiles x out; and db (a.c) (+)= the groups' sums of them.  a:
+// n = out, rows, groups, offsets, act; c, c_dt, accumulate.  dz may be NULL.
+int64_t linear_slope_tiles(int64_t rows, int64_t out, int64_t groups);
+hipError_t launch_linear_slope_sums(const LinArgs& a, const void* dy, int64_t ld_dy, const void* pre, int64_t ld_pre,
+                                    void* dz, int64_t ld_dz, float* sums, hipStream_t s);
+hipError_t launch_linear_sums(const LinArgs& a, const float* sums, hipStream_t s);
 int linear_bias_parts(int64_t rows, int64_t groups);
 bool linear_bias_fits(int64_t out, int64_t groups);
 // db (+)= column sums of every group's rows, in `parts` parts.

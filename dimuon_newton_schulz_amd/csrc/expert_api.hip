@@ -200,6 +200,7 @@ muon_status_t check_activation(int32_t act) {
 struct GradLayout {
   int64_t dz_ld = 0;
   int parts = 1, bias_parts = 1;
+  bool slope_sums = false;   // db from the pass that forms dz, whose terms are not rounded yet
   size_t dz = 0, part = 0, bias_part = 0, bytes = 0;
 };
 
@@ -219,7 +220,11 @@ muon_status_t grad_layout(const linear_grad_args_t* a, GradLayout& l) {
     l.part = at;
     if (l.parts > 1) at += round_up(l.parts * a->groups * a->out * a->in * 4, kAlign);
   }
-  if (a->db) {
+  if (a->db && a->activation != LINEAR_NONE && a->dtype == MUON_BF16) {
+    l.slope_sums = true;
+    l.bias_part = at;
+    at += round_up(linear_slope_tiles(a->rows, a->out, a->groups) * a->out * 4, kAlign);
+  } else if (a->db) {
     l.bias_parts = linear_bias_parts(a->rows, a->groups);
     l.bias_part = at;
     if (l.bias_parts > 1) at += round_up(l.bias_parts * a->groups * a->out * 4, kAlign);
@@ -471,9 +476,25 @@ muon_status_t linear_grad(const linear_grad_args_t* p, void* workspace, size_t w
     wt.part = reinterpret_cast<float*>(ws + l.part);
     if ((p->dx && !linear_fits(in, LIN_INPUT, p->dtype, align)) || (p->dw && !linear_fits(wt, LIN_WEIGHT, p->dtype, align)))
       return fail(MUON_ERR_UNSUPPORTED, "the product is too large");
-    if (p->db && !linear_bias_fits(p->out, p->groups)) return fail(MUON_ERR_UNSUPPORTED, "the bias is too large");
+    if (p->db && (!linear_bias_fits(p->out, p->groups) ||
+                  linear_slope_tiles(p->rows, p->out, p->groups) * ceil_div(p->out, 64) >= int64_t{1} << 30))
+      return fail(MUON_ERR_UNSUPPORTED, "the bias is too large");
+    LinArgs bias{};
+    bias.offsets = p->offsets;
+    bias.rows = in.rows;
+    bias.groups = in.groups;
+    bias.n = static_cast<int32_t>(p->out);
+    bias.act = p->activation;
+    bias.c = p->db;
+    bias.c_dt = p->grad_dtype;
+    bias.accumulate = p->accumulate;
+    float* const sums = reinterpret_cast<float*>(ws + l.bias_part);
     MUON_HOOK_START();
-    if (has_act && p->rows)
+    if (l.slope_sums && p->rows)
+      MUON_LAUNCH(MUON_LAUNCH_LINEAR_SLOPE,
+                  launch_linear_slope_sums(bias, p->dy, p->dy_stride, p->pre, p->pre_stride,
+                                           p->dx || p->dw ? ws + l.dz : nullptr, dz_ld, sums, s));
+    else if (has_act && p->rows)
       MUON_LAUNCH(MUON_LAUNCH_LINEAR_SLOPE,
                   launch_linear_slope(p->dy, p->dy_stride, p->pre, p->pre_stride, ws + l.dz, dz_ld, p->offsets,
                                       in.groups, p->rows, p->out, p->activation, p->dtype, align, s));
@@ -483,10 +504,12 @@ muon_status_t linear_grad(const linear_grad_args_t* p, void* workspace, size_t w
       if (l.parts > 1) MUON_HIP_TRY(launch_linear_join(wt, s));
       MUON_HIP_TRY(hook_record(MUON_LAUNCH_LINEAR_WEIGHT, s));
     }
-    if (p->db)
+    if (l.slope_sums)
+      MUON_LAUNCH(MUON_LAUNCH_LINEAR_BIAS, launch_linear_sums(bias, sums, s));
+    else if (p->db)
       MUON_LAUNCH(MUON_LAUNCH_LINEAR_BIAS,
                   launch_linear_bias(dz, dz_ld, p->offsets, in.groups, p->rows, p->out, p->db, p->dtype, p->grad_dtype,
-                                     p->accumulate, reinterpret_cast<float*>(ws + l.bias_part), l.bias_parts, s));
+                                     p->accumulate, sums, l.bias_parts, s));
     return launched();
   });
 }

@@ -1099,6 +1099,122 @@ __global__ __launch_bounds__(kPassThreads) void k_linear_slope(const void* dy, i
   }
 }
 
+// The same in bf16 where db is wanted too: the terms dy act'(pre) of one tile
+// of `per` rows and 64 N columns of a group are summed in float32 as they are
+// formed (dz, rounded for the matrix units, is only written; with random
+// signs its half steps would be sqrt(rows) 2^-9 of a term in db), and
+// k_linear_sums adds a group's tiles up.  Four waves take every fourth row,
+// four in flight.  N = 2 where rows lie on 4-byte borders.  Tiles of rows and
+// not parts of a group, so that one group with most rows is split as well.
+// 98304 rows of 64 groups, 1408 columns, silu: 118 us for db alone (4.7 TB/s;
+// with erfc's gelu the slopes bound it, 268); with dz 37 us more than
+// k_linear_slope without db.  Reading the rounded dz again took 140 more.
+constexpr int kSumThreads = 256;
+template <int N>
+__global__ __launch_bounds__(kSumThreads) void k_linear_slope_sums(LinArgs a, const void* dy, int64_t ld_dy,
+                                                                   const void* pre, int64_t ld_pre, void* dz,
+                                                                   int64_t ld_dz, int per, int tiles, float* sums) {
+  constexpr int NW = kSumThreads / 64, AHEAD = 4;
+  __shared__ float red[NW][64 * N];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, blocks = (a.n + 64 * N - 1) / (64 * N);
+  auto load = [&](const void* p, int64_t at, float (&v)[N][AHEAD], int i) {
+    if constexpr (N == 2) {
+      const uint32_t u = gmem(static_cast<const uint32_t*>(p))[at / 2];
+      v[0][i] = __uint_as_float(u << 16);
+      v[1][i] = __uint_as_float(u & 0xffff0000u);
+    } else {
+      v[0][i] = load_elem(p, at, DT_BF16);
+    }
+  };
+  Group g;
+  int local;
+  // (Offsets that decrease would name more than `tiles` tiles.)
+  for (int idx = blockIdx.x; idx < tiles * blocks && find_rows(a, idx, per, blocks, g, local); idx += gridDim.x) {
+    const int first = g.lo + local / blocks * per, last = min(g.hi, first + per), c0 = local % blocks * 64 * N;
+    const int c = c0 + lane * N;
+    float s[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e] = 0.0f;
+    if (c < a.n)
+      for (int r0 = first + wave; r0 < last; r0 += NW * AHEAD) {
+        float v[N][AHEAD], z[N][AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          const int64_t r = min(r0 + i * NW, last - 1);   // (behind the last row: read again, not added)
+          load(dy, r * ld_dy + c, v, i);
+          load(pre, r * ld_pre + c, z, i);
+        }
+        times_slopes<false>(a.act, z, v);
+        if (dz) {
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            const int64_t r = r0 + i * NW;
+            if (r >= last) break;
+            if constexpr (N == 2) gmem(static_cast<uint32_t*>(dz))[(r * ld_dz + c) / 2] = pack_bf16x2(v[0][i], v[1][i]);
+            else store_elem(dz, r * ld_dz + c, DT_BF16, v[0][i]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+#pragma unroll
+          for (int i = 1; i < AHEAD; ++i) v[e][i] = r0 + i * NW < last ? v[e][i] : 0.0f;
+          s[e] += (v[e][0] + v[e][1]) + (v[e][2] + v[e][3]);
+        }
+      }
+#pragma unroll
+    for (int e = 0; e < N; ++e) red[wave][lane * N + e] = s[e];
+    __syncthreads();
+    if (threadIdx.x < 64 * N && c0 + static_cast<int>(threadIdx.x) < a.n) {
+      float sum = red[0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) sum += red[w][threadIdx.x];
+      sums[static_cast<int64_t>(idx / blocks) * a.n + c0 + threadIdx.x] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+// db (+)= the sums of a group's tiles of `per` rows: a workgroup per 64 columns
+// of a group, whose sixteen waves take every sixteenth tile, four in flight,
+// and are added in wave order.  Each wave counts the tiles before the group's.
+constexpr int kJoinThreads = 1024;
+__global__ __launch_bounds__(kJoinThreads) void k_linear_sums(LinArgs a, const float* sums, int per, int most) {
+  constexpr int NW = kJoinThreads / 64, AHEAD = 4;
+  __shared__ float red[NW][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int blocks = (a.n + 63) / 64, g = blockIdx.x / blocks, c = blockIdx.x % blocks * 64 + lane;
+  auto tiles_of = [&](int i) {
+    const int lo = a.offsets ? clamped(gmem(a.offsets)[i], 0, a.rows) : 0;
+    const int hi = a.offsets ? clamped(gmem(a.offsets)[i + 1], lo, a.rows) : a.rows;
+    return (hi - lo + per - 1) / per;
+  };
+  int before = 0;
+  for (int i = lane; i < g; i += 64) before = min(most, before + tiles_of(i));
+  for (int d = 1; d < 64; d <<= 1) before = min(most, before + __shfl_xor(before, d));
+  const int tiles = min(tiles_of(g), most - before);   // (fewer where offsets decrease)
+  float s = 0.0f;
+  if (c < a.n)
+    for (int t0 = wave; t0 < tiles; t0 += NW * AHEAD) {
+      float v[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int t = t0 + i * NW;
+        v[i] = t < tiles ? gmem(sums)[static_cast<int64_t>(before + t) * a.n + c] : 0.0f;
+      }
+      s += (v[0] + v[1]) + (v[2] + v[3]);
+    }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < a.n) {
+    s = red[0][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) s += red[w][lane];
+    const int64_t at = static_cast<int64_t>(g) * a.n + c;
+    if (a.accumulate) s += load_elem(a.c, at, a.c_dt);
+    store_elem(a.c, at, a.c_dt, s);
+  }
+}
+
 // Column sums of a group's rows (or of one part of them): sixteen waves take
 // every sixteenth row, 64 columns each, eight rows in flight, and are added in
 // wave order.
@@ -1312,6 +1428,40 @@ hipError_t launch_linear_slope(const void* dy, int64_t ld_dy, const void* pre, i
     if (runs) MUON_SLOPE(false, 8); else MUON_SLOPE(false, 1);
   }
 #undef MUON_SLOPE
+  return hipGetLastError();
+}
+
+// Rows of a tile: 64 while they are few, at most 256.
+constexpr int64_t kSumTiles = 2048;
+static int slope_rows(int64_t rows, int64_t out) {
+  const int64_t blocks = ceil_of(out, 128);
+  return static_cast<int>(std::max<int64_t>(64, std::min<int64_t>(256, ceil_of(rows * blocks, kSumTiles * 64) * 64)));
+}
+// Tiles at most.  (Bounded so that fewer rows never have more: a workspace is
+// used for up to so many rows.)
+int64_t linear_slope_tiles(int64_t rows, int64_t out, int64_t groups) {
+  return std::max(std::min(rows / 64, kSumTiles / ceil_of(out, 128)), rows / 256) + groups;
+}
+
+hipError_t launch_linear_slope_sums(const LinArgs& a, const void* dy, int64_t ld_dy, const void* pre, int64_t ld_pre,
+                                    void* dz, int64_t ld_dz, float* sums, hipStream_t s) {
+  const bool pairs = a.n % 2 == 0 && ld_dy % 2 == 0 && ld_pre % 2 == 0 && reinterpret_cast<uintptr_t>(dy) % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(pre) % 4 == 0;
+  const int per = slope_rows(a.rows, a.n), tiles = static_cast<int>(linear_slope_tiles(a.rows, a.n, a.groups));
+  const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(tiles * ceil_of(a.n, pairs ? 128 : 64), 1 << 16)));
+  if (pairs)
+    hipLaunchKernelGGL(k_linear_slope_sums<2>, grid, dim3(kSumThreads), 0, s, a, dy, ld_dy, pre, ld_pre, dz, ld_dz, per,
+                       tiles, sums);
+  else
+    hipLaunchKernelGGL(k_linear_slope_sums<1>, grid, dim3(kSumThreads), 0, s, a, dy, ld_dy, pre, ld_pre, dz, ld_dz, per,
+                       tiles, sums);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_sums(const LinArgs& a, const float* sums, hipStream_t s) {
+  const dim3 grid(static_cast<uint32_t>(ceil_of(a.n, 64) * a.groups));   // (linear_bias_fits)
+  hipLaunchKernelGGL(k_linear_sums, grid, dim3(kJoinThreads), 0, s, a, sums, slope_rows(a.rows, a.n),
+                     static_cast<int>(linear_slope_tiles(a.rows, a.n, a.groups)));
   return hipGetLastError();
 }
 

@@ -554,7 +554,7 @@ muon_status_t expert_combine_grad(const void* dy, int64_t dy_stride, const void*
  * Products of bf16 values with float32 sums (MFMA), or of float32 values
  * (dtype F32).  y and pre are rounded once from float32, y from the unrounded
  * z.  dz is rounded to dtype before its products (it is an operand of the
- * matrix units).  Results repeat bit for bit.
+ * matrix units); db sums it unrounded.  Results repeat bit for bit.
  *
  * Strides are in elements, rows' elements consecutive, strides at most 2^20.
  * The fast case: in and out multiples of 8, rows and group strides on 16-byte
@@ -625,7 +625,7 @@ typedef struct linear_grad_args {
 } linear_grad_args_t;
 
 /* Workspace of linear_grad: dz (with an activation), and sums in parts where
- * a gradient's rows are split.  Checks sizes, not pointers. */
+ * a gradient's rows are split; fewer rows need no more.  Checks sizes, not pointers. */
 muon_status_t linear_grad_workspace_bytes(const linear_grad_args_t* args, size_t* bytes);
 muon_status_t linear_grad(const linear_grad_args_t* args, void* workspace, size_t workspace_bytes, void* stream);
 
