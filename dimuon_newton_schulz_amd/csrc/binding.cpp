@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -73,6 +74,14 @@ bool routes_of(PyObject* const* a, int gpu, expert_routes_t& r) {
   return true;
 }
 
+// Whether autograd would have to record a call on one of these arguments.
+bool recorded(PyObject* const* a, Py_ssize_t n) {
+  if (!c10::GradMode::is_enabled()) return false;
+  for (Py_ssize_t i = 0; i < n; ++i)
+    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) return true;
+  return false;
+}
+
 #define MUON_ORDINARY(cond) \
   do {                      \
     if (!(cond)) Py_RETURN_NONE; \
@@ -130,7 +139,7 @@ PyObject* py_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const int gpu = current_gpu();
   expert_routes_t r;
-  MUON_ORDINARY(n == 5 && f_gather && routes_of(a + 1, gpu, r));
+  MUON_ORDINARY(n == 5 && f_gather && !recorded(a, n) && routes_of(a + 1, gpu, r));
   const at::Tensor* x = tensor_on(a[0], gpu);
   MUON_ORDINARY(x && x->dim() == 2 && dtype_of(*x) >= 0);
   const int64_t width = x->size(1), slots = r.tokens * r.top;
@@ -166,7 +175,7 @@ PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const int gpu = current_gpu();
   expert_routes_t r;
-  MUON_ORDINARY(n == 7 && f_combine && routes_of(a + 1, gpu, r));
+  MUON_ORDINARY(n == 7 && f_combine && !recorded(a, n) && routes_of(a + 1, gpu, r));
   const at::Tensor* ys = tensor_on(a[0], gpu);
   MUON_ORDINARY(ys && ys->dim() == 2 && dtype_of(*ys) >= 0);
   const int64_t width = ys->size(1);
@@ -210,7 +219,7 @@ PyObject* py_combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const int gpu = current_gpu();
   expert_routes_t r;
-  MUON_ORDINARY(n == 8 && f_combine_grad && routes_of(a + 3, gpu, r));
+  MUON_ORDINARY(n == 8 && f_combine_grad && !recorded(a, 1) && routes_of(a + 3, gpu, r));
   const at::Tensor *dy = tensor_on(a[0], gpu), *ys = tensor_on(a[1], gpu), *w = tensor_on(a[2], gpu);
   const at::Tensor *dys = tensor_on(a[6], gpu), *dw = tensor_on(a[7], gpu);
   MUON_ORDINARY(ys && ys->dim() == 2 && dtype_of(*ys) >= 0);
@@ -235,7 +244,7 @@ PyObject* py_combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const int gpu = current_gpu();
-  MUON_ORDINARY(n == 8 && f_linear && PyLong_Check(a[3]));
+  MUON_ORDINARY(n == 8 && f_linear && !recorded(a, n) && PyLong_Check(a[3]));
   const at::Tensor *x = tensor_on(a[0], gpu), *w = tensor_on(a[1], gpu);
   MUON_ORDINARY(x && x->dim() == 2 && dtype_of(*x) >= 0 && w && (w->dim() == 2 || w->dim() == 3));
   const int dt = dtype_of(*x), d = static_cast<int>(w->dim());
@@ -306,7 +315,7 @@ bool weight_strides(const at::Tensor* t, int dims, int64_t groups, int64_t out, 
 PyObject* py_linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const int gpu = current_gpu();
-  MUON_ORDINARY(n == 13 && f_grad && f_grad_bytes && PyLong_Check(a[3]) && PyBool_Check(a[9]) && PyLong_Check(a[10]));
+  MUON_ORDINARY(n == 13 && f_grad && f_grad_bytes && !recorded(a, 1) && PyLong_Check(a[3]) && PyBool_Check(a[9]) && PyLong_Check(a[10]));
   const at::Tensor* dy = tensor_on(a[0], gpu);
   MUON_ORDINARY(dy && dy->dim() == 2 && dtype_of(*dy) >= 0);
   const int dt = dtype_of(*dy);

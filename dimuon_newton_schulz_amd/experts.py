@@ -5,6 +5,11 @@ gradients (``expert_*`` and ``linear_*`` of ``include/muon_mi355x.h``).
 Argument marshalling only, like the rest of the package.  Rows may be strided
 (``stride(1) == 1``); everything else is contiguous.  Calls are asynchronous
 on ``stream`` (the current stream if None) and can be captured into a graph.
+
+Autograd records none of these calls: each gradient is a call of its own.  An
+input that requires a gradient is therefore refused while autograd is on (as
+torch's functions with ``out=`` do); call under ``torch.no_grad()``, or from
+the forward and backward of a ``torch.autograd.Function``.
 """
 
 from __future__ import annotations
@@ -178,6 +183,15 @@ def _matrix(t, name):
     return t.shape, t.dtype
 
 
+def _unrecorded(call, gradient, **tensors):
+    """Refuses a call that autograd would have to record."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name} requires a gradient, but autograd does not record {call} ({gradient}): call it "
+                                 "under torch.no_grad() or on detached tensors")
+
+
 class _Launch:
     """Where a call runs: the GPU of its tensors and the launch stream."""
     __slots__ = ("index", "stream", "given")
@@ -313,6 +327,7 @@ def expert_gather(x: torch.Tensor, routes: ExpertRoutes, out: Optional[torch.Ten
         done = _native().gather(x, routes.offsets, routes.order, routes.place, out)
         if done is not None:
             return _done(done)
+    _unrecorded("expert_gather", "its gradient is expert_combine without weights", x=x, out=out)
     c, ref, index = _routes(routes)
     (_, width), dt = _matrix(x, "x")
     ld = _rows(x, "x", index, (c.tokens, width), dt)
@@ -341,6 +356,7 @@ def expert_combine(ys: torch.Tensor, routes: ExpertRoutes, weights: Optional[tor
         done = _native().combine(ys, routes.offsets, routes.order, routes.place, weights, residual, out)
         if done is not None:
             return _done(done)
+    _unrecorded("expert_combine", "its gradient is expert_combine_grad", ys=ys, weights=weights, residual=residual, out=out)
     c, ref, index = _routes(routes)
     (_, width), dt = _matrix(ys, "ys")
     ld = _rows(ys, "ys", index, (c.tokens * c.top, width), dt)
@@ -365,6 +381,7 @@ def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tenso
         done = _native().combine_grad(dy, ys, weights, routes.offsets, routes.order, routes.place, dys, dweights)
         if done is not None:
             return _done(done)
+    _unrecorded("expert_combine_grad", "a gradient itself", dy=dy)
     c, ref, index = _routes(routes)
     (_, width), dt = _matrix(ys, "ys")
     shape = (c.tokens * c.top, width)
@@ -435,6 +452,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
         done = _native().linear(x, w, bias, act, residual, offsets, pre, out)
         if done is not None:
             return _done(done)
+    _unrecorded("linear", "its gradient is linear_grad", x=x, w=w, bias=bias, residual=residual, pre=pre, out=out)
     (rows, k), dt = _matrix(x, "x")
     index = x.get_device()
     groups, n, k_w, ld_w, group_w = _weight(w, "w", index, dt)
@@ -478,6 +496,7 @@ def linear_grad(dy: torch.Tensor, x: Optional[torch.Tensor] = None, w: Optional[
             if done is not True:
                 _check(done)
             return dx, dw, db
+    _unrecorded("linear_grad", "a gradient itself", dy=dy)
     if dx is None and dw is None and db is None:
         raise ValueError("give at least one of dx, dw and db")
     (rows, n), dt = _matrix(dy, "dy")
