@@ -116,6 +116,11 @@ muon_status_t launched() {
   g_hook.last_count = g_hook.next;
   return MUON_OK;
 }
+// A call that has nothing to launch (and so records no event).
+muon_status_t no_launch() {
+  g_hook.next = 0;
+  return launched();
+}
 
 muon_status_t check_dtype(int32_t dt, const char* what) {
   if (dt != MUON_F32 && dt != MUON_BF16) return fail(MUON_ERR_DTYPE, "%s: unknown dtype %d", what, dt);
@@ -277,7 +282,7 @@ muon_status_t expert_gather(const void* x, int64_t x_stride, int64_t width, muon
     MUON_CHECK(check_routes(routes, b, false));
     MUON_CHECK(check_width(width));
     MoveArgs a = move_args(routes, width);
-    if (a.slots == 0) return MUON_OK;
+    if (a.slots == 0) return no_launch();
     const size_t es = dtype_size(dtype);
     MUON_CHECK(b.add(x, "x", a.tokens, width, x_stride, es, false));
     MUON_CHECK(b.add(xs, "xs", a.slots, width, xs_stride, es, true));
@@ -302,7 +307,7 @@ muon_status_t expert_combine(const void* ys, int64_t ys_stride, int64_t width, m
     MUON_CHECK(check_routes(routes, b, false));
     MUON_CHECK(check_width(width));
     MoveArgs a = move_args(routes, width);
-    if (a.slots == 0) return MUON_OK;
+    if (a.slots == 0) return no_launch();
     const size_t es = dtype_size(dtype);
     MUON_CHECK(b.add(ys, "ys", a.slots, width, ys_stride, es, false));
     if (weights) {
@@ -339,7 +344,7 @@ muon_status_t expert_combine_grad(const void* dy, int64_t dy_stride, const void*
     MUON_CHECK(check_routes(routes, b, false));
     MUON_CHECK(check_width(width));
     MoveArgs a = move_args(routes, width);
-    if (a.slots == 0) return MUON_OK;
+    if (a.slots == 0) return no_launch();
     const size_t es = dtype_size(dtype), ws = dtype_size(weights_dtype);
     MUON_CHECK(b.add(dy, "dy", a.tokens, width, dy_stride, es, false));
     MUON_CHECK(b.add(ys, "ys", a.slots, width, ys_stride, es, false));
@@ -367,7 +372,7 @@ muon_status_t linear_forward(const linear_args_t* p, void* stream) {
   return guarded([&]() -> muon_status_t {
     MUON_CHECK(check_sizes(p));
     MUON_CHECK(check_activation(p->activation));
-    if (p->rows == 0) return MUON_OK;
+    if (p->rows == 0) return no_launch();
     const size_t es = dtype_size(p->dtype);
     Buffers b;
     if (p->offsets) MUON_CHECK(b.list(p->offsets, "offsets", p->groups + 1, 4, false));
