@@ -427,6 +427,8 @@ muon_status_t linear_grad(const linear_grad_args_t* p, void* workspace, size_t w
   return guarded([&]() -> muon_status_t {
     GradLayout l;
     MUON_CHECK(grad_layout(p, l));
+    // (dx of no rows is an empty buffer, whose address may be NULL.)
+    if (!p->dx && !p->dw && !p->db && p->rows == 0) return no_launch();
     if (!p->dx && !p->dw && !p->db) return fail(MUON_ERR_INVALID_ARG, "none of dx, dw and db is given");
     const bool has_act = p->activation != LINEAR_NONE;
     const size_t es = dtype_size(p->dtype), gs = dtype_size(p->grad_dtype);
