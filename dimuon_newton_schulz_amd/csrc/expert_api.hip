@@ -26,14 +26,16 @@ struct Buffer {
 };
 
 // Whether two buffers may share a byte.  Rows of one stride that keep to
-// columns of their own (views of one wide buffer) do not.
+// columns of their own (views of one wide buffer) do not; a single row has any
+// stride.
 bool overlap(const Buffer& a, const Buffer& b) {
   if (a.empty() || b.empty() || a.end() <= b.at || b.end() <= a.at) return false;
-  if (a.stride == b.stride && a.groups == 1 && b.groups == 1 && a.rows > 1 && b.rows > 1) {
+  if ((a.stride == b.stride || a.rows == 1 || b.rows == 1) && a.groups == 1 && b.groups == 1) {
     const Buffer& lo = a.at <= b.at ? a : b;
     const Buffer& hi = a.at <= b.at ? b : a;
-    const int64_t d = static_cast<int64_t>((hi.at - lo.at) % static_cast<uintptr_t>(lo.stride));
-    if (lo.width <= d && d + hi.width <= lo.stride) return false;
+    const int64_t stride = a.rows > 1 ? a.stride : b.stride;
+    const int64_t d = static_cast<int64_t>((hi.at - lo.at) % static_cast<uintptr_t>(stride));
+    if (lo.width <= d && d + hi.width <= stride) return false;
   }
   return true;
 }
