@@ -110,3 +110,46 @@ def test_fewer_rows_need_no_larger_workspace():
             assert lib.linear_grad_workspace_bytes(ctypes.byref(a), ctypes.byref(n)) == 0
             assert n.value >= before, (rows, out, groups)
             before = n.value
+
+
+@gpu
+def test_bias_gradient_captured_and_on_two_streams():
+    """Replays of a captured backward, with eager work between them, and two
+    streams at once give the eager bits."""
+    announce("db captured, on two streams")
+    rows, inn, out, groups = 3000, 64, 136, 5
+    off = torch.linspace(0, rows, groups + 1, device="cuda").int()
+    dy, pre, x, w = (rows_of(rows, out, torch.bfloat16, 1), rows_of(rows, out, torch.bfloat16, 2),
+                     rows_of(rows, inn, torch.bfloat16, 3), weight(groups, out, inn, torch.bfloat16, 4))
+
+    def buffers():
+        return torch.zeros_like(x), torch.zeros(groups, out, inn, device="cuda"), torch.zeros(groups, out, device="cuda")
+
+    def backward(into, stream=None):
+        D.linear_grad(dy, x, w, "gelu", pre, off, *into, accumulate=True, stream=stream)
+
+    want = [buffers()]
+    for _ in range(3):   # (each adds to what the one before left)
+        want.append(tuple(t.clone() for t in want[-1]))
+        backward(want[-1])
+    into, eager = buffers(), buffers()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        backward(eager)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        backward(into)
+    for step in range(1, 4):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(into, want[step])), step
+        backward(eager)
+    two = [(buffers(), torch.cuda.Stream()) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for b, s in two:
+            backward(b, s)
+    torch.cuda.synchronize()
+    for b, _ in two:
+        assert all(torch.equal(a, t) for a, t in zip(b, want[3]))
