@@ -798,17 +798,32 @@ __device__ __forceinline__ void leave(const LinArgs& a, const Tile& w, const Old
       __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     }
-    // (Accumulators have no run-time index.  As a switch this left the Large
-    // kernels short of registers, and their main loops moved accumulators and
-    // spilled: the input gradient through x_pre 1125 instead of 603 us, 8192^3
-    // 1597 instead of 789.)
+    // Accumulators have no run-time index.  A switch is the shorter way to
+    // them (300 rows, 768 x 768: 7.9 instead of 8.7 us), but left the Large
+    // kernels short of registers: their main loops moved accumulators and
+    // spilled (the input gradient through x_pre 1125 instead of 603 us, 8192^3
+    // 1597 instead of 789).
     f32x4_t row[G::NS];
+    auto take = [&](auto b) {
 #pragma unroll
-    for (int b = 0; b < G::MS; ++b)
-      if (b == s) {
+      for (int t = 0; t < G::NS; ++t) row[t] = acc[b][t];
+    };
+    if constexpr (G::MS * G::NS > 16) {
 #pragma unroll
-        for (int t = 0; t < G::NS; ++t) row[t] = acc[b][t];
+      for (int b = 0; b < G::MS; ++b)
+        if (b == s) {
+#pragma unroll
+          for (int t = 0; t < G::NS; ++t) row[t] = acc[b][t];
+        }
+    } else {
+      static_assert(G::MS <= 4, "a case per row of blocks");
+      switch (s) {
+        case 0: take(std::integral_constant<int, 0>{}); break;
+        case 1: take(std::integral_constant<int, 1>{}); break;
+        case 2: take(std::integral_constant<int, (G::MS > 2 ? 2 : 0)>{}); break;
+        default: take(std::integral_constant<int, (G::MS > 3 ? 3 : 0)>{}); break;
       }
+    }
 #pragma unroll
     for (int i = 0; i < RUNS; i += H) {
       float v[H][8], o[H][8];
