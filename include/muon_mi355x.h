@@ -220,15 +220,15 @@ typedef enum muon_launch_kind {
   MUON_LAUNCH_STATE_GET = 15, /* AdamW moments to values */
   MUON_LAUNCH_STATE_SET = 16, /* values to AdamW moments */
   MUON_LAUNCH_GRAD_NORM = 17, /* global gradient norm */
-  MUON_LAUNCH_EXPERT_SORT = 18,    /* expert_sort (one or two kernels) */
+  MUON_LAUNCH_EXPERT_SORT = 18,    /* expert_sort (one to three kernels) */
   MUON_LAUNCH_EXPERT_GATHER = 19,
   MUON_LAUNCH_EXPERT_COMBINE = 20,
   MUON_LAUNCH_EXPERT_COMBINE_GRAD = 21,
   MUON_LAUNCH_LINEAR = 22,         /* linear_forward */
-  MUON_LAUNCH_LINEAR_SLOPE = 23,   /* linear_grad: dz */
+  MUON_LAUNCH_LINEAR_SLOPE = 23,   /* linear_grad: dz (and, in bf16, the column sums of its tiles for db) */
   MUON_LAUNCH_LINEAR_INPUT = 24,   /* linear_grad: dx */
   MUON_LAUNCH_LINEAR_WEIGHT = 25,  /* linear_grad: dW (and the sum of its parts) */
-  MUON_LAUNCH_LINEAR_BIAS = 26     /* linear_grad: db (and the sum of its parts) */
+  MUON_LAUNCH_LINEAR_BIAS = 26     /* linear_grad: db (and the sum of its parts or tiles) */
 } muon_launch_kind_t;
 
 /* Timing hook, per host thread; not part of the method.  When `events` is
@@ -498,7 +498,8 @@ void muon_grad_norm_plan_destroy(muon_grad_norm_plan_t* plan);
  * 1024, slots <= 2^30, width <= 65536; tokens = 0 is allowed (the sort
  * then writes offsets only).  A written buffer overlaps no other buffer,
  * except that y may be the residual itself (same pointer and stride).
- * Entries of place outside 0 .. slots-1 count as -1, whatever wrote them.
+ * Entries of place outside 0 .. slots-1 count as -1, whatever wrote them; a
+ * row that two of them name (expert_sort writes none such) is undefined.
  *
  * These calls allocate nothing and upload nothing: they may be captured.
  * The buffers are those of the stream's device, which is current.
