@@ -4,11 +4,11 @@
 // rows lie in the order of their slots, so results repeat bit for bit and no
 // atomic decides a place.
 //
-// Sort: bound by latency (a launch and a few barriers: 48 slots 3.4 us, 98304
+// Sort: bound by latency (a launch and a few barriers: 48 slots 3.7 us, 98304
 // slots of 64 experts 12 us in two launches).  Rows: bound by memory; 16384
 // tokens of six choices, 2048 bf16: gather 91 us (5.2 TB/s), combine with
-// weights and residual 89 to 97 (5.5 to 6), its gradient 168 (5.2); a copy reaches 4.8 on
-// the same card, writes alone 6.8.
+// weights and residual 88 to 97 (5.5 to 6.1), its gradient 174 (5.0); a copy
+// reaches 5.1 on the same card, writes alone 6.8.
 #include <algorithm>
 #include <type_traits>
 
@@ -455,8 +455,9 @@ hipError_t launch_expert_combine(const MoveArgs& a, int dt, bool vec, hipStream_
 hipError_t launch_expert_combine_grad(const MoveArgs& a, int dt, bool vec, hipStream_t s) {
   const bool wide = a.width / (vec ? (dt == DT_BF16 ? 8 : 4) : 1) > 128;
   const int64_t blocks = std::min<int64_t>(kMaxBlocks, wide ? a.tokens : (a.tokens + 3) / 4);
-  // (1009 tokens of three choices, 769 float32: 7.0 us one by one, 8.2
-  // together; 16384 of six, 2048 bf16: 178 against 168.)
+  // (One by one against together: 1009 tokens of three choices, 769 float32,
+  // 6.7 us against 7.7; 2048 of six, 2048 bf16, 17.4 against 20.0; 8192 of
+  // four, 96 bf16, 8.0 against 9.2; 16384 of six, 2048 bf16, 178 against 171.)
   const bool one = blocks <= 2048;
   const int n = one ? 1 : kAtOnce;
   const dim3 grid(static_cast<uint32_t>(blocks), static_cast<uint32_t>((a.top + n - 1) / n));

@@ -22,10 +22,12 @@
 // 32 x 32 x 16: half the accumulator traffic), and every step's order is
 // given (pace): without it the compiler put a step's reads behind its
 // products, before the wait.  A ring of five units gives one operand two
-// stages' time to arrive: 8192^3 bf16 985 -> 868 us forward, 999 -> 771 and
-// 834 -> 767 for the gradients (the library's: 725, 816, 957).  The GPU holds
-// about 1.6 GHz there, the matrix units busy 72% of cycles.  A tile costs
-// 10 us beside its k (16 with an activation, 20 with a residual).
+// stages' time to arrive (8 to 23% of the time at 8192^3).  8192^3 bf16 takes
+// 750 us, forward and for either gradient (the library's: 680, 791, 918).  The
+// GPU holds about 1.6 GHz there, the matrix units busy 73% of cycles.  A round
+// of tiles takes 21 us per 1024 of k, and beside its k 8 to 12 us for the sums
+// alone, 15 with an activation, 19 with a residual, 18 added to what dW holds
+// and 25 through x_pre.
 #include <algorithm>
 #include <type_traits>
 
@@ -1354,9 +1356,9 @@ hipError_t pick(const LinArgs& a, int dt, int align, bool dry, hipStream_t s) {
   const int64_t mean = a.rows / a.groups;   // rows of a group
   if constexpr (MODE == LIN_FORWARD) {
     // Few rows: every 16 of a group's read its weight again (from the L2 or
-    // the Infinity Cache).  64 experts of 2048 x 1408: 66 us against 97 (Small)
-    // at three rows an expert, 85 against 100 at nine, 101 against 92 at twelve;
-    // 4096 x 4096, one group: 19 us against 23 (SmallDeep) at 32 rows, 32
+    // the Infinity Cache).  64 experts of 2048 x 1408: 69 us against 92 (Small)
+    // at three rows an expert, 84 against 99 at nine, 95 against 100 at twelve;
+    // 4096 x 4096, one group: 18 us against 22 (SmallDeep) at 32 rows, 31
     // against 24 at 64.
     if (align == 16 && (mean <= 10 || (mean <= 40 && small <= 256))) {
       const hipError_t e = dt == DT_F32 ? go_thin<true>(a, dry, s) : go_thin<false>(a, dry, s);
@@ -1387,8 +1389,9 @@ hipError_t pick(const LinArgs& a, int dt, int align, bool dry, hipStream_t s) {
   // beginning and end take as long as 600 steps, or two Medium ones at once,
   // 7/8 of a step (their fragment reads take the LDS 1.5 times as long as
   // their products the matrix units) and no more.  Experts of 2048 x 1408, 1536
-  // rows each: 610 us (Large) against 711; 16384 rows, 768 x 768, residual: 34
-  // against 32.
+  // rows each: 562 us (Large) against 663, with silu, pre and residual 641
+  // against 736; 16384 rows, 768 x 768: 24.5 against 26.9, with silu, pre and
+  // residual 35.7 against 33.6.
   const int64_t k = MODE == LIN_WEIGHT ? mean / a.parts : a.k;
   if (half_rounds(tiles_expected<Large>(a, MODE), 256) * (k + 600) <= half_rounds(medium, 512) * (k * 7 / 8))
     return plain(a, MODE) ? go<false, MODE, Large, 16, true>(a, dry, s) : go<false, MODE, Large, 16>(a, dry, s);
