@@ -485,8 +485,8 @@ muon_status_t linear_grad(const linear_grad_args_t* p, void* workspace, size_t w
     wt.part = reinterpret_cast<float*>(ws + l.part);
     if ((p->dx && !linear_fits(in, LIN_INPUT, p->dtype, align)) || (p->dw && !linear_fits(wt, LIN_WEIGHT, p->dtype, align)))
       return fail(MUON_ERR_UNSUPPORTED, "the product is too large");
-    if (p->db && (!linear_bias_fits(p->out, p->groups) ||
-                  linear_slope_tiles(p->rows, p->out, p->groups) * ceil_div(p->out, 64) >= int64_t{1} << 30))
+    if ((p->db && !linear_bias_fits(p->out, p->groups)) ||
+        (l.slope_sums && linear_slope_tiles(p->rows, p->out, p->groups) * ceil_div(p->out, 64) >= int64_t{1} << 30))
       return fail(MUON_ERR_UNSUPPORTED, "the bias is too large");
     LinArgs bias{};
     bias.offsets = p->offsets;
